@@ -1,0 +1,409 @@
+"""Measured cases of the 4-bit expert operators and the block norms.
+
+Four operators, each with its plain form (elementary torch operations, in 32
+bits, rounded once at the end) and the call of this package that does the same:
+
+  quantize  rows of numbers -> MXFP4 (32 elements of e2m1 share a power of two)
+            and back to the numbers they stand for;
+  ffn       the expert FFN's two passes with MXFP4 weights and bf16
+            activations, over rows grouped by expert: gate/up with SwiGLU (h),
+            and down (y_rows);
+  product   products grouped by expert with both operands in MXFP4, plain or
+            with the SwiGLU of two weight matrices;
+  norm      the RMS norm before a block, and after it: the combine of the
+            experts' rows, the norm, the gate, the residual sum with its scales
+            and the next block's norm.
+
+MXFP4 here: rows of cols elements, two 4-bit codes a byte (the even element in
+the low half), one scale byte b for every 32 elements, worth 2^(b - 127); a
+block's scale is 2^(floor(log2(largest magnitude)) - 2), an element is the
+nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (ties to the even code), larger ones are 6.
+"""
+from __future__ import annotations
+
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+EPS = 1e-6
+
+
+# ------------------------------------------------------------------ cases
+
+def listed():
+    return [
+        # the activations of one decode step of two tokens, quantized on their own
+        {"name": "quantize-2x4096", "op": "quantize", "rows": 2, "cols": 4096, "src": "bf16", "tiled": False},
+        # loading a layer: the gate matrices of 16 experts, into the kernels' layout
+        {"name": "quantize-weights", "op": "quantize", "rows": 16 * 14336, "cols": 4096, "src": "bf16",
+         "tiled": True},
+        # one token through the layer: two experts' gate and up weights are read
+        {"name": "gate-up-1-token", "op": "ffn", "pass": "gate_up", "T": 1, "d": 4096, "f": 14336, "E": 16, "K": 2,
+         "skew": 0.0},
+        # a decode batch of the large layer: every expert's down weights are read
+        {"name": "down-decode-64", "op": "ffn", "pass": "down", "T": 64, "d": 8192, "f": 24576, "E": 16, "K": 2,
+         "skew": 0.0},
+        # prompt processing
+        {"name": "gate-up-prefill", "op": "ffn", "pass": "gate_up", "T": 8192, "d": 4096, "f": 14336, "E": 16,
+         "K": 2, "skew": 0.0},
+        # an odd number of prompt tokens, unevenly spread over the experts
+        {"name": "down-ragged", "op": "ffn", "pass": "down", "T": 2999, "d": 8192, "f": 24576, "E": 16, "K": 2,
+         "skew": 1.0},
+        # a small batch with both operands in 4 bits, tokens gathered by slot
+        {"name": "product-17", "op": "product", "T": 17, "d": 4096, "f": 14336, "E": 16, "K": 2, "skew": 0.0,
+         "gather": True, "swiglu": False, "out": "f32"},
+        # prompt processing with both operands in 4 bits: gate/up with SwiGLU
+        {"name": "product-swiglu-prefill", "op": "product", "T": 8192, "d": 4096, "f": 14336, "E": 16, "K": 2,
+         "skew": 0.0, "gather": True, "swiglu": True, "out": "bf16"},
+        # the largest: the down product of a long prompt chunk, two experts crowded
+        {"name": "product-down-skewed", "op": "product", "T": 16384, "d": 24576, "f": 8192, "E": 16, "K": 2,
+         "skew": 1.0, "gather": False, "swiglu": False, "out": "bf16"},
+        # the norm before the block for one token
+        {"name": "norm-pre-1-token", "op": "norm", "pass": "pre", "T": 1, "d": 8192, "K": 2, "act": "bf16",
+         "gate": 0},
+        # a decode batch after the block: combine, norm, gate, residual, next norm
+        {"name": "norm-post-decode", "op": "norm", "pass": "post", "T": 63, "d": 4096, "K": 2, "act": "bf16",
+         "gate": 1},
+        # the same for a long prompt chunk
+        {"name": "norm-post-prefill", "op": "norm", "pass": "post", "T": 16384, "d": 8192, "K": 2, "act": "bf16",
+         "gate": 4096},
+    ]
+
+
+def _log_int(rng, lo, hi, step=1):
+    v = math.exp(rng.uniform(math.log(lo), math.log(hi)))
+    return max(lo, min(hi, int(round(v / step)) * step))
+
+
+def draw(rng):
+    op = rng.choice(["quantize", "ffn", "product", "norm"])
+    if op == "quantize":
+        tiled = rng.random() < 0.5
+        cols = _log_int(rng, 128, 24576, 128 if tiled else 32)
+        rows = _log_int(rng, 16, 229376, 16) if tiled else _log_int(rng, 1, 229376)
+        while rows * cols > 16 * 14336 * 4096:
+            rows = max(16, rows // 2 // 16 * 16) if tiled else max(1, rows // 2)
+        return {"op": op, "rows": rows, "cols": cols, "src": rng.choice(["bf16", "f32"]), "tiled": tiled}
+    if op == "norm":
+        T = _log_int(rng, 1, 16384)
+        return {"op": op, "pass": rng.choice(["pre", "post", "post"]), "T": T, "d": _log_int(rng, 256, 8192, 64),
+                "K": rng.choice([1, 2, 2]), "act": rng.choice(["bf16", "f32"]), "gate": rng.choice([0, 1, max(1, T // 3), T])}
+    E = _log_int(rng, 1, 64)
+    K = min(E, rng.choice([1, 2, 2, 4, 8]))
+    case = {"op": op, "T": _log_int(rng, 1, 16384), "d": _log_int(rng, 256, 8192, 128),
+            "f": _log_int(rng, 256, 24576, 128), "E": E, "K": K, "skew": rng.choice([0.0, 0.5, 1.0])}
+    if op == "ffn":
+        case["pass"] = rng.choice(["gate_up", "down"])
+        top_flops, top_weights = 4e12, 16 * 3 * 8192 * 24576
+    else:
+        case.update(gather=rng.random() < 0.5, swiglu=rng.random() < 0.5, out=rng.choice(["bf16", "f32"]))
+        top_flops, top_weights = 1.3e13, 16 * 2 * 8192 * 24576
+    while E * 3 * case["d"] * case["f"] > top_weights:
+        case["f"] = max(256, case["f"] // 2 // 128 * 128)
+    while work(case)["flops"] > top_flops:
+        case["T"] = max(1, case["T"] // 2)
+    return case
+
+
+# ------------------------------------------------------------------ inputs
+
+def _mx_quantize(v):
+    """fp32 [..., cols] -> (codes uint8 [..., cols/2], scales uint8 [..., cols/32])."""
+    b = v.reshape(*v.shape[:-1], v.shape[-1] // 32, 32)
+    amax = b.abs().amax(-1)
+    exp = ((amax.view(torch.int32) >> 23) - 127 - 2).clamp(-127, 125)
+    exp = torch.where(amax > 0, exp, torch.full_like(exp, -127))
+    # two exact factors: 2^-exp itself may lie outside the normal range
+    r = b.abs() * _pow2(-(exp // 2)).unsqueeze(-1) * _pow2(-(exp - exp // 2)).unsqueeze(-1)
+    code = (r > 0.25).to(torch.uint8)
+    for mid, up in ((0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True), (5.0, False)):
+        code += (r >= mid) if up else (r > mid)
+    code |= ((b < 0) & (code > 0)).to(torch.uint8) << 3
+    code = code.reshape(*v.shape[:-1], v.shape[-1] // 2, 2)
+    return code[..., 0] | (code[..., 1] << 4), (exp + 127).to(torch.uint8)
+
+
+def _pow2(e):
+    """2^e in fp32 for integers -126 <= e <= 127."""
+    return ((e + 127) << 23).view(torch.float32)
+
+
+def _mx_values(q, s):
+    """The fp32 numbers that codes q [..., cols/2] with scales s [..., cols/32] stand for."""
+    half = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], device=q.device)
+    i = torch.arange(256, device=q.device)
+    table = torch.stack([half[i & 15], half[i >> 4]], -1)
+    v = table[q.int()].reshape(*s.shape, 32)
+    e = s.int() - 127
+    v = v * _pow2(e // 2).unsqueeze(-1) * _pow2(e - e // 2).unsqueeze(-1)
+    return v.reshape(*q.shape[:-1], q.shape[-1] * 2)
+
+
+def _draw_mx(gen, rows, cols, sigma):
+    """Normal numbers in MXFP4, drawn in slabs of rows."""
+    q = torch.empty(rows, cols // 2, dtype=torch.uint8, device=DEV)
+    s = torch.empty(rows, cols // 32, dtype=torch.uint8, device=DEV)
+    slab = max(1, (1 << 27) // cols)
+    for r in range(0, rows, slab):
+        n = min(slab, rows - r)
+        q[r:r + n], s[r:r + n] = _mx_quantize(torch.randn(n, cols, generator=gen, device=DEV) * sigma)
+    return q, s
+
+
+def _draw_routing(gen, T, E, K, skew):
+    """Slots grouped by expert; skew crowds the first experts and leaves late ones empty."""
+    logits = torch.randn(T, E, generator=gen, device=DEV)
+    logits -= skew * 0.5 * torch.arange(E, device=DEV)
+    ids = logits.topk(K, dim=1).indices.reshape(-1)
+    slots = torch.argsort(ids, stable=True).to(torch.int32)
+    counts = torch.bincount(ids, minlength=E)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    offsets[1:] = counts.cumsum(0)
+    return slots, offsets, counts.tolist()
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    st = {"case": dict(case)}
+    op = case["op"]
+
+    def randn(*shape, dtype=torch.float32, scale=1.0):
+        return (torch.randn(*shape, generator=gen, device=DEV) * scale).to(dtype)
+
+    if op == "quantize":
+        dt = DTYPES[case["src"]]
+        w = torch.empty(case["rows"], case["cols"], dtype=dt, device=DEV)
+        slab = max(1, (1 << 27) // case["cols"])
+        for r in range(0, case["rows"], slab):
+            n = min(slab, case["rows"] - r)
+            w[r:r + n] = randn(n, case["cols"], scale=0.02)
+        st["w"] = w
+        return st
+
+    T, d, K = case["T"], case["d"], case["K"]
+    if op == "norm":
+        dt = DTYPES[case["act"]]
+        st["residual"] = randn(T, d, dtype=dt)
+        st["weight"] = (1.0 + randn(d, scale=0.1)).to(dt)
+        if case["pass"] == "post":
+            st["rows"] = randn(T * K, d, scale=0.5)
+            st["slot_to_row"] = torch.randperm(T * K, generator=gen, device=DEV).to(torch.int32)
+            w = torch.rand(T, K, generator=gen, device=DEV) + 0.1
+            st["topk_w"] = w / w.sum(1, keepdim=True)
+            st["next_weight"] = (1.0 + randn(d, scale=0.1)).to(dt)
+            if case["gate"]:
+                groups = (T + case["gate"] - 1) // case["gate"]
+                st["gate"] = torch.sigmoid(randn(groups, d)).to(dt)
+            st["residual_scale"], st["block_scale"] = 0.9, 0.5
+        return st
+
+    f, E = case["f"], case["E"]
+    st["slots"], st["offsets"], st["counts"] = _draw_routing(gen, T, E, K, case["skew"])
+    if op == "ffn":
+        for name, rows, cols in (("gate", f, d), ("up", f, d), ("down", d, f)):
+            q, s = _draw_mx(gen, E * rows, cols, 0.02)
+            st["q_" + name], st["s_" + name] = q.view(E, rows, cols // 2), s.view(E, rows, cols // 32)
+        if case["pass"] == "gate_up":
+            st["x"] = randn(T, d, dtype=torch.bfloat16)
+        else:
+            g = randn(T * K, f)
+            st["h"] = (g * torch.sigmoid(g) * randn(T * K, f)).to(torch.bfloat16)
+        if own:
+            import int8_weight_moe_amd as m
+            st["experts"] = m.pack_mxfp4_experts(*(st.pop(k) for k in (
+                "q_gate", "q_up", "q_down", "s_gate", "s_up", "s_down")))
+        return st
+    st["a_q"], st["a_s"] = _draw_mx(gen, T if case["gather"] else T * K, d, 1.0)
+    for name in ("w0", "w1") if case["swiglu"] else ("w0",):
+        q, s = _draw_mx(gen, E * f, d, 0.02)
+        q, s = q.view(E, f, d // 2), s.view(E, f, d // 32)
+        if own:
+            import int8_weight_moe_amd as m
+            q, s = m.moe_pack_mxfp4(q, s)
+        st[name + "_q"], st[name + "_s"] = q, s
+    return st
+
+
+# ------------------------------------------------------------------ one pass
+
+def run(st):
+    return _run_own(st) if own else _run_plain(st)
+
+
+def _run_own(st):
+    import int8_weight_moe_amd as m
+    c = st["case"]
+    if c["op"] == "quantize":
+        q, s = m.moe_quantize_mxfp4(st["w"], tiled=c["tiled"])
+        return m.moe_dequantize_mxfp4(q, s, st["w"].dtype, tiled=c["tiled"])
+    if c["op"] == "ffn":
+        if c["pass"] == "gate_up":
+            return m.moe_expert_gate_up(st["x"], st["offsets"], st["slots"], st["experts"], c["K"])
+        return m.moe_expert_down(st["h"], st["offsets"], st["experts"], c["T"], c["K"])
+    if c["op"] == "product":
+        return m.moe_grouped_mm_mxfp4(st["a_q"], st["a_s"], st["offsets"], st["w0_q"], st["w0_s"],
+                                      DTYPES[c["out"]], sorted_slots=st["slots"] if c["gather"] else None,
+                                      K=c["K"], w2_q=st.get("w1_q"), w2_s=st.get("w1_s"))
+    if c["pass"] == "pre":
+        return m.moe_norm_pre(st["residual"], st["weight"], EPS)
+    return m.moe_combine_post(st["rows"], st["slot_to_row"], st["topk_w"], st["residual"], weight=st["weight"],
+                              gate=st.get("gate"), gate_tokens=max(1, c["gate"]),
+                              residual_scale=st["residual_scale"], block_scale=st["block_scale"], eps=EPS,
+                              next_weight=st["next_weight"])
+
+
+def _rms(v, weight):
+    return v * torch.rsqrt((v * v).mean(-1, keepdim=True) + EPS) * weight.float()
+
+
+def _run_plain(st):
+    c = st["case"]
+    if c["op"] == "quantize":
+        return _mx_values(*_mx_quantize(st["w"].float())).to(st["w"].dtype)
+    if c["op"] == "norm":
+        res = st["residual"].float()
+        if c["pass"] == "pre":
+            return _rms(res, st["weight"]).to(st["residual"].dtype)
+        T, K = st["topk_w"].shape
+        rows = st["slot_to_row"].view(T, K)
+        y = st["topk_w"][:, 0:1] * st["rows"][rows[:, 0]]
+        for k in range(1, K):
+            y = y + st["topk_w"][:, k:k + 1] * st["rows"][rows[:, k]]
+        n = _rms(y, st["weight"])
+        if c["gate"]:
+            n = n * st["gate"].float()[torch.arange(T, device=n.device) // c["gate"]]
+        out = st["residual_scale"] * res + st["block_scale"] * n
+        return out.to(st["residual"].dtype), _rms(out, st["next_weight"]).to(st["residual"].dtype)
+
+    E = c["E"]
+    if c["op"] == "ffn":
+        gate_up = c["pass"] == "gate_up"
+        a = (st["x"] if gate_up else st["h"]).float()
+        mats = [(st["q_gate"], st["s_gate"]), (st["q_up"], st["s_up"])] if gate_up else [(st["q_down"], st["s_down"])]
+        gather, dt = gate_up, torch.bfloat16 if gate_up else torch.float32
+    else:
+        a = _mx_values(st["a_q"], st["a_s"])
+        mats = [(st["w0_q"], st["w0_s"])] + ([(st["w1_q"], st["w1_s"])] if c["swiglu"] else [])
+        gather, dt = c["gather"], DTYPES[c["out"]]
+    out = torch.empty(c["T"] * c["K"], mats[0][0].shape[1], dtype=dt, device=a.device)
+    r0 = 0
+    for e in range(E):
+        r1 = r0 + st["counts"][e]
+        if r1 == r0:
+            continue
+        rows = a[st["slots"][r0:r1] // c["K"]] if gather else a[r0:r1]
+        p = [rows @ _mx_values(q[e], s[e]).t() for q, s in mats]
+        out[r0:r1] = (p[0] * torch.sigmoid(p[0]) * p[1] if len(p) == 2 else p[0]).to(dt)
+        r0 = r1
+    return out
+
+
+# ------------------------------------------------------------------ what a pass cannot do without
+
+def work(case):
+    op = case["op"]
+    if op == "quantize":
+        n = case["rows"] * case["cols"]
+        b = 2 if case["src"] == "bf16" else 4
+        # the numbers in, codes and scales out; those in, the numbers out
+        return {"bytes": 2 * n * b + 2 * (n // 2 + n // 32), "flops": 4 * n}
+    T, d, K = case["T"], case["d"], case["K"]
+    if op == "norm":
+        b = 2 if case["act"] == "bf16" else 4
+        if case["pass"] == "pre":
+            return {"bytes": 2 * T * d * b + d * b, "flops": 4 * T * d}
+        gate = -(-T // case["gate"]) * d * b if case["gate"] else 0
+        return {"bytes": T * K * (d * 4 + 8) + 3 * T * d * b + 2 * d * b + gate, "flops": (2 * K + 11) * T * d}
+    f, E = case["f"], case["E"]
+    S = T * K
+    hit = min(E, S)   # experts with rows, at most
+    two = case["pass"] == "gate_up" if op == "ffn" else case["swiglu"]
+    mats = 2 if two else 1
+    weights = hit * mats * (d * f // 2 + d * f // 32)
+    if op == "ffn":
+        acts = (T * d * 2 + S * f * 2) if case["pass"] == "gate_up" else (S * f * 2 + S * d * 4)
+    else:
+        acts = (T if case["gather"] else S) * (d // 2 + d // 32) + S * f * (2 if case["out"] == "bf16" else 4)
+    return {"bytes": weights + acts, "flops": 2 * mats * S * d * f}
+
+
+# ------------------------------------------------------------------ the definition in 64 bits
+
+def _exact_values(q, s):
+    lo, hi = (q & 15).long(), (q >> 4).long()
+    c = torch.stack([lo, hi], -1).reshape(*q.shape[:-1], -1)
+    ex, m = (c >> 1) & 3, (c & 1).double()
+    mag = torch.where(ex == 0, 0.5 * m, (1.0 + 0.5 * m) * (1 << (ex - 1).clamp(min=0)).double())
+    mag = torch.where(c >= 8, -mag, mag)
+    scale = ((s.long() - 127 + 1023) << 52).view(torch.float64)
+    return mag * scale.repeat_interleave(32, dim=-1)
+
+
+def _exact_round_trip(w):
+    w = w.double()
+    b = w.reshape(w.shape[0], -1, 32)
+    amax = b.abs().amax(-1, keepdim=True)
+    _, e = torch.frexp(amax)                       # amax = m * 2^e, 0.5 <= m < 1
+    e = (e.long() - 1 - 2).clamp(min=-127)
+    step = ((e + 1023) << 52).view(torch.float64)
+    r = (b / step).abs().clamp(max=6.0)
+    # the quantum is 0.5 below 2, 1 below 4 and 2 above; round() takes ties to even multiples
+    quantum = torch.where(r < 2, 0.5, torch.where(r < 4, 1.0, 2.0)).double()
+    v = torch.round(r / quantum) * quantum
+    v = torch.where(amax > 0, torch.copysign(v, b) * step, torch.zeros_like(v))
+    return v.reshape(w.shape)
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False
+    try:
+        st = prepare(case, seed)
+    finally:
+        own = was
+    op = case["op"]
+    if op == "quantize":
+        w = st["w"]
+        slab = max(1, (1 << 25) // case["cols"])
+        out = torch.empty_like(w, dtype=torch.float32)     # the values are exact in 32 bits
+        for r in range(0, case["rows"], slab):
+            out[r:r + slab] = _exact_round_trip(w[r:r + slab])
+        return out
+    if op == "norm":
+        res, g1 = st["residual"].double(), st["weight"].double()
+        if case["pass"] == "pre":
+            return res / torch.sqrt(res.pow(2).mean(1, keepdim=True) + EPS) * g1
+        T, K = st["topk_w"].shape
+        y = (st["topk_w"].double().unsqueeze(-1) * st["rows"].double()[st["slot_to_row"].long()].view(T, K, -1)).sum(1)
+        n = y / torch.sqrt(y.pow(2).mean(1, keepdim=True) + EPS) * g1
+        if case["gate"]:
+            n = n * st["gate"].double().repeat_interleave(case["gate"], dim=0)[:T]
+        out = st["residual_scale"] * res + st["block_scale"] * n
+        return out, out / torch.sqrt(out.pow(2).mean(1, keepdim=True) + EPS) * st["next_weight"].double()
+    if op == "ffn":
+        names = ("gate", "up") if case["pass"] == "gate_up" else ("down",)
+        mats = [(st["q_" + n], st["s_" + n]) for n in names]
+        a = (st["x"] if case["pass"] == "gate_up" else st["h"]).double()
+        gather = case["pass"] == "gate_up"
+    else:
+        mats = [(st[n + "_q"], st[n + "_s"]) for n in (("w0", "w1") if case["swiglu"] else ("w0",))]
+        a = _exact_values(st["a_q"], st["a_s"])
+        gather = case["gather"]
+    N = mats[0][0].shape[1]
+    out = torch.empty(case["T"] * case["K"], N, dtype=torch.float64, device=a.device)
+    slab = max(16, (1 << 26) // a.shape[1])
+    ends = torch.tensor(st["counts"]).cumsum(0).tolist()
+    for e, r1 in enumerate(ends):
+        r0 = r1 - st["counts"][e]
+        if r0 == r1:
+            continue
+        rows = a[torch.div(st["slots"][r0:r1].long(), case["K"], rounding_mode="floor")] if gather else a[r0:r1]
+        for c0 in range(0, N, slab):
+            p = [torch.mm(rows, _exact_values(q[e, c0:c0 + slab], s[e, c0:c0 + slab]).t()) for q, s in mats]
+            out[r0:r1, c0:c0 + slab] = p[0] / (1 + torch.exp(-p[0])) * p[1] if len(p) == 2 else p[0]
+    return out
