@@ -248,7 +248,7 @@ def _run_own(st):
     if c["op"] == "product":
         return m.moe_grouped_mm_mxfp4(st["a_q"], st["a_s"], st["offsets"], st["w0_q"], st["w0_s"],
                                       DTYPES[c["out"]], sorted_slots=st["slots"] if c["gather"] else None,
-                                      K=c["K"], w2_q=st.get("w1_q"), w2_s=st.get("w1_s"))
+                                      K=c["K"] if c["gather"] else 1, w2_q=st.get("w1_q"), w2_s=st.get("w1_s"))
     if c["pass"] == "pre":
         return m.moe_norm_pre(st["residual"], st["weight"], EPS)
     return m.moe_combine_post(st["rows"], st["slot_to_row"], st["topk_w"], st["residual"], weight=st["weight"],
