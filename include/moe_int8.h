@@ -104,8 +104,17 @@ enum { MOE_F32 = 0, MOE_BF16 = 1 };
  * bf16 matrix [rows, cols] is packed as int8 [rows, 2*cols]). The bf16 and
  * fp8 encodings need bf16 activations; on the TILED schedule their tensors
  * must also fit 32-bit byte offsets (x and h below 4 GiB, one expert's matrix
- * below 4 GiB), else MOE_ERR_UNSUPPORTED. */
-enum { MOE_W_INT8 = 0, MOE_W_BF16 = 1, MOE_W_FP8 = 2 };
+ * below 4 GiB), else MOE_ERR_UNSUPPORTED.
+ *   MOE_W_MXFP4 4-bit codes with one power-of-two scale byte per 32 elements
+ *               along the row (moe_quantize_mxfp4), a quarter of bf16's bytes.
+ *               The w_* pointers hold the tiled codes, the s_* pointers the
+ *               tiled scale bytes ([E, out, in/32]; scale_dtype is not used).
+ *               Codes become bf16 exactly, scale included, so the products are
+ *               exact and the sums fp32 as for the others. bf16 activations
+ *               (else MOE_ERR_UNSUPPORTED), d and f multiples of 128 (else
+ *               MOE_ERR_SHAPE); TILED as for bf16 and fp8.
+ * Code 3 is not assigned. */
+enum { MOE_W_INT8 = 0, MOE_W_BF16 = 1, MOE_W_FP8 = 2, MOE_W_MXFP4 = 4 };
 
 /* expert-FFN schedule: AUTO picks STREAM when at most 64 rows fall on each
  * expert on average (T*K <= 64*E: decode) and TILED otherwise (prefill).
@@ -335,6 +344,124 @@ moe_status moe_quantize_pack_rows(int64_t rows, int32_t cols, int32_t src_dtype,
  *   q [rows, cols] int8 row-major in, packed [rows*cols] int8 out (not in place).
  * A byte permutation: bit-exact. */
 moe_status moe_pack_rows(int64_t rows, int32_t cols, const int8_t* q, int8_t* packed, hipStream_t stream);
+
+/* ---------------------------------------------------------------- MXFP4
+ * Microscaled 4-bit floating point (OCP MX): along a row of a matrix, each
+ * block of 32 elements has one scale byte b worth 2^(b - 127) (255: not a
+ * number), and an element is a 4-bit e2m1 code: sign, then the magnitudes
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6. Two codes a byte, the even element in the low
+ * half.
+ *
+ * Layouts of codes and scales:
+ *   MOE_MX_ROWS   row-major: codes [rows, cols/2], scales [rows, cols/32];
+ *                 cols a multiple of 32, 32..1048576.
+ *   MOE_MX_TILED  what the kernels read weights in (rows % 16 == 0, cols % 128
+ *                 == 0). Codes: the layout of moe_pack_rows over the cols/2
+ *                 bytes of a row. Scales: with n = cols/128, the scale of row
+ *                 r, columns 32*c .. +32 is byte
+ *                   (r/16)*n*64 + 256*(k/4) + m*(16*(c%4) + r%16) + k%4,
+ *                   k = c/4, m = min(4, n - 4*(k/4)).
+ *                 An expert tensor [E, out, in] is rows = E*out, cols = in. */
+enum { MOE_MX_ROWS = 0, MOE_MX_TILED = 1 };
+
+/* Quantizer. Per block: b = floor(log2(max |w|)) - 2 + 127, at least 0 (an
+ * all-zero block: 0); code = the e2m1 value nearest to w / 2^(b - 127), ties to
+ * the even code, saturated to +-6, with the sign of w (so of -0 too). A block
+ * holding an infinity or a NaN gets b = 255 and zero codes. Bit-exact.
+ *   w [rows, cols] src_dtype in, q [rows*cols/2] and s [rows*cols/32] bytes out
+ *   in `layout`; rows in [0, 2^31). */
+moe_status moe_quantize_mxfp4(int64_t rows, int32_t cols, int32_t src_dtype, const void* w, int32_t layout,
+                              uint8_t* q, uint8_t* s, hipStream_t stream);
+
+/* The numbers that codes and scales stand for, in dst_dtype (exact; past the
+ * type's largest number: infinite; a scale of 255: NaN). */
+moe_status moe_dequantize_mxfp4(int64_t rows, int32_t cols, int32_t layout, const uint8_t* q, const uint8_t* s,
+                                int32_t dst_dtype, void* w, hipStream_t stream);
+
+/* Row-major codes and scales (a checkpoint's) -> MOE_MX_TILED; not in place. */
+moe_status moe_pack_mxfp4(int64_t rows, int32_t cols, const uint8_t* q, const uint8_t* s, uint8_t* q_tiled,
+                          uint8_t* s_tiled, hipStream_t stream);
+
+/* Product grouped by expert, both operands in MXFP4 (the layer's own
+ * contraction with 4-bit activations: the scaled MFMA takes both as they are).
+ *   row r of expert e's segment [off[e], off[e+1]):
+ *     out[r, n] = sum_k A[row(r), k] * W_e[n, k],                   n < f, k < d
+ *     or, with a second matrix, silu(W_e . a) * (W2_e . a).
+ *   shape: T tokens, K slots a token (rows of out: T*K), d the reduction, f the
+ *     output channels, E experts; weight_fmt MOE_W_MXFP4 (else MOE_ERR_DTYPE);
+ *     act_dtype is out's type; scale_dtype is not used; ffn_path as for the
+ *     expert FFN; d and f multiples of 128.
+ *   a_q, a_s  codes and scales of A, row-major, d columns. With sorted_slots
+ *     [T*K]: [T, .], row(r) = sorted_slots[r] / K; NULL: [T*K, .], row(r) = r.
+ *   w_q, w_s, w2_q, w2_s  [E, f, d] tiled codes and scales (w2_*: both NULL for
+ *     the plain product).
+ *   out [T*K, f] act_dtype; rows past off[E] are left untouched.
+ * Products are exact, sums fp32, one rounding. Any segment lengths. */
+moe_status moe_grouped_mm_mxfp4(const moe_shape* shape, const uint8_t* a_q, const uint8_t* a_s,
+                                const int32_t* expert_offsets, const int32_t* sorted_slots, const uint8_t* w_q,
+                                const uint8_t* w_s, const uint8_t* w2_q, const uint8_t* w2_s, void* out,
+                                hipStream_t stream);
+
+/* The expert FFN with MXFP4 weights AND activations, on the permuted rows:
+ * x is quantized per token, gate/up with SwiGLU gives h (bf16), h is quantized
+ * per row, down gives y_rows. As moe_expert_ffn with 4-bit products (four times
+ * the bf16 rate) and the rounding of 4-bit activations.
+ *   weight_fmt MOE_W_MXFP4; act_dtype is x's type; d, f multiples of 128;
+ *   workspace >= moe_expert_ffn_mxfp4_workspace_size bytes. */
+moe_status moe_expert_ffn_mxfp4_workspace_size(const moe_shape* shape, size_t* bytes);
+moe_status moe_expert_ffn_mxfp4(const moe_shape* shape, const void* x, const int32_t* expert_offsets,
+                                const int32_t* sorted_slots, const uint8_t* w_gate, const uint8_t* w_up,
+                                const uint8_t* w_down, const uint8_t* s_gate, const uint8_t* s_up,
+                                const uint8_t* s_down, float* y_rows, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream);
+
+/* ---------------------------------------------------------------- norms around the layer
+ * rms(v) = v / sqrt(mean(v^2) + eps) over the d elements of a token, in fp32.
+ *
+ * Before the layer: n = rms(x) * weight.
+ *   x, n [T, d], weight [d], all act_dtype; n may be x. eps >= 0, finite. */
+moe_status moe_norm_pre(const moe_shape* shape, const void* x, const void* weight, float eps, void* n,
+                        hipStream_t stream);
+
+/* After the layer, with y its output:
+ *   out  = residual_scale * residual + block_scale * gate * (rms(y) * weight)
+ *   next = rms(out) * next_weight      (the next block's moe_norm_pre)
+ * in one pass, each rounded once; next is taken from the unrounded sum. */
+typedef struct moe_post {
+  const void* weight;      /* [d] act_dtype, or NULL: y without the norm                       */
+  const void* gate;        /* [ceil(T / gate_tokens), d] act_dtype, token t takes row t /
+                              gate_tokens; NULL: 1                                             */
+  const void* next_weight; /* [d] act_dtype, or NULL: no next                                  */
+  int32_t gate_tokens;     /* tokens that share a row of the gate, >= 1 (read with gate only)  */
+  float residual_scale, block_scale;
+  float eps, next_eps;     /* >= 0, finite                                                     */
+} moe_post;
+
+/* y [T, d], residual [T, d], out [T, d], next [T, d] (NULL without next_weight),
+ * all act_dtype; out may be residual or y, next may not overlap the others. */
+moe_status moe_norm_post(const moe_shape* shape, const moe_post* post, const void* y, const void* residual, void* out,
+                         void* next, hipStream_t stream);
+
+/* The same with y taken from the experts' rows, as moe_combine does (K = 1..8,
+ * a slot with row -1 contributes nothing) but unrounded: one pass in place of
+ * the combine and the norm. */
+moe_status moe_combine_post(const moe_shape* shape, const moe_post* post, const float* y_rows,
+                            const int32_t* slot_to_row, const float* topk_w, const void* residual, void* out,
+                            void* next, hipStream_t stream);
+
+/* A block: moe_norm_pre of the residual stream, the layer (moe_forward's steps
+ * on it), moe_combine_post onto the stream; any weight encoding.
+ *   residual [T, d] act_dtype; pre_weight [d] or NULL : x is given instead
+ *   x [T, d] or NULL: the layer's input (the `next` of the block before), read
+ *   when pre_weight is NULL; exactly one of the two is given
+ *   out, next as in moe_norm_post (out may be residual)
+ *   workspace >= moe_block_workspace_size bytes. */
+moe_status moe_block_workspace_size(const moe_shape* shape, size_t* bytes);
+moe_status moe_block_forward(const moe_shape* shape, const void* residual, const void* pre_weight, float pre_eps,
+                             const void* x, const moe_post* post, const void* router_w, const float* router_bias,
+                             const void* w_gate, const void* w_up, const void* w_down, const void* s_gate,
+                             const void* s_up, const void* s_down, void* out, void* next, int32_t* topk_ids_out,
+                             float* topk_w_out, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -20,7 +20,8 @@ STATUS_NAMES = {
 }
 MOE_F32, MOE_BF16 = 0, 1
 MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_TILED = 0, 1, 2
-MOE_W_INT8, MOE_W_BF16, MOE_W_FP8 = 0, 1, 2
+MOE_W_INT8, MOE_W_BF16, MOE_W_FP8, MOE_W_MXFP4 = 0, 1, 2, 4
+MOE_MX_ROWS, MOE_MX_TILED = 0, 1
 
 # every symbol the header declares
 EXPORTS = (
@@ -28,6 +29,9 @@ EXPORTS = (
     "moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_gate_up", "moe_expert_down", "moe_combine", "moe_forward", "moe_quantize_rows",
     "moe_pack_rows", "moe_mlp_workspace_size", "moe_mlp_forward", "moe_quantize_rows_fp8", "moe_down_workspace_size",
     "moe_forward_noalloc", "moe_gate_up_workspace_size", "moe_quantize_pack_rows",
+    "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_pack_mxfp4", "moe_grouped_mm_mxfp4",
+    "moe_expert_ffn_mxfp4_workspace_size", "moe_expert_ffn_mxfp4", "moe_norm_pre", "moe_norm_post",
+    "moe_combine_post", "moe_block_workspace_size", "moe_block_forward",
 )
 
 
@@ -35,6 +39,12 @@ class MoeShape(ctypes.Structure):
     _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("f", ctypes.c_int32), ("E", ctypes.c_int32),
                 ("K", ctypes.c_int32), ("act_dtype", ctypes.c_int32), ("scale_dtype", ctypes.c_int32),
                 ("ffn_path", ctypes.c_int32), ("weight_fmt", ctypes.c_int32)]
+
+
+class MoePost(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("next_weight", ctypes.c_void_p),
+                ("gate_tokens", ctypes.c_int32), ("residual_scale", ctypes.c_float), ("block_scale", ctypes.c_float),
+                ("eps", ctypes.c_float), ("next_eps", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -45,6 +55,8 @@ class MoeError(RuntimeError):
 
 _P = ctypes.c_void_p
 _SHAPE = ctypes.POINTER(MoeShape)
+_POST = ctypes.POINTER(MoePost)
+_I32, _I64, _F32, _SIZE = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _SIGS = {
     "moe_abi_version": (ctypes.c_int32, []),
     "moe_status_str": (ctypes.c_char_p, [ctypes.c_int32]),
@@ -68,6 +80,17 @@ _SIGS = {
     "moe_mlp_workspace_size": (ctypes.c_int32, [_SHAPE, ctypes.POINTER(ctypes.c_size_t)]),
     "moe_mlp_forward": (ctypes.c_int32, [_SHAPE, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_forward_noalloc": (ctypes.c_int32, [_SHAPE, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_quantize_mxfp4": (_I32, [_I64, _I32, _I32, _P, _I32, _P, _P, _P]),
+    "moe_dequantize_mxfp4": (_I32, [_I64, _I32, _I32, _P, _P, _I32, _P, _P]),
+    "moe_pack_mxfp4": (_I32, [_I64, _I32, _P, _P, _P, _P, _P]),
+    "moe_grouped_mm_mxfp4": (_I32, [_SHAPE] + [_P] * 10),
+    "moe_expert_ffn_mxfp4_workspace_size": (_I32, [_SHAPE, ctypes.POINTER(_SIZE)]),
+    "moe_expert_ffn_mxfp4": (_I32, [_SHAPE] + [_P] * 11 + [_SIZE, _P]),
+    "moe_norm_pre": (_I32, [_SHAPE, _P, _P, _F32, _P, _P]),
+    "moe_norm_post": (_I32, [_SHAPE, _POST, _P, _P, _P, _P, _P]),
+    "moe_combine_post": (_I32, [_SHAPE, _POST, _P, _P, _P, _P, _P, _P, _P]),
+    "moe_block_workspace_size": (_I32, [_SHAPE, ctypes.POINTER(_SIZE)]),
+    "moe_block_forward": (_I32, [_SHAPE, _P, _P, _F32, _P, _POST] + [_P] * 13 + [_SIZE, _P]),
 }
 
 _lib = None

@@ -108,7 +108,7 @@ moe_status check_shape(const moe_shape* s) {
   if (s->act_dtype != MOE_F32 && s->act_dtype != MOE_BF16) return fail(MOE_ERR_DTYPE, "act_dtype=%d", s->act_dtype);
   if (s->scale_dtype != MOE_F32 && s->scale_dtype != MOE_BF16) return fail(MOE_ERR_DTYPE, "scale_dtype=%d", s->scale_dtype);
   if (s->ffn_path < MOE_PATH_AUTO || s->ffn_path > MOE_PATH_TILED) return fail(MOE_ERR_SHAPE, "ffn_path=%d", s->ffn_path);
-  if (s->weight_fmt < MOE_W_INT8 || s->weight_fmt > MOE_W_FP8) return fail(MOE_ERR_DTYPE, "weight_fmt=%d", s->weight_fmt);
+  if ((s->weight_fmt < MOE_W_INT8 || s->weight_fmt > MOE_W_FP8) && s->weight_fmt != MOE_W_MXFP4) return fail(MOE_ERR_DTYPE, "weight_fmt=%d", s->weight_fmt);
   return MOE_OK;
 }
 
@@ -156,6 +156,7 @@ WsLayout forward_layout(const moe_shape* s) {
 // split), or the tiled schedule's tile claim words.
 size_t down_ws_bytes(const moe_shape* s) {
   if (!use_stream(s)) return moe::kTileClaimBytes;
+  if (s->weight_fmt == MOE_W_MXFP4) return 0;   // its stream pass splits inside the workgroup only
   const long S = (long)s->T * s->K;
   const int planes = moe::stream_down_planes(S, s->d, s->f, s->E);
   return (size_t)planes * (size_t)S * (size_t)s->d * 4;
@@ -183,6 +184,8 @@ moe_status check_ffn(const moe_shape* s) {
   if (s->weight_fmt == MOE_W_INT8) return MOE_OK;
   if (s->act_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "weight_fmt=%d needs bf16 activations", s->weight_fmt);
+  if (s->weight_fmt == MOE_W_MXFP4 && (s->d % 128 || s->f % 128))
+    return fail(MOE_ERR_SHAPE, "MXFP4 weights need d=%d and f=%d to be multiples of 128", s->d, s->f);
   const int wbytes = s->weight_fmt == MOE_W_BF16 ? 2 : 1;
   if (!use_stream(s) && !moe::dma_offsets_fit(s->T, (long)s->T * s->K, s->d, s->f, wbytes))
     return fail(MOE_ERR_UNSUPPORTED, "weight_fmt=%d: tensors too large for the tiled schedule", s->weight_fmt);
@@ -249,14 +252,61 @@ void log_pass(const char* call, bool gate_up, const moe_shape* s, const moe::Ffn
                S > 32L * s->E ? 64 : 32);
     }
   }
-  static const char* const kFmt[] = {"int8", "bf16", "fp8"};
+  static const char* const kFmt[] = {"int8", "bf16", "fp8", "", "mxfp4"};
   fprintf(stderr, "[moe] %s %s: T=%d d=%d f=%d E=%d K=%d act=%s scale=%s weights=%s; %s\n", call,
           gate_up ? "gate/up" : "down", s->T, s->d, s->f, s->E, s->K, s->act_dtype == MOE_BF16 ? "bf16" : "f32",
           s->scale_dtype == MOE_BF16 ? "bf16" : "f32", kFmt[s->weight_fmt], how);
 }
 
+// The passes of the expert FFN as products with MXFP4 weights.
+moe::MxArgs mx_gate_up(const moe::FfnArgs& a) {
+  moe::MxArgs m;
+  m.a = a.x;
+  m.a_s = nullptr;
+  m.offsets = a.offsets;
+  m.sorted_slots = a.sorted_slots;
+  m.topk = a.K;
+  m.w0 = reinterpret_cast<const uint8_t*>(a.w_gate);
+  m.s0 = static_cast<const uint8_t*>(a.s_gate);
+  m.w1 = reinterpret_cast<const uint8_t*>(a.w_up);
+  m.s1 = static_cast<const uint8_t*>(a.s_up);
+  m.out = a.h;
+  m.out_bf16 = true;
+  m.E = a.E;
+  m.N = a.f;
+  m.Kd = a.d;
+  m.S = a.S;
+  return m;
+}
+
+moe::MxArgs mx_down(const moe::FfnArgs& a) {
+  moe::MxArgs m;
+  m.a = a.h;
+  m.a_s = nullptr;
+  m.offsets = a.offsets;
+  m.sorted_slots = nullptr;
+  m.topk = 1;
+  m.w0 = reinterpret_cast<const uint8_t*>(a.w_down);
+  m.s0 = static_cast<const uint8_t*>(a.s_down);
+  m.w1 = m.s1 = nullptr;
+  m.out = a.y_rows;
+  m.out_bf16 = false;
+  m.E = a.E;
+  m.N = a.d;
+  m.Kd = a.f;
+  m.S = a.S;
+  return m;
+}
+
+moe_status run_mx(const char* what, const moe_shape* s, const moe::MxArgs& m, hipStream_t stream) {
+  const hipError_t e = moe::launch_mx_stream(m, stream);
+  if (e != hipSuccess) return hip_fail(e, what);
+  return MOE_OK;
+}
+
 moe_status run_gate_up(const char* call, const moe_shape* s, const moe::FfnArgs& a, hipStream_t stream) {
   if (log_on()) log_pass(call, true, s, a);
+  if (s->weight_fmt == MOE_W_MXFP4) return run_mx("gate/up launch", s, mx_gate_up(a), stream);
   const hipError_t e = use_stream(s) ? moe::launch_stream_gate_up(a, stream) : moe::launch_tiled_gate_up(a, stream);
   if (e != hipSuccess) return hip_fail(e, "gate/up launch");
   return MOE_OK;
@@ -264,9 +314,99 @@ moe_status run_gate_up(const char* call, const moe_shape* s, const moe::FfnArgs&
 
 moe_status run_down(const char* call, const moe_shape* s, const moe::FfnArgs& a, hipStream_t stream) {
   if (log_on()) log_pass(call, false, s, a);
+  if (s->weight_fmt == MOE_W_MXFP4) return run_mx("down launch", s, mx_down(a), stream);
   const hipError_t e = use_stream(s) ? moe::launch_stream_down(a, stream) : moe::launch_tiled_down(a, stream);
   if (e != hipSuccess) return hip_fail(e, "down launch");
   return MOE_OK;
+}
+
+// MXFP4 codes and scales: sizes of a layout, and the pointers.
+moe_status check_mxfp4(int64_t rows, int32_t cols, int32_t layout, const void* q, const void* s) {
+  if (layout != MOE_MX_ROWS && layout != MOE_MX_TILED) return fail(MOE_ERR_SHAPE, "layout=%d", layout);
+  if (rows < 0 || rows > 0x7fffffffL) return fail(MOE_ERR_SHAPE, "rows=%ld must be in [0, 2^31)", (long)rows);
+  if (cols < 32 || cols > (1 << 20) || cols % 32) return fail(MOE_ERR_SHAPE, "cols=%d must be a multiple of 32 in [32, 2^20]", cols);
+  if (layout == MOE_MX_TILED && (rows % 16 || cols % 128))
+    return fail(MOE_ERR_SHAPE, "the tiled layout needs rows=%ld to be a multiple of 16 and cols=%d of 128", (long)rows, cols);
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(q);
+  REQUIRE_PTR(s);
+  return MOE_OK;
+}
+
+// Shape of a product with both operands in MXFP4.
+moe_status check_mx_shape(const moe_shape* s) {
+  const moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (s->weight_fmt != MOE_W_MXFP4) return fail(MOE_ERR_DTYPE, "weight_fmt=%d: this call takes MXFP4 weights", s->weight_fmt);
+  if (s->d % 128 || s->f % 128)
+    return fail(MOE_ERR_SHAPE, "MXFP4 weights need d=%d and f=%d to be multiples of 128", s->d, s->f);
+  return MOE_OK;
+}
+
+// moe_block_forward's workspace: moe_forward's, then the normalised input.
+size_t block_x_bytes(const moe_shape* s) {
+  return round_up((size_t)s->T * s->d * (s->act_dtype == MOE_BF16 ? 2 : 4));
+}
+
+// Workspace of moe_expert_ffn_mxfp4: x in MXFP4, h, h in MXFP4.
+struct MxFfnLayout {
+  size_t xq, xs, h, hq, hs, total;
+};
+
+MxFfnLayout mx_ffn_layout(const moe_shape* s) {
+  const size_t T = (size_t)s->T, S = T * s->K, d = (size_t)s->d, f = (size_t)s->f;
+  MxFfnLayout L;
+  size_t o = 0;
+  L.xq = o; o += round_up(T * (d / 2));
+  L.xs = o; o += round_up(T * (d / 32));
+  L.h = o;  o += round_up(S * f * 2);
+  L.hq = o; o += round_up(S * (f / 2));
+  L.hs = o; o += round_up(S * (f / 32));
+  L.total = o;
+  return L;
+}
+
+bool finite_f32(float v) { return v - v == 0.f; }
+
+moe_status check_eps(const char* what, float eps) {
+  if (!finite_f32(eps) || eps < 0.f) return fail(MOE_ERR_SHAPE, "%s=%g must be finite and not negative", what, (double)eps);
+  return MOE_OK;
+}
+
+moe_status check_post(const moe_shape* s, const moe_post* p, const void* residual, const void* out, const void* next) {
+  if (!p) return fail(MOE_ERR_NULL, "post is NULL");
+  moe_status st;
+  if (p->weight && (st = check_eps("eps", p->eps)) != MOE_OK) return st;
+  if (p->next_weight && (st = check_eps("next_eps", p->next_eps)) != MOE_OK) return st;
+  if (p->gate && p->gate_tokens < 1) return fail(MOE_ERR_SHAPE, "gate_tokens=%d must be at least 1", p->gate_tokens);
+  if (s->T == 0) return MOE_OK;
+  if (!aligned16(p->weight)) return fail(MOE_ERR_ALIGN, "weight is not 16-byte aligned");
+  if (!aligned16(p->gate)) return fail(MOE_ERR_ALIGN, "gate is not 16-byte aligned");
+  if (!aligned16(p->next_weight)) return fail(MOE_ERR_ALIGN, "next_weight is not 16-byte aligned");
+  REQUIRE_PTR(residual);
+  REQUIRE_PTR(out);
+  if (p->next_weight) REQUIRE_PTR(next);
+  return MOE_OK;
+}
+
+moe::NormArgs post_args(const moe_shape* s, const moe_post* p, const void* residual, void* out, void* next) {
+  moe::NormArgs a = {};
+  a.act_bf16 = s->act_dtype == MOE_BF16;
+  a.residual = residual;
+  a.weight = p->weight;
+  a.gate = p->gate;
+  a.next_weight = p->next_weight;
+  a.out = out;
+  a.next = next;
+  a.residual_scale = p->residual_scale;
+  a.block_scale = p->block_scale;
+  a.eps = p->eps;
+  a.next_eps = p->next_eps;
+  a.T = s->T;
+  a.d = s->d;
+  a.K = s->K;
+  a.gate_tokens = p->gate ? p->gate_tokens : 1;
+  return a;
 }
 
 moe_status check_quantize(int64_t rows, int32_t cols, int32_t src_dtype, const void* w, int32_t scale_dtype,
@@ -315,10 +455,12 @@ moe_status scratch_on_current_device(void** out) {
   return MOE_OK;
 }
 
+// post: null, or the norm and residual sum that take the combine's place (y is then unused).
 moe_status forward_impl(const char* call, const moe_shape* s, const void* x, const void* router_w,
                        const float* router_bias, const void* w_gate, const void* w_up, const void* w_down,
                        const void* s_gate, const void* s_up, const void* s_down, void* y, int32_t* topk_ids_out,
-                       float* topk_w_out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                       float* topk_w_out, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                       moe::NormArgs* post = nullptr) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
   st = check_ffn(s);
@@ -332,7 +474,7 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
   REQUIRE_SCALE(s, s_gate);
   REQUIRE_SCALE(s, s_up);
   REQUIRE_SCALE(s, s_down);
-  REQUIRE_PTR(y);
+  if (!post) REQUIRE_PTR(y);
   REQUIRE_PTR(workspace);
   if (router_bias && !aligned16(router_bias)) return fail(MOE_ERR_ALIGN, "router_bias is not 16-byte aligned");
   if (topk_ids_out && !aligned16(topk_ids_out)) return fail(MOE_ERR_ALIGN, "topk_ids_out is not 16-byte aligned");
@@ -359,7 +501,7 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
     a.claims_gate_up = reinterpret_cast<unsigned long long*>(ws + L.claims);
     a.claims_down = reinterpret_cast<unsigned long long*>(ws + L.claims + moe::kTileClaimBytes);
   }
-  if (use_stream(s) && moe::stream_gate_up_takes_ids((long)s->T * s->K, s->E)) {
+  if (use_stream(s) && s->weight_fmt != MOE_W_MXFP4 && moe::stream_gate_up_takes_ids((long)s->T * s->K, s->E)) {
     // at most 256 slots: the gate/up pass derives the permutation from the ids
     // and writes it for the down pass and the combine (one launch fewer)
     a.ids = ids;
@@ -381,6 +523,14 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
   if (st != MOE_OK) return st;
   st = run_down(call, s, a, stream);
   if (st != MOE_OK) return st;
+  if (post) {
+    post->y_rows = y_rows;
+    post->slot_to_row = s2r;
+    post->topk_w = wts;
+    e = moe::launch_block_norm(*post, stream);
+    if (e != hipSuccess) return hip_fail(e, "norm launch");
+    return MOE_OK;
+  }
   e = moe::launch_combine(y_rows, s2r, wts, s->T, s->d, s->K, s->act_dtype == MOE_BF16, y, stream);
   if (e != hipSuccess) return hip_fail(e, "combine launch");
   return MOE_OK;
@@ -721,6 +871,263 @@ moe_status moe_pack_rows(int64_t rows, int32_t cols, const int8_t* q, int8_t* pa
   const hipError_t e = moe::launch_pack_rows(rows, cols, q, packed, stream);
   if (e != hipSuccess) return hip_fail(e, "pack launch");
   return MOE_OK;
+}
+
+moe_status moe_quantize_mxfp4(int64_t rows, int32_t cols, int32_t src_dtype, const void* w, int32_t layout, uint8_t* q,
+                              uint8_t* s, hipStream_t stream) {
+  const moe_status st = check_mxfp4(rows, cols, layout, q, s);
+  if (st != MOE_OK) return st;
+  if (src_dtype != MOE_F32 && src_dtype != MOE_BF16) return fail(MOE_ERR_DTYPE, "src_dtype=%d", src_dtype);
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(w);
+  const hipError_t e = moe::launch_mx_quantize(rows, cols, src_dtype == MOE_BF16, w, layout == MOE_MX_TILED, q, s, stream);
+  if (e != hipSuccess) return hip_fail(e, "quantize launch");
+  return MOE_OK;
+}
+
+moe_status moe_dequantize_mxfp4(int64_t rows, int32_t cols, int32_t layout, const uint8_t* q, const uint8_t* s,
+                                int32_t dst_dtype, void* w, hipStream_t stream) {
+  const moe_status st = check_mxfp4(rows, cols, layout, q, s);
+  if (st != MOE_OK) return st;
+  if (dst_dtype != MOE_F32 && dst_dtype != MOE_BF16) return fail(MOE_ERR_DTYPE, "dst_dtype=%d", dst_dtype);
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(w);
+  const hipError_t e = moe::launch_mx_dequantize(rows, cols, layout == MOE_MX_TILED, q, s, dst_dtype == MOE_BF16, w, stream);
+  if (e != hipSuccess) return hip_fail(e, "dequantize launch");
+  return MOE_OK;
+}
+
+moe_status moe_pack_mxfp4(int64_t rows, int32_t cols, const uint8_t* q, const uint8_t* s, uint8_t* q_tiled,
+                          uint8_t* s_tiled, hipStream_t stream) {
+  moe_status st = check_mxfp4(rows, cols, MOE_MX_TILED, q, s);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  REQUIRE_PTR(q_tiled);
+  REQUIRE_PTR(s_tiled);
+  if (q == q_tiled || s == s_tiled) return fail(MOE_ERR_UNSUPPORTED, "packing cannot be done in place");
+  const hipError_t e = moe::launch_mx_pack(rows, cols, q, s, q_tiled, s_tiled, stream);
+  if (e != hipSuccess) return hip_fail(e, "pack launch");
+  return MOE_OK;
+}
+
+moe_status moe_grouped_mm_mxfp4(const moe_shape* s, const uint8_t* a_q, const uint8_t* a_s,
+                                const int32_t* expert_offsets, const int32_t* sorted_slots, const uint8_t* w_q,
+                                const uint8_t* w_s, const uint8_t* w2_q, const uint8_t* w2_s, void* out,
+                                hipStream_t stream) {
+  moe_status st = check_mx_shape(s);
+  if (st != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  REQUIRE_PTR(a_q);
+  REQUIRE_PTR(a_s);
+  REQUIRE_PTR(expert_offsets);
+  if (!aligned16(sorted_slots)) return fail(MOE_ERR_ALIGN, "sorted_slots is not 16-byte aligned");
+  REQUIRE_PTR(w_q);
+  REQUIRE_PTR(w_s);
+  if (w2_q || w2_s) {
+    REQUIRE_PTR(w2_q);
+    REQUIRE_PTR(w2_s);
+  }
+  REQUIRE_PTR(out);
+  if (debug_on() && (st = debug_inputs(s, expert_offsets, sorted_slots, stream)) != MOE_OK) return st;
+  moe::MxArgs m;
+  m.a = a_q;
+  m.a_s = a_s;
+  m.offsets = expert_offsets;
+  m.sorted_slots = sorted_slots;
+  m.topk = s->K;
+  m.w0 = w_q;
+  m.s0 = w_s;
+  m.w1 = w2_q;
+  m.s1 = w2_s;
+  m.out = out;
+  m.out_bf16 = s->act_dtype == MOE_BF16;
+  m.E = s->E;
+  m.N = s->f;
+  m.Kd = s->d;
+  m.S = s->T * s->K;
+  return run_mx("product launch", s, m, stream);
+}
+
+moe_status moe_expert_ffn_mxfp4_workspace_size(const moe_shape* shape, size_t* bytes) {
+  const moe_status st = check_mx_shape(shape);
+  if (st != MOE_OK) return st;
+  if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+  *bytes = mx_ffn_layout(shape).total;
+  return MOE_OK;
+}
+
+moe_status moe_expert_ffn_mxfp4(const moe_shape* s, const void* x, const int32_t* expert_offsets,
+                                const int32_t* sorted_slots, const uint8_t* w_gate, const uint8_t* w_up,
+                                const uint8_t* w_down, const uint8_t* s_gate, const uint8_t* s_up,
+                                const uint8_t* s_down, float* y_rows, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream) {
+  moe_status st = check_mx_shape(s);
+  if (st != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(expert_offsets);
+  REQUIRE_PTR(sorted_slots);
+  REQUIRE_PTR(w_gate);
+  REQUIRE_PTR(w_up);
+  REQUIRE_PTR(w_down);
+  REQUIRE_PTR(s_gate);
+  REQUIRE_PTR(s_up);
+  REQUIRE_PTR(s_down);
+  REQUIRE_PTR(y_rows);
+  REQUIRE_PTR(workspace);
+  const MxFfnLayout L = mx_ffn_layout(s);
+  if (workspace_bytes < L.total)
+    return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, L.total);
+  if (debug_on() && (st = debug_inputs(s, expert_offsets, sorted_slots, stream)) != MOE_OK) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  const long S = (long)s->T * s->K;
+  moe::MxArgs m;
+  m.offsets = expert_offsets;
+  m.E = s->E;
+  m.S = (int)S;
+
+  hipError_t e = moe::launch_mx_quantize(s->T, s->d, s->act_dtype == MOE_BF16, x, false, ws + L.xq, ws + L.xs, stream);
+  if (e != hipSuccess) return hip_fail(e, "quantize launch");
+  m.a = ws + L.xq;
+  m.a_s = ws + L.xs;
+  m.sorted_slots = sorted_slots;
+  m.topk = s->K;
+  m.w0 = w_gate;
+  m.s0 = s_gate;
+  m.w1 = w_up;
+  m.s1 = s_up;
+  m.out = ws + L.h;
+  m.out_bf16 = true;
+  m.N = s->f;
+  m.Kd = s->d;
+  st = run_mx("gate/up launch", s, m, stream);
+  if (st != MOE_OK) return st;
+
+  // rows past off[E] hold whatever the workspace held: their codes are never read
+  e = moe::launch_mx_quantize(S, s->f, true, ws + L.h, false, ws + L.hq, ws + L.hs, stream);
+  if (e != hipSuccess) return hip_fail(e, "quantize launch");
+  m.a = ws + L.hq;
+  m.a_s = ws + L.hs;
+  m.sorted_slots = nullptr;
+  m.topk = 1;
+  m.w0 = w_down;
+  m.s0 = s_down;
+  m.w1 = m.s1 = nullptr;
+  m.out = y_rows;
+  m.out_bf16 = false;
+  m.N = s->d;
+  m.Kd = s->f;
+  return run_mx("down launch", s, m, stream);
+}
+
+moe_status moe_norm_pre(const moe_shape* s, const void* x, const void* weight, float eps, void* n, hipStream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if ((st = check_eps("eps", eps)) != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(weight);
+  REQUIRE_PTR(n);
+  moe::NormArgs a = {};
+  a.act_bf16 = s->act_dtype == MOE_BF16;
+  a.x = x;
+  a.weight = weight;
+  a.out = n;
+  a.eps = eps;
+  a.T = s->T;
+  a.d = s->d;
+  const hipError_t e = moe::launch_block_norm(a, stream);
+  if (e != hipSuccess) return hip_fail(e, "norm launch");
+  return MOE_OK;
+}
+
+moe_status moe_norm_post(const moe_shape* s, const moe_post* post, const void* y, const void* residual, void* out,
+                         void* next, hipStream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if ((st = check_post(s, post, residual, out, next)) != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  REQUIRE_PTR(y);
+  moe::NormArgs a = post_args(s, post, residual, out, next);
+  a.x = y;
+  const hipError_t e = moe::launch_block_norm(a, stream);
+  if (e != hipSuccess) return hip_fail(e, "norm launch");
+  return MOE_OK;
+}
+
+moe_status moe_combine_post(const moe_shape* s, const moe_post* post, const float* y_rows, const int32_t* slot_to_row,
+                            const float* topk_w, const void* residual, void* out, void* next, hipStream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if ((st = check_post(s, post, residual, out, next)) != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  REQUIRE_PTR(y_rows);
+  REQUIRE_PTR(slot_to_row);
+  REQUIRE_PTR(topk_w);
+  if (debug_on() && (st = debug_rows(s, slot_to_row, stream)) != MOE_OK) return st;
+  moe::NormArgs a = post_args(s, post, residual, out, next);
+  a.y_rows = y_rows;
+  a.slot_to_row = slot_to_row;
+  a.topk_w = topk_w;
+  const hipError_t e = moe::launch_block_norm(a, stream);
+  if (e != hipSuccess) return hip_fail(e, "norm launch");
+  return MOE_OK;
+}
+
+moe_status moe_block_workspace_size(const moe_shape* shape, size_t* bytes) {
+  const moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+  *bytes = round_up(forward_layout(shape).total) + block_x_bytes(shape);
+  return MOE_OK;
+}
+
+moe_status moe_block_forward(const moe_shape* s, const void* residual, const void* pre_weight, float pre_eps,
+                             const void* x, const moe_post* post, const void* router_w, const float* router_bias,
+                             const void* w_gate, const void* w_up, const void* w_down, const void* s_gate,
+                             const void* s_up, const void* s_down, void* out, void* next, int32_t* topk_ids_out,
+                             float* topk_w_out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if ((st = check_ffn(s)) != MOE_OK) return st;
+  if ((st = check_post(s, post, residual, out, next)) != MOE_OK) return st;
+  if (pre_weight && (st = check_eps("pre_eps", pre_eps)) != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  if (!x == !pre_weight)
+    return fail(x ? MOE_ERR_UNSUPPORTED : MOE_ERR_NULL, "exactly one of x and pre_weight is given");
+  if (!aligned16(pre_weight)) return fail(MOE_ERR_ALIGN, "pre_weight is not 16-byte aligned");
+  REQUIRE_PTR(workspace);
+  const size_t fwd = round_up(forward_layout(s).total), need = fwd + block_x_bytes(s);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
+  // everything forward_impl checks, before the first launch
+  REQUIRE_PTR(router_w);
+  REQUIRE_PTR(w_gate);
+  REQUIRE_PTR(w_up);
+  REQUIRE_PTR(w_down);
+  REQUIRE_SCALE(s, s_gate);
+  REQUIRE_SCALE(s, s_up);
+  REQUIRE_SCALE(s, s_down);
+  if (!aligned16(router_bias)) return fail(MOE_ERR_ALIGN, "router_bias is not 16-byte aligned");
+  if (!aligned16(topk_ids_out)) return fail(MOE_ERR_ALIGN, "topk_ids_out is not 16-byte aligned");
+  if (!aligned16(topk_w_out)) return fail(MOE_ERR_ALIGN, "topk_w_out is not 16-byte aligned");
+  if (!aligned16(x)) return fail(MOE_ERR_ALIGN, "x is not 16-byte aligned");
+  moe::NormArgs pa = post_args(s, post, residual, out, next);
+  if (pre_weight) {
+    moe::NormArgs a = {};
+    a.act_bf16 = s->act_dtype == MOE_BF16;
+    a.x = residual;
+    a.weight = pre_weight;
+    a.out = static_cast<char*>(workspace) + fwd;
+    a.eps = pre_eps;
+    a.T = s->T;
+    a.d = s->d;
+    const hipError_t e = moe::launch_block_norm(a, stream);
+    if (e != hipSuccess) return hip_fail(e, "norm launch");
+    x = a.out;
+  }
+  return forward_impl("moe_block_forward", s, x, router_w, router_bias, w_gate, w_up, w_down, s_gate, s_up, s_down,
+                      nullptr, topk_ids_out, topk_w_out, workspace, fwd, stream, &pa);
 }
 
 }  // extern "C"

@@ -83,4 +83,46 @@ hipError_t launch_pack_rows(long rows, int cols, const int8_t* src, int8_t* dst,
 hipError_t launch_quantize_rows(int64_t rows, int cols, bool src_bf16, const void* w, bool scale_bf16, int8_t* q,
                                 void* s, bool fp8, bool tiled, hipStream_t stream);
 
+// MXFP4 (mx_common.h): quantizer, dequantizer and packer. tiled: rows % 16 ==
+// 0, cols % 128 == 0; row-major: cols % 32 == 0.
+hipError_t launch_mx_quantize(int64_t rows, int cols, bool src_bf16, const void* w, bool tiled, uint8_t* q, uint8_t* s,
+                              hipStream_t stream);
+hipError_t launch_mx_dequantize(int64_t rows, int cols, bool tiled, const uint8_t* q, const uint8_t* s, bool dst_bf16,
+                                void* w, hipStream_t stream);
+hipError_t launch_mx_pack(int64_t rows, int cols, const uint8_t* q, const uint8_t* s, uint8_t* q_tiled,
+                          uint8_t* s_tiled, hipStream_t stream);
+
+// Products with MXFP4 weights over rows grouped by expert.
+struct MxArgs {
+  const void* a;                // rows: bf16 [., Kd], or MXFP4 codes [., Kd/2]
+  const uint8_t* a_s;           // their scales [., Kd/32], or null: a is bf16
+  const int32_t* offsets;       // [E + 1]
+  const int32_t* sorted_slots;  // [S]: sorted row r reads row sorted_slots[r] / topk of a; null: row r
+  int topk;
+  const uint8_t *w0, *s0;       // [E, N, Kd] codes and scales, tiled
+  const uint8_t *w1, *s1;       // second matrix: out = silu(w0 . a) * (w1 . a); null: out = w0 . a
+  void* out;                    // [S, N]
+  bool out_bf16;                // else fp32
+  int E, N, Kd, S;
+};
+hipError_t launch_mx_stream(const MxArgs& a, hipStream_t stream);
+
+// Norms around the layer (block_norm.hip).
+struct NormArgs {
+  bool act_bf16;               // x, residual, weights, gate, out, next
+  const void* x;               // [T, d]: normalised (residual null), or the layer's output y
+  const float* y_rows;         // the experts' rows, combined into y; null: y is x
+  const int32_t* slot_to_row;  // [T, K]
+  const float* topk_w;         // [T, K]
+  const void* residual;        // [T, d]; null: out = rms(x) * weight
+  const void* weight;          // [d]; null after the block: y as it is
+  const void* gate;            // [ceil(T / gate_tokens), d] or null
+  const void* next_weight;     // [d] or null: no next
+  void* out;                   // [T, d]
+  void* next;                  // [T, d]
+  float residual_scale, block_scale, eps, next_eps;
+  int T, d, K, gate_tokens;
+};
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t stream);
+
 }  // namespace moe

@@ -14,8 +14,8 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import (MOE_BF16, MOE_F32, MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_TILED, MOE_W_BF16,  # noqa: F401
-                   MOE_W_FP8, MOE_W_INT8, MoeError, MoeShape)
+from ._lib import (MOE_BF16, MOE_F32, MOE_MX_ROWS, MOE_MX_TILED, MOE_PATH_AUTO, MOE_PATH_STREAM,  # noqa: F401
+                   MOE_PATH_TILED, MOE_W_BF16, MOE_W_FP8, MOE_W_INT8, MOE_W_MXFP4, MoeError, MoePost, MoeShape)
 
 _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -30,6 +30,8 @@ class Int8Experts:
     OCP e4m3 codes (uint8 tensors). fmt MOE_W_BF16 (comparator): q_* are the
     bf16 weights themselves and s_* are None. Every q_* holds its bytes in the
     tiled layout of moe_pack_rows; the tensor shape is kept for the sizes.
+    fmt MOE_W_MXFP4: q_* [E, out, in/2] uint8 (two codes a byte) and s_* [E, out,
+    in/32] uint8 in the tiled layout of moe_quantize_mxfp4.
     """
     q_gate: torch.Tensor
     q_up: torch.Tensor
@@ -49,10 +51,12 @@ class Int8Experts:
 
     @property
     def d(self) -> int:
-        return self.q_gate.shape[2]
+        return self.q_gate.shape[2] * (2 if self.fmt == MOE_W_MXFP4 else 1)
 
     @property
     def scale_dtype(self) -> torch.dtype:
+        if self.fmt == MOE_W_MXFP4:
+            return torch.bfloat16   # not used: the scales are bytes
         return self.s_gate.dtype if self.s_gate is not None else torch.bfloat16
 
 
@@ -396,3 +400,246 @@ def quantize_experts(w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Ten
         out.append(q)
         scales.append(s)
     return Int8Experts(out[0], out[1], out[2], scales[0], scales[1], scales[2])
+
+
+# ---------------------------------------------------------------- MXFP4 and the norms around the layer
+
+def _arg(name: str, t: Optional[torch.Tensor], dtype: Optional[torch.dtype], shape=None):
+    """Pointer of a tensor of this type and shape on the current device (None: NULL)."""
+    if t is None:
+        return None
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current HIP device")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    return _ptr(t)
+
+
+def moe_quantize_mxfp4(w: torch.Tensor, tiled: bool = False):
+    """w [..., cols] (fp32/bf16) -> (codes uint8 [..., cols/2], scale bytes uint8 [..., cols/32]),
+    row-major or in the tiled layout the kernels read weights in."""
+    lib = _lib_handle()
+    if w.dim() < 1 or w.shape[-1] % 32:
+        raise ValueError(f"the last dimension of {tuple(w.shape)} is not a multiple of 32")
+    cols = w.shape[-1]
+    rows = w.numel() // cols if cols else 0
+    q = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
+    s = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
+    _lib.check(lib.moe_quantize_mxfp4(rows, cols, _dtype_code(w.dtype), _arg("w", w, None),
+                                      MOE_MX_TILED if tiled else MOE_MX_ROWS, _ptr(q), _ptr(s), _stream()))
+    return q, s
+
+
+def _mx_shape(q: torch.Tensor, s: torch.Tensor):
+    cols = q.shape[-1] * 2
+    if q.dim() < 1 or cols % 32 or tuple(s.shape) != (*q.shape[:-1], cols // 32):
+        raise ValueError(f"codes {tuple(q.shape)} and scales {tuple(s.shape)} do not belong together")
+    return (q.numel() // q.shape[-1] if cols else 0), cols
+
+
+def moe_dequantize_mxfp4(q: torch.Tensor, s: torch.Tensor, dtype: torch.dtype, tiled: bool = False) -> torch.Tensor:
+    """The numbers [..., cols] in `dtype` that codes and scales stand for."""
+    lib = _lib_handle()
+    rows, cols = _mx_shape(q, s)
+    code = _dtype_code(dtype)
+    w = torch.empty((*q.shape[:-1], cols), dtype=dtype, device=q.device)
+    _lib.check(lib.moe_dequantize_mxfp4(rows, cols, MOE_MX_TILED if tiled else MOE_MX_ROWS,
+                                        _arg("q", q, torch.uint8), _arg("s", s, torch.uint8), code, _ptr(w),
+                                        _stream()))
+    return w
+
+
+def moe_pack_mxfp4(q: torch.Tensor, s: torch.Tensor):
+    """Row-major codes and scales (a checkpoint's) -> (codes, scales) in the tiled layout, same shapes."""
+    lib = _lib_handle()
+    rows, cols = _mx_shape(q, s)
+    qt, st = torch.empty_like(q), torch.empty_like(s)
+    _lib.check(lib.moe_pack_mxfp4(rows, cols, _arg("q", q, torch.uint8), _arg("s", s, torch.uint8), _ptr(qt),
+                                  _ptr(st), _stream()))
+    return qt, st
+
+
+def quantize_experts_mxfp4(w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor) -> Int8Experts:
+    """Load time: (out, in) expert weights -> MXFP4 in the tiled layout (one pass)."""
+    g, u, d = (moe_quantize_mxfp4(w, tiled=True) for w in (w_gate, w_up, w_down))
+    return Int8Experts(g[0], u[0], d[0], g[1], u[1], d[1], fmt=MOE_W_MXFP4)
+
+
+def pack_mxfp4_experts(q_gate: torch.Tensor, q_up: torch.Tensor, q_down: torch.Tensor, s_gate: torch.Tensor,
+                       s_up: torch.Tensor, s_down: torch.Tensor) -> Int8Experts:
+    """Row-major MXFP4 codes and scales -> Int8Experts in the kernels' tiled layout."""
+    g, u, d = (moe_pack_mxfp4(q, s) for q, s in ((q_gate, s_gate), (q_up, s_up), (q_down, s_down)))
+    return Int8Experts(g[0], u[0], d[0], g[1], u[1], d[1], fmt=MOE_W_MXFP4)
+
+
+def moe_grouped_mm_mxfp4(a_q: torch.Tensor, a_s: torch.Tensor, expert_offsets: torch.Tensor, w_q: torch.Tensor,
+                         w_s: torch.Tensor, out_dtype: torch.dtype, sorted_slots: Optional[torch.Tensor] = None,
+                         K: int = 1, w2_q: Optional[torch.Tensor] = None, w2_s: Optional[torch.Tensor] = None,
+                         path: int = MOE_PATH_AUTO, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Products grouped by expert, both operands in MXFP4.
+
+    a_q [rows, d/2], a_s [rows, d/32] row-major; w_q [E, f, d/2], w_s [E, f, d/32]
+    tiled. With sorted_slots [rows*K] sorted row r reads a's row
+    sorted_slots[r] // K, else its own row r (K = 1). With w2_*: silu(W a) *
+    (W2 a). Returns out [rows*K, f] in out_dtype (rows past the last segment are
+    left as they are: uninitialised unless `out` is given)."""
+    lib = _lib_handle()
+    if a_q.dim() != 2 or w_q.dim() != 3:
+        raise ValueError("a_q must be [rows, d/2] and w_q [E, f, d/2]")
+    rows, d = a_q.shape[0], a_q.shape[1] * 2
+    E, f = w_q.shape[0], w_q.shape[1]
+    if sorted_slots is None and K != 1:
+        raise ValueError("K is the slots per row of sorted_slots: 1 without it")
+    if (w2_q is None) != (w2_s is None):
+        raise ValueError("w2_q and w2_s are given together")
+    shape = MoeShape(rows, d, f, E, K, _dtype_code(out_dtype), MOE_BF16, path, MOE_W_MXFP4)
+    if out is None:
+        out = torch.empty((rows * K, f), dtype=out_dtype, device=a_q.device)
+    u8, w_shape, s_shape = torch.uint8, (E, f, d // 2), (E, f, d // 32)
+    _lib.check(lib.moe_grouped_mm_mxfp4(
+        ctypes.byref(shape), _arg("a_q", a_q, u8), _arg("a_s", a_s, u8, (rows, d // 32)),
+        _arg("expert_offsets", expert_offsets, torch.int32, (E + 1,)),
+        _arg("sorted_slots", sorted_slots, torch.int32, (rows * K,)), _arg("w_q", w_q, u8),
+        _arg("w_s", w_s, u8, s_shape), _arg("w2_q", w2_q, u8, w_shape), _arg("w2_s", w2_s, u8, s_shape),
+        _arg("out", out, out_dtype, (rows * K, f)), _stream()))
+    return out
+
+
+def moe_expert_ffn_mxfp4(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_slots: torch.Tensor,
+                         experts: Int8Experts, K: int, path: int = MOE_PATH_AUTO,
+                         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Expert SwiGLU FFNs with weights and activations in MXFP4. Returns y_rows fp32 [T*K, d]."""
+    lib = _lib_handle()
+    if experts.fmt != MOE_W_MXFP4:
+        raise ValueError("the experts are not in MXFP4")
+    T, d = x.shape
+    if d != experts.d:
+        raise ValueError(f"x has {d} columns, the experts {experts.d}")
+    shape = make_shape(T, d, experts.f, experts.E, K, x.dtype, experts.scale_dtype, path, experts.fmt)
+    n = ctypes.c_size_t(0)
+    _lib.check(lib.moe_expert_ffn_mxfp4_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    y_rows = torch.empty((T * K, d), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=x.device)
+    _lib.check(lib.moe_expert_ffn_mxfp4(
+        ctypes.byref(shape), _arg("x", x, None),
+        _arg("expert_offsets", expert_offsets, torch.int32, (experts.E + 1,)),
+        _arg("sorted_slots", sorted_slots, torch.int32, (T * K,)), _ptr(experts.q_gate), _ptr(experts.q_up),
+        _ptr(experts.q_down), _ptr(experts.s_gate), _ptr(experts.s_up), _ptr(experts.s_down), _ptr(y_rows),
+        _arg("workspace", workspace, torch.uint8), ctypes.c_size_t(workspace.numel()), _stream()))
+    return y_rows
+
+
+def moe_norm_pre(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """RMS norm before the layer: x / sqrt(mean(x^2) + eps) * weight, [T, d] in x.dtype. out may be x."""
+    lib = _lib_handle()
+    T, d = x.shape
+    shape = make_shape(T, d, 64, 1, 1, x.dtype, torch.float32)
+    if out is None:
+        out = torch.empty_like(x)
+    _lib.check(lib.moe_norm_pre(ctypes.byref(shape), _arg("x", x, None), _arg("weight", weight, x.dtype, (d,)), eps,
+                                _arg("out", out, x.dtype, (T, d)), _stream()))
+    return out
+
+
+def _post(T: int, d: int, dtype: torch.dtype, weight, gate, gate_tokens: int, residual_scale: float,
+          block_scale: float, eps: float, next_weight, next_eps: Optional[float]) -> MoePost:
+    rows = (-(-T // gate_tokens), d) if gate_tokens >= 1 else None
+    return MoePost(_arg("weight", weight, dtype, (d,)), _arg("gate", gate, dtype, rows),
+                   _arg("next_weight", next_weight, dtype, (d,)), gate_tokens, residual_scale, block_scale, eps,
+                   eps if next_eps is None else next_eps)
+
+
+def _post_outputs(residual, out, next_weight, next_out):
+    if out is None:
+        out = torch.empty_like(residual)
+    if next_weight is not None and next_out is None:
+        next_out = torch.empty_like(residual)
+    return out, next_out if next_weight is not None else None
+
+
+def moe_norm_post(y: torch.Tensor, residual: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, gate_tokens: int = 1, residual_scale: float = 1.0,
+                  block_scale: float = 1.0, eps: float = 1e-6, next_weight: Optional[torch.Tensor] = None,
+                  next_eps: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                  next_out: Optional[torch.Tensor] = None):
+    """After the layer, y [T, d] its output: out = residual_scale * residual + block_scale * gate *
+    (rms(y) * weight), and with next_weight also next = rms(out) * next_weight, in one pass.
+
+    Without weight y is not normalised; gate [ceil(T / gate_tokens), d] is shared by gate_tokens
+    consecutive tokens a row (None: 1). Returns (out, next or None) in y.dtype; out may be residual or y."""
+    lib = _lib_handle()
+    T, d = y.shape
+    shape = make_shape(T, d, 64, 1, 1, y.dtype, torch.float32)
+    p = _post(T, d, y.dtype, weight, gate, gate_tokens, residual_scale, block_scale, eps, next_weight, next_eps)
+    res = _arg("residual", residual, y.dtype, (T, d))
+    out, nxt = _post_outputs(residual, out, next_weight, next_out)
+    _lib.check(lib.moe_norm_post(ctypes.byref(shape), ctypes.byref(p), _arg("y", y, None), res,
+                                 _arg("out", out, y.dtype, (T, d)), _arg("next_out", nxt, y.dtype, (T, d)),
+                                 _stream()))
+    return out, nxt
+
+
+def moe_combine_post(y_rows: torch.Tensor, slot_to_row: torch.Tensor, topk_w: torch.Tensor, residual: torch.Tensor,
+                     weight: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                     gate_tokens: int = 1, residual_scale: float = 1.0, block_scale: float = 1.0, eps: float = 1e-6,
+                     next_weight: Optional[torch.Tensor] = None, next_eps: Optional[float] = None,
+                     out: Optional[torch.Tensor] = None, next_out: Optional[torch.Tensor] = None):
+    """moe_norm_post with y = sum_k topk_w[t, k] * y_rows[slot_to_row[t*K + k]] (as moe_combine, unrounded)."""
+    lib = _lib_handle()
+    T, K = topk_w.shape
+    d = y_rows.shape[1]
+    dt = residual.dtype
+    shape = make_shape(T, d, 64, max(K, 1), K, dt, torch.float32)
+    p = _post(T, d, dt, weight, gate, gate_tokens, residual_scale, block_scale, eps, next_weight, next_eps)
+    res = _arg("residual", residual, dt, (T, d))
+    out, nxt = _post_outputs(residual, out, next_weight, next_out)
+    _lib.check(lib.moe_combine_post(
+        ctypes.byref(shape), ctypes.byref(p), _arg("y_rows", y_rows, torch.float32, (T * K, d)),
+        _arg("slot_to_row", slot_to_row.view(-1), torch.int32, (T * K,)), _arg("topk_w", topk_w, torch.float32), res,
+        _arg("out", out, dt, (T, d)), _arg("next_out", nxt, dt, (T, d)), _stream()))
+    return out, nxt
+
+
+def block_workspace_size(shape: MoeShape) -> int:
+    lib = _lib_handle()
+    n = ctypes.c_size_t(0)
+    _lib.check(lib.moe_block_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def moe_block_forward(residual: torch.Tensor, router_w: torch.Tensor, bias: Optional[torch.Tensor],
+                      experts: Int8Experts, K: int, pre_weight: Optional[torch.Tensor] = None, pre_eps: float = 1e-6,
+                      x: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                      gate: Optional[torch.Tensor] = None, gate_tokens: int = 1, residual_scale: float = 1.0,
+                      block_scale: float = 1.0, eps: float = 1e-6, next_weight: Optional[torch.Tensor] = None,
+                      next_eps: Optional[float] = None, path: int = MOE_PATH_AUTO,
+                      out: Optional[torch.Tensor] = None, next_out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None):
+    """A block on the residual stream [T, d]: norm (pre_weight; or x, already normalised), the layer, then
+    moe_combine_post. Returns (out, next or None, topk_ids [T, K], topk_w [T, K])."""
+    lib = _lib_handle()
+    T, d = residual.shape
+    dt = residual.dtype
+    if d != experts.d:
+        raise ValueError(f"residual has {d} columns, the experts {experts.d}")
+    shape = make_shape(T, d, experts.f, experts.E, K, dt, experts.scale_dtype, path, experts.fmt)
+    p = _post(T, d, dt, weight, gate, gate_tokens, residual_scale, block_scale, eps, next_weight, next_eps)
+    res = _arg("residual", residual, dt)
+    out, nxt = _post_outputs(residual, out, next_weight, next_out)
+    ids = torch.empty((T, K), dtype=torch.int32, device=residual.device)
+    w = torch.empty((T, K), dtype=torch.float32, device=residual.device)
+    need = block_workspace_size(shape)
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=residual.device)
+    _lib.check(lib.moe_block_forward(
+        ctypes.byref(shape), res, _arg("pre_weight", pre_weight, dt, (d,)), pre_eps, _arg("x", x, dt, (T, d)),
+        ctypes.byref(p), _arg("router_w", router_w, dt, (experts.E, d)),
+        _arg("bias", bias, torch.float32, (experts.E,)), _ptr(experts.q_gate), _ptr(experts.q_up),
+        _ptr(experts.q_down), _ptr(experts.s_gate), _ptr(experts.s_up), _ptr(experts.s_down),
+        _arg("out", out, dt, (T, d)), _arg("next_out", nxt, dt, (T, d)), _ptr(ids), _ptr(w),
+        _arg("workspace", workspace, torch.uint8), ctypes.c_size_t(workspace.numel()), _stream()))
+    return out, nxt, ids, w

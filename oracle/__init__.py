@@ -17,6 +17,8 @@ Modules:
   moe   -- router, top-K gate, permutation, SwiGLU experts, combine (the
            expert FFN takes any codes and per-row scales: int8, e4m3 values,
            or bf16 weights with unit scales).
+  mxfp4 -- MXFP4 encoding, quantizer, tiled layout and grouped products.
+  norm  -- the RMS norms before and after the layer.
 
 Readings taken where the paper is silent:
   * gate = softmax over all n logits, keep the K largest, renormalise;
@@ -29,4 +31,4 @@ Readings taken where the paper is silent:
 Every function's parity is pinned by tests that do not reuse its own formula:
 see tests/test_oracle_*.py.
 """
-from . import quant, fp8, moe  # noqa: F401
+from . import quant, fp8, moe, mxfp4, norm  # noqa: F401
