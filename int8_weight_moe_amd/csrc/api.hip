@@ -235,7 +235,9 @@ bool log_on() {
 void log_pass(const char* call, bool gate_up, const moe_shape* s, const moe::FfnArgs& a) {
   const long S = (long)s->T * s->K;
   char how[192];
-  if (!use_stream(s)) {
+  if (s->weight_fmt == MOE_W_MXFP4 && use_stream(s)) {
+    snprintf(how, sizeof(how), "stream schedule, MXFP4 kernel");
+  } else if (!use_stream(s)) {
     snprintf(how, sizeof(how), "tiled schedule, %s",
              (gate_up ? a.claims_gate_up : a.claims_down) ? "the last tiles of each XCD queue claimed"
                                                           : "static tile order");
@@ -272,6 +274,7 @@ moe::MxArgs mx_gate_up(const moe::FfnArgs& a) {
   m.s1 = static_cast<const uint8_t*>(a.s_up);
   m.out = a.h;
   m.out_bf16 = true;
+  m.claims = a.claims_gate_up;
   m.E = a.E;
   m.N = a.f;
   m.Kd = a.d;
@@ -291,6 +294,7 @@ moe::MxArgs mx_down(const moe::FfnArgs& a) {
   m.w1 = m.s1 = nullptr;
   m.out = a.y_rows;
   m.out_bf16 = false;
+  m.claims = a.claims_down;
   m.E = a.E;
   m.N = a.d;
   m.Kd = a.f;
@@ -299,7 +303,7 @@ moe::MxArgs mx_down(const moe::FfnArgs& a) {
 }
 
 moe_status run_mx(const char* what, const moe_shape* s, const moe::MxArgs& m, hipStream_t stream) {
-  const hipError_t e = moe::launch_mx_stream(m, stream);
+  const hipError_t e = use_stream(s) ? moe::launch_mx_stream(m, stream) : moe::launch_mx_tiled(m, stream);
   if (e != hipSuccess) return hip_fail(e, what);
   return MOE_OK;
 }
@@ -941,6 +945,7 @@ moe_status moe_grouped_mm_mxfp4(const moe_shape* s, const uint8_t* a_q, const ui
   m.s1 = w2_s;
   m.out = out;
   m.out_bf16 = s->act_dtype == MOE_BF16;
+  m.claims = nullptr;
   m.E = s->E;
   m.N = s->f;
   m.Kd = s->d;
@@ -983,6 +988,7 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* s, const void* x, const int32_t
   const long S = (long)s->T * s->K;
   moe::MxArgs m;
   m.offsets = expert_offsets;
+  m.claims = nullptr;
   m.E = s->E;
   m.S = (int)S;
 

@@ -103,9 +103,12 @@ struct MxArgs {
   const uint8_t *w1, *s1;       // second matrix: out = silu(w0 . a) * (w1 . a); null: out = w0 . a
   void* out;                    // [S, N]
   bool out_bf16;                // else fp32
+  unsigned long long* claims;   // tile claim words of the tiled kernel ([8], cleared by the launch), or null
   int E, N, Kd, S;
 };
 hipError_t launch_mx_stream(const MxArgs& a, hipStream_t stream);
+// Needs the rows of a, and a's scales, within 32-bit byte offsets.
+hipError_t launch_mx_tiled(const MxArgs& a, hipStream_t stream);
 
 // Norms around the layer (block_norm.hip).
 struct NormArgs {
