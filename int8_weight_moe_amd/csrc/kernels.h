@@ -99,6 +99,7 @@ struct MxArgs {
   const int32_t* offsets;       // [E + 1]
   const int32_t* sorted_slots;  // [S]: sorted row r reads row sorted_slots[r] / topk of a; null: row r
   int topk;
+  long a_rows;                  // rows of a
   const uint8_t *w0, *s0;       // [E, N, Kd] codes and scales, tiled
   const uint8_t *w1, *s1;       // second matrix: out = silu(w0 . a) * (w1 . a); null: out = w0 . a
   void* out;                    // [S, N]
@@ -107,7 +108,8 @@ struct MxArgs {
   int E, N, Kd, S;
 };
 hipError_t launch_mx_stream(const MxArgs& a, hipStream_t stream);
-// Needs the rows of a, and a's scales, within 32-bit byte offsets.
+// Needs the rows of a within 32-bit byte offsets.
+bool mx_tiled_offsets_fit(const MxArgs& a);
 hipError_t launch_mx_tiled(const MxArgs& a, hipStream_t stream);
 
 // Norms around the layer (block_norm.hip).

@@ -38,7 +38,7 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t* group, int m, int
   return v;
 }
 
-template <bool kMxAct, int NMAT, int NG, int RB, int KS, bool kOutBf16>
+template <bool kMxAct, int NMAT, int NG, int RB, int KS, bool kOutBf16, int U>
 __global__ __launch_bounds__(block_waves(KS) * kWave) void mx_stream_kernel(MxArgs a) {
   constexpr int IPW = block_waves(KS) / KS;   // items per workgroup
   constexpr int AQ = kMxAct ? 1 : 4;          // 16-byte pieces of a token's row per lane and step
@@ -75,8 +75,35 @@ __global__ __launch_bounds__(block_waves(KS) * kWave) void mx_stream_kernel(MxAr
   const int groups = (n + kMxGroup - 1) / kMxGroup;
   const int g0 = kslice * groups / KS, g1 = (kslice + 1) * groups / KS;
 
+  // weights and scales of the steps in use and of the next ones
+  constexpr int UPG = kMxGroup / U;   // units per scale group
+  uint4 w[2][U][NG][NMAT];
+  uint32_t sc[2][NG][NMAT];           // scales of the group in use, and of the next
+  const int s_begin = g0 * kMxGroup, s_end = min(g1 * kMxGroup, n);
+  auto load_w = [&](int s, uint4 (&wb)[U][NG][NMAT]) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (s + j < s_end)
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+          for (int m = 0; m < NMAT; ++m) wb[j][ng][m] = load_nt16(wp[ng][m] + (long)(s + j) * 1024);
+  };
+  auto load_s = [&](int s, uint32_t (&sb)[NG][NMAT]) {
+    const int m4 = min(kMxGroup, n - s);
+#pragma unroll
+    for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) sb[ng][m] = load_scales(sp[ng][m] + (long)s * 64, m4, lane);
+  };
+
   for (int p0 = 0; p0 < nrows; p0 += 16 * RB) {
     const int nrb = min(RB, (nrows - p0 + 15) >> 4);
+    // the first weights are requested before the row numbers are looked up
+    if (s_begin < s_end) {
+      load_w(s_begin, w[0]);
+      load_s(s_begin, sc[0]);
+    }
     const uint8_t* ap[RB];
     const uint8_t* asp[RB];
     bool aok[RB];
@@ -101,62 +128,88 @@ __global__ __launch_bounds__(block_waves(KS) * kWave) void mx_stream_kernel(MxAr
 #pragma unroll
         for (int m = 0; m < NMAT; ++m) acc[rb][ng][m] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    for (int g = g0; g < g1; ++g) {
-      const int s0 = g * kMxGroup;
-      const int m4 = min(kMxGroup, n - s0);
-      uint4 w[kMxGroup][NG][NMAT];
-      uint32_t sc[NG][NMAT];
+    // U steps at a time (U divides a scale group), NRB row blocks present: the
+    // activations of these steps are requested, then the weights of the next
+    // ones, then the steps are computed. Loads return in order, so waiting for
+    // the activations does not wait for the weights requested behind them.
+    auto run = [&](auto nrbc) {
+      constexpr int NRB = decltype(nrbc)::value;
+      // unit kU of the group at step s0, whose scales are sb; its weights are wb
+      auto unit = [&](auto uc, int s0, const uint4 (&wb)[U][NG][NMAT], const uint32_t (&sb)[NG][NMAT],
+                      uint4 (&wn)[U][NG][NMAT], uint32_t (&sn)[NG][NMAT]) {
+        constexpr int UI = decltype(uc)::value;
+        const int s1 = s0 + UI * U;
+        if (s1 >= s_end) return;
+        uint4 av[U][NRB][AQ];
+        uint32_t as[U][NRB];
 #pragma unroll
-      for (int ng = 0; ng < NG; ++ng)
+        for (int j = 0; j < U; ++j)
 #pragma unroll
-        for (int m = 0; m < NMAT; ++m) {
-          sc[ng][m] = load_scales(sp[ng][m] + s0 * 64, m4, lane);
+          for (int rb = 0; rb < NRB; ++rb) {
+            as[j][rb] = 0;
 #pragma unroll
-          for (int j = 0; j < kMxGroup; ++j)
-            if (j < m4) w[j][ng][m] = load_nt16(wp[ng][m] + (long)(s0 + j) * 1024);
-        }
-      auto step = [&](auto jc) {
-        constexpr int j = decltype(jc)::value;
-        if (j >= m4) return;
-        uint4 av[RB][AQ];
-        uint32_t as[RB];
+            for (int q = 0; q < AQ; ++q) av[j][rb][q] = make_uint4(0, 0, 0, 0);
+            if (s1 + j < s_end && aok[rb]) {
+              const uint8_t* p = ap[rb] + (long)(s1 + j) * (kMxAct ? 64 : 256);
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-          as[rb] = 0;
-#pragma unroll
-          for (int q = 0; q < AQ; ++q) av[rb][q] = make_uint4(0, 0, 0, 0);
-          if (rb < nrb && aok[rb]) {
-            const uint8_t* p = ap[rb] + (long)(s0 + j) * (kMxAct ? 64 : 256);
-#pragma unroll
-            for (int q = 0; q < AQ; ++q) av[rb][q] = *reinterpret_cast<const uint4*>(p + 16 * q);
-            if constexpr (kMxAct) as[rb] = asp[rb][(s0 + j) * 4];
-          }
-        }
-#pragma unroll
-        for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-          for (int m = 0; m < NMAT; ++m) {
-            if constexpr (kMxAct) {
-#pragma unroll
-              for (int rb = 0; rb < RB; ++rb)
-                if (rb < nrb) acc[rb][ng][m] = mfma_mx<j, 0>(w[j][ng][m], av[rb][0], acc[rb][ng][m], sc[ng][m], as[rb]);
-            } else {
-              const float s = mx_scale_of<j>(sc[ng][m]);
-              const uint32_t c[4] = {w[j][ng][m].x, w[j][ng][m].y, w[j][ng][m].z, w[j][ng][m].w};
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const bf16x8 wf = mx_bf16x8(c[q], s);
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb)
-                  if (rb < nrb) acc[rb][ng][m] = mfma_bf16(wf, as_bf16x8(av[rb][q]), acc[rb][ng][m]);
-              }
+              for (int q = 0; q < AQ; ++q) av[j][rb][q] = *reinterpret_cast<const uint4*>(p + 16 * q);
+              if constexpr (kMxAct) as[j][rb] = asp[rb][(s1 + j) * 4];
             }
           }
+        load_w(s1 + U, wn);
+        if constexpr (UI == UPG - 1)
+          if (s1 + U < s_end) load_s(s1 + U, sn);
+        auto step = [&](auto jc) {
+          constexpr int j = decltype(jc)::value;
+          if constexpr (j < U) {
+            constexpr int J = UI * U + j;
+            if (s1 + j >= s_end) return;
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+              for (int m = 0; m < NMAT; ++m) {
+                if constexpr (kMxAct) {
+#pragma unroll
+                  for (int rb = 0; rb < NRB; ++rb)
+                    acc[rb][ng][m] = mfma_mx<J, 0>(wb[j][ng][m], av[j][rb][0], acc[rb][ng][m], sb[ng][m], as[j][rb]);
+                } else {
+                  const float s = mx_scale_of<J>(sb[ng][m]);
+                  const uint32_t c[4] = {wb[j][ng][m].x, wb[j][ng][m].y, wb[j][ng][m].z, wb[j][ng][m].w};
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    const bf16x8 wf = mx_bf16x8(c[q], s);
+#pragma unroll
+                    for (int rb = 0; rb < NRB; ++rb)
+                      acc[rb][ng][m] = mfma_bf16(wf, as_bf16x8(av[j][rb][q]), acc[rb][ng][m]);
+                  }
+                }
+              }
+          }
+        };
+        step(int_constant<0>{});
+        step(int_constant<1>{});
+        step(int_constant<2>{});
+        step(int_constant<3>{});
       };
-      step(int_constant<0>{});
-      step(int_constant<1>{});
-      step(int_constant<2>{});
-      step(int_constant<3>{});
+      auto group = [&](auto pc, int s0) {
+        constexpr int G = decltype(pc)::value;   // parity of the group
+        // with one unit a group, the weight buffers alternate with the groups
+        unit(int_constant<0>{}, s0, w[UPG == 1 ? G : 0], sc[G], w[UPG == 1 ? 1 - G : 1], sc[1 - G]);
+        if constexpr (UPG >= 2) unit(int_constant<(UPG >= 2 ? 1 : 0)>{}, s0, w[1], sc[G], w[0], sc[1 - G]);
+        if constexpr (UPG >= 4) {
+          unit(int_constant<(UPG >= 4 ? 2 : 0)>{}, s0, w[0], sc[G], w[1], sc[1 - G]);
+          unit(int_constant<(UPG >= 4 ? 3 : 0)>{}, s0, w[1], sc[G], w[0], sc[1 - G]);
+        }
+      };
+      for (int s0 = s_begin; s0 < s_end; s0 += 2 * kMxGroup) {
+        group(int_constant<0>{}, s0);
+        group(int_constant<1>{}, s0 + kMxGroup);
+      }
+    };
+    if (RB == 1 || nrb == 1) {
+      run(int_constant<1>{});
+    } else {
+      run(int_constant<RB>{});
     }
 
     if constexpr (KS > 1) {
@@ -194,17 +247,33 @@ __global__ __launch_bounds__(block_waves(KS) * kWave) void mx_stream_kernel(MxAr
   }
 }
 
-template <bool kMxAct, int NMAT, int NG, int RB, bool kOutBf16>
-hipError_t launch_ks(const MxArgs& a, hipStream_t stream) {
-  const long items = (long)min(a.E, a.S) * (a.N / (16 * NG));   // an expert with rows has one of the S at least
-  const int groups = (a.Kd / kMxStep + kMxGroup - 1) / kMxGroup;
+// Items of 16*NG channels over the experts that can have rows (each has one of
+// the S at least).
+long stream_items(const MxArgs& a, int NG) { return (long)min(a.E, a.S) * (a.N / (16 * NG)); }
+
+// Slices of the reduction (whole scale groups): doubled until the pass has 4096
+// waves, and on to 8192 as long as a wave keeps 64 KiB of codes to stream.
+// Measured (us) for 1, 2, 4, 8 slices: gate/up of one token (d 4096, f 14336,
+// 1792 items) -, -, 25.3, 29.0; of 32 tokens (7168 items) 164, 148, -, -; down of 32
+// tokens (1024 items, 28 groups) -, 81.8, 82.5, 91.6; of 64 tokens (d 8192, f
+// 24576, 2048 items, 48 groups) 283, 301, 279, -.
+int stream_slices(long items, int groups, long group_bytes) {
   int ks = 1;
-  while (ks < 8 && items * ks < 8192 && 2 * ks <= groups) ks *= 2;
+  while (ks < 8 && 2 * ks <= groups &&
+         (items * ks < 4096 || (items * ks < 8192 && groups * group_bytes >= 2 * ks * (64L << 10))))
+    ks *= 2;
+  return ks;
+}
+
+template <bool kMxAct, int NMAT, int NG, int RB, bool kOutBf16, int U>
+hipError_t launch_ks(const MxArgs& a, hipStream_t stream) {
+  const long items = stream_items(a, NG);
+  const int groups = (a.Kd / kMxStep + kMxGroup - 1) / kMxGroup;
 #define MOE_MX_STREAM(KS)                                                                                       \
-  hipLaunchKernelGGL((mx_stream_kernel<kMxAct, NMAT, NG, RB, KS, kOutBf16>),                                    \
+  hipLaunchKernelGGL((mx_stream_kernel<kMxAct, NMAT, NG, RB, KS, kOutBf16, U>),                                 \
                      dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves)),              \
                      dim3(block_waves(KS) * kWave), 0, stream, a)
-  switch (ks) {
+  switch (stream_slices(items, groups, NG * NMAT * kMxGroup * 1024L)) {
     case 1: MOE_MX_STREAM(1); break;
     case 2: MOE_MX_STREAM(2); break;
     case 4: MOE_MX_STREAM(4); break;
@@ -214,21 +283,49 @@ hipError_t launch_ks(const MxArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Channels per item: wide items read the rows' activations fewer times (a wave
+// reads its rows' bf16 activations from L2 for every item: down of 64 tokens, d
+// 8192, 534, 351 and 279 us for 16, 32 and 64 channels), narrow ones give few
+// items more waves (gate/up of one token: 25.3 us for 16 channels, 27.3 for 32;
+// down of one token: 15.4 us for 32, 20.5 for 64). MXFP4 activations are a
+// quarter of the bytes: 32 channels pay for one matrix with many items (64
+// tokens, d 24576, f 8192: 306 us for 16 channels, 282 for 32; 17 tokens, d 4096,
+// f 14336: 68 and 74). N is a multiple of 128, so every width divides it.
+template <bool kMxAct, int NMAT, int RB, bool kOutBf16>
+hipError_t launch_width(const MxArgs& a, hipStream_t stream) {
+  constexpr int U = RB == 1 ? 2 : 1;   // two row blocks: more steps at once would spill
+  if constexpr (kMxAct) {
+    if constexpr (NMAT == 1)
+      if (stream_items(a, 2) >= 4096) return launch_ks<true, 1, 2, RB, kOutBf16, 2>(a, stream);
+    return launch_ks<true, NMAT, 1, RB, kOutBf16, 2>(a, stream);
+  } else if constexpr (NMAT == 2) {
+    if (stream_items(a, 2) >= 1024) return launch_ks<false, 2, 2, RB, kOutBf16, U>(a, stream);
+    return launch_ks<false, 2, 1, RB, kOutBf16, 1>(a, stream);
+  } else {
+    if (stream_items(a, 4) >= 1024) return launch_ks<false, 1, 4, RB, kOutBf16, U>(a, stream);
+    if (stream_items(a, 2) >= 256) return launch_ks<false, 1, 2, RB, kOutBf16, U>(a, stream);
+    return launch_ks<false, 1, 1, RB, kOutBf16, U>(a, stream);
+  }
+}
+
+// Row blocks per pass: one for up to eight rows an expert on average (an expert
+// with more than 16 streams its weights again), else two.
 template <bool kMxAct, int NMAT, bool kOutBf16>
-hipError_t launch_rb(const MxArgs& a, hipStream_t stream) {
-  return launch_ks<kMxAct, NMAT, 1, 2, kOutBf16>(a, stream);
+hipError_t launch_rows(const MxArgs& a, hipStream_t stream) {
+  return a.S <= 8L * a.E ? launch_width<kMxAct, NMAT, 1, kOutBf16>(a, stream)
+                         : launch_width<kMxAct, NMAT, 2, kOutBf16>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_mx_stream(const MxArgs& a, hipStream_t stream) {
   if (a.a_s) {
-    if (a.w1) return a.out_bf16 ? launch_rb<true, 2, true>(a, stream) : launch_rb<true, 2, false>(a, stream);
-    return a.out_bf16 ? launch_rb<true, 1, true>(a, stream) : launch_rb<true, 1, false>(a, stream);
+    if (a.w1) return a.out_bf16 ? launch_rows<true, 2, true>(a, stream) : launch_rows<true, 2, false>(a, stream);
+    return a.out_bf16 ? launch_rows<true, 1, true>(a, stream) : launch_rows<true, 1, false>(a, stream);
   }
   // bf16 activations: the expert FFN's gate/up (bf16 h) and down (fp32 rows) passes
-  if (a.w1) return a.out_bf16 ? launch_rb<false, 2, true>(a, stream) : hipErrorInvalidValue;
-  return a.out_bf16 ? hipErrorInvalidValue : launch_rb<false, 1, false>(a, stream);
+  if (a.w1) return a.out_bf16 ? launch_rows<false, 2, true>(a, stream) : hipErrorInvalidValue;
+  return a.out_bf16 ? hipErrorInvalidValue : launch_rows<false, 1, false>(a, stream);
 }
 
 }  // namespace moe

@@ -182,18 +182,23 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
       constexpr int J = decltype(jc)::value;
       constexpr int K = J % KB;
       if constexpr (kMxAct) {
-        uint4 xf[MBV];
-        uint32_t xs[MBV];
+        // half of the row blocks at a time: all of them at once would spill
+        constexpr int HB = (MBV + 1) / 2;
 #pragma unroll
-        for (int i = 0; i < MBV; ++i) {
-          const int r = i * 16 + li;
-          xf[i] = *reinterpret_cast<const uint4*>(&As[buf][r * ROWB + (((4 * K + lg) ^ (r % CPR)) * 16)]);
-          xs[i] = reinterpret_cast<const uint8_t*>(&Ss[gbuf][J * kBM + r])[lg];
+        for (int h = 0; h < MBV; h += HB) {
+          uint4 xf[HB];
+          uint32_t xs[HB];
+#pragma unroll
+          for (int i = 0; i < HB; ++i) {
+            const int r = (h + i) * 16 + li;
+            xf[i] = *reinterpret_cast<const uint4*>(&As[buf][r * ROWB + (((4 * K + lg) ^ (r % CPR)) * 16)]);
+            xs[i] = reinterpret_cast<const uint8_t*>(&Ss[gbuf][J * kBM + r])[lg];
+          }
+#pragma unroll
+          for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int i = 0; i < HB; ++i) acc[h + i][j] = mfma_mx<J, 0>(w[j][K], xf[i], acc[h + i][j], sb[j], xs[i]);
         }
-#pragma unroll
-        for (int j = 0; j < NB; ++j)
-#pragma unroll
-          for (int i = 0; i < MBV; ++i) acc[i][j] = mfma_mx<J, 0>(w[j][K], xf[i], acc[i][j], sb[j], xs[i]);
       } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -274,13 +279,16 @@ __global__ void zero_words_kernel(unsigned long long* __restrict__ claims) {
 }
 
 template <bool kMxAct, int NMAT, bool kOutBf16>
-hipError_t launch_tiled(const MxArgs& a, hipStream_t stream) {
+hipError_t launch_tiled(MxArgs a, hipStream_t stream) {
   constexpr int GM = NMAT == 2 ? 8 : 4;
   constexpr int CH = kBN / NMAT;
   const int n_tiles = (a.N + CH - 1) / CH;
   const long total = ((long)(a.S + kBM - 1) / kBM + a.E) * n_tiles;
   const long per_xcd = (total + kXcds - 1) / kXcds;
   long blocks = kXcds * per_xcd;
+  // The claimed tail costs a launch (3 us) and balances the XCDs over many
+  // rounds of the 512 workgroups that run at once: not for a few rounds.
+  if (total < 2048) a.claims = nullptr;
   if (a.claims) {
     // the static blocks of the longest queue, then one and a half times its tail
     blocks = kXcds * (per_xcd + min(per_xcd, (long)kClaimTail) / 2);
@@ -292,6 +300,10 @@ hipError_t launch_tiled(const MxArgs& a, hipStream_t stream) {
 }
 
 }  // namespace
+
+bool mx_tiled_offsets_fit(const MxArgs& a) {
+  return (uint64_t)a.a_rows * (uint64_t)a.Kd * (a.a_s ? 1 : 4) < (1ull << 33);
+}
 
 hipError_t launch_mx_tiled(const MxArgs& a, hipStream_t stream) {
   if (a.a_s) {

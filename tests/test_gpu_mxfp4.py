@@ -125,6 +125,17 @@ CASES = [
     ([0, 257, 0], 2, 2048, 128),
     ([1] * 40 + [0] * 24, 0, 256, 256),
 ]
+# many channel groups (the wide items of the streaming kernel, one and two row blocks, a second pass over the
+# weights), long reductions (all its splits, a partial last scale group) and, for the tiled kernel, many rounds of tiles
+LARGE = [
+    ([9, 0, 1, 16, 17] + [2] * 11, 0, 4096, 256),
+    ([20, 0, 33, 16, 17] + [12] * 11, 0, 4096, 128),
+    ([9, 0, 1, 16, 17] + [2] * 11, 0, 256, 2048),
+    ([20, 0, 33, 16, 17] + [12] * 11, 0, 128, 2048),
+    ([3, 0, 18], 1, 4224, 128),
+    ([3, 0, 18], 1, 128, 4224),
+    ([2] * 40 + [0] * 23 + [130], 0, 128, 4096),
+]
 
 
 def _slots_for(counts, extra, rng, K=2):
@@ -136,7 +147,7 @@ def _slots_for(counts, extra, rng, K=2):
 
 
 @pytest.mark.parametrize("path", PATHS)
-@pytest.mark.parametrize("counts,extra,d,f", CASES)
+@pytest.mark.parametrize("counts,extra,d,f", CASES + LARGE)
 def test_ffn_passes(counts, extra, d, f, path):
     rng = np.random.default_rng(d + f + sum(counts))
     E, K = len(counts), 2 if len(counts) > 1 else 1
@@ -189,6 +200,13 @@ def test_grouped_mm(counts, extra, d, f, gather, swiglu, out, path):
                                bf16=out == "bf16")
     check(got, ref, bound, int(off[-1]), "product")
     assert (got[int(off[-1]):] == 7.0).all()
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("counts,extra,d,f", LARGE)
+def test_grouped_mm_large(counts, extra, d, f, swiglu, path):
+    test_grouped_mm(counts, extra, d, f, True, swiglu, "f32", path)
 
 
 @pytest.mark.parametrize("path", PATHS)
