@@ -98,9 +98,9 @@ size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 constexpr long kStreamRowsPerExpert = 64;
 // The same for MXFP4 weights with bf16 activations, and with MXFP4 activations.
 // Measured (us, stream / tiled; d 4096, f 14336, 16 experts): gate/up at 8 rows an
-// expert 165 / 234, at 16 196 / 243, at 32 334 / 269; both in MXFP4 at 4 rows 84 /
-// 87, at 8 88 / 90, at 16 102 / 93.
-constexpr long kMxStreamRowsPerExpert = 24;
+// expert 163 / 188, at 16 196 / 191, at 32 338 / 261, down at 16 114 / 122, at 32 212
+// / 135; both in MXFP4 (SwiGLU) at 8 rows 157 / 168, at 16 178 / 174, at 32 324 / 182.
+constexpr long kMxStreamRowsPerExpert = 16;
 constexpr long kMxMxStreamRowsPerExpert = 8;
 
 moe_status check_shape(const moe_shape* s) {

@@ -32,8 +32,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kBM = 128;
-constexpr int kBN = 256;
 constexpr int kWaves = 4;
 constexpr int kXcds = 8;
 constexpr int kClaimTail = 128;   // as in ffn_tiled.hip: the tiles of a queue's end that are claimed
@@ -43,13 +41,21 @@ __device__ __forceinline__ void dma4(const void* base, uint32_t voff, uint32_t l
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(voff), "s"(base) : "memory");
 }
 
-template <bool kMxAct, int NMAT, bool kOutBf16, int GM>
-__global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2))) void mx_tiled_kernel(
+// Waves a SIMD must have room for, which is workgroups a CU: a smaller tile
+// needs fewer accumulators, and more workgroups keep more weights in flight
+// (bf16 activations of 128 rows fill LDS with two).
+constexpr int waves_per_simd(bool mx_act, int rows, int channels) {
+  return rows * channels >= 128 * 256 || (!mx_act && rows >= 128) ? 2 : 3;
+}
+
+template <bool kMxAct, int NMAT, bool kOutBf16, int GM, int kBM, int kBN>
+__global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(waves_per_simd(kMxAct, kBM, kBN)))) void mx_tiled_kernel(
     MxArgs a, int n_tiles) {
   constexpr int KB = kMxAct ? 2 : 1;               // 128-column blocks per step
   constexpr int SPG = kMxGroup / KB;               // steps per scale group
   constexpr int ROWB = kMxAct ? 128 : 256;         // bytes of an activation row per step
   constexpr int CPR = ROWB / 16;                   // its 16-byte chunks
+  constexpr int SROWS = kBM < 64 ? 64 : kBM;       // rows of a block's scales in LDS: whole loads of 64
   constexpr int A_STAGE = kBM * ROWB;
   constexpr int A_INSTR = A_STAGE / 1024 / kWaves; // 1 KiB loads per wave and step
   constexpr int RPI = 1024 / ROWB;                 // rows per load
@@ -58,7 +64,7 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
   constexpr int HALF = NB / NMAT;                  // of each matrix
   constexpr int CH_TILE = kBN / NMAT;
   __shared__ __attribute__((aligned(1024))) uint8_t As[2][A_STAGE];
-  __shared__ __attribute__((aligned(1024))) uint32_t Ss[2][kMxAct ? kMxGroup * kBM : 4];
+  __shared__ __attribute__((aligned(1024))) uint32_t Ss[2][kMxAct ? kMxGroup * SROWS : 4];
   __shared__ int s_tile;
 
   const int lane = threadIdx.x & 63;
@@ -76,8 +82,8 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
   }
   const int n0 = nt * CH_TILE;
 
-  // ---- activation sources: instruction j of this wave covers rows RPI*(A_INSTR*wave + j) + lane/CPR; byte offset of
-  // this lane's chunk at step 0
+  // ---- activation sources: load j of this wave covers rows RPI*(wave + kWaves*j) + lane/CPR (so the first loads of
+  // all the waves cover the first rows); byte offset of this lane's chunk at step 0
   const uint32_t row_bytes = kMxAct ? (uint32_t)a.Kd / 2u : (uint32_t)a.Kd * 2u;
   uint32_t a_off[A_INSTR];
   auto src_row = [&](int r) {
@@ -86,25 +92,23 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
   };
 #pragma unroll
   for (int j = 0; j < A_INSTR; ++j) {
-    const int r = RPI * (A_INSTR * wave + j) + lane / CPR;
+    const int r = RPI * (wave + kWaves * j) + lane / CPR;
     const int chunk = (lane % CPR) ^ (r % CPR);
     a_off[j] = src_row(r) * row_bytes + (uint32_t)(chunk * 16);
   }
-  // second block of the last step of an odd number of blocks: re-read the first one
-  auto step_off = [&](int j, int step) {
-    uint32_t off = a_off[j] + (uint32_t)step * ROWB;
-    if constexpr (KB == 2) {
-      const int r = RPI * (A_INSTR * wave + j) + lane / CPR;
-      const int chunk = (lane % CPR) ^ (r % CPR);
-      if (2 * step + 1 >= n && chunk >= 4) off -= 64u;
-    }
+  // The second block of the last step of an odd number of blocks re-reads the first one: 64 bytes back for the lanes
+  // whose chunk lies in it (a load covers whole swizzle periods, so the chunk is the same for every load).
+  const uint32_t second = KB == 2 && (((lane % CPR) ^ (lane / CPR % CPR)) & 4) ? 64u : 0u;
+  auto step_off = [&](int step) {
+    uint32_t off = (uint32_t)step * ROWB;
+    if constexpr (KB == 2) off -= second & (2 * step + 1 >= n ? ~0u : 0u);
     return off;
   };
   // byte offsets of the scales of rows lane and 64 + lane
   uint32_t s_off[2] = {0, 0};
   if constexpr (kMxAct) {
     s_off[0] = src_row(lane) * (uint32_t)(n * 4);
-    s_off[1] = src_row(64 + lane) * (uint32_t)(n * 4);
+    if constexpr (kBM > 64) s_off[1] = src_row(64 + lane) * (uint32_t)(n * 4);
   }
 
   // ---- weight sources: this lane's 16 bytes of block 0 of each channel block, and the row group's scales
@@ -121,18 +125,20 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
   }
 
   const int nsteps = (n + KB - 1) / KB;
-  auto issue_a = [&](int step, int buf) {
-    const int st = min(step, nsteps - 1);
+  // the first MBV row blocks of a step
+  auto issue_a = [&](int step, int buf, auto mbc) {
+    constexpr int LOADS = decltype(mbc)::value * 16 / RPI / kWaves;
+    const uint32_t off = step_off(min(step, nsteps - 1));
 #pragma unroll
-    for (int j = 0; j < A_INSTR; ++j)
-      dma16(a.a, step_off(j, st), lds_addr(&As[buf][0]) + (A_INSTR * wave + j) * 1024);
+    for (int j = 0; j < LOADS; ++j)
+      dma16(a.a, a_off[j] + off, lds_addr(&As[buf][0]) + (wave + kWaves * j) * 1024);
   };
   // wave w copies the row scales of block w of the group (past the row's end: of its last block)
   auto issue_s = [&](int group, int buf) {
     if constexpr (kMxAct) {
       const uint32_t blk = (uint32_t)min(group * kMxGroup + wave, n - 1);
-      dma4(a.a_s, s_off[0] + blk * 4u, lds_addr(&Ss[buf][wave * kBM]));
-      dma4(a.a_s, s_off[1] + blk * 4u, lds_addr(&Ss[buf][wave * kBM + 64]));
+      dma4(a.a_s, s_off[0] + blk * 4u, lds_addr(&Ss[buf][wave * SROWS]));
+      if constexpr (kBM > 64) dma4(a.a_s, s_off[1] + blk * 4u, lds_addr(&Ss[buf][wave * SROWS + 64]));
     }
   };
   auto load_b = [&](int step, uint4 (&b)[NB][KB]) {
@@ -140,8 +146,8 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
     for (int j = 0; j < NB; ++j)
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
-        const int blk = min(step * KB + k, n - 1);
-        b[j][k] = *reinterpret_cast<const uint4*>(b_ptr[j] + (long)blk * 1024 + 16 * lane);
+        const uint8_t* p = b_ptr[j] + (long)min(step * KB + k, n - 1) * 1024;   // uniform
+        b[j][k] = *reinterpret_cast<const uint4*>(p + 16u * (uint32_t)lane);
       }
   };
   auto load_sb = [&](int group, uint32_t (&s)[NB]) {
@@ -168,13 +174,14 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
 
   const int mb_valid = (nrows + 15) / 16;
   auto main_loop = [&](auto mbc) {
-    constexpr int MBV = decltype(mbc)::value;      // row blocks computed
+    constexpr int MBV = decltype(mbc)::value;      // row blocks loaded and computed
+    static_assert(MBV * 16 % (RPI * kWaves) == 0, "whole loads");
     uint4 b[2][NB][KB];
     uint32_t sb[NB], sb_next[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) sb[j] = sb_next[j] = 0;
     issue_s(0, 0);
-    issue_a(0, 0);
+    issue_a(0, 0, mbc);
     load_b(0, b[0]);
     load_sb(0, sb_next);
     // one 128-column block of a step: kJ is its place in the scale group
@@ -192,7 +199,7 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
           for (int i = 0; i < HB; ++i) {
             const int r = (h + i) * 16 + li;
             xf[i] = *reinterpret_cast<const uint4*>(&As[buf][r * ROWB + (((4 * K + lg) ^ (r % CPR)) * 16)]);
-            xs[i] = reinterpret_cast<const uint8_t*>(&Ss[gbuf][J * kBM + r])[lg];
+            xs[i] = reinterpret_cast<const uint8_t*>(&Ss[gbuf][J * SROWS + r])[lg];
           }
 #pragma unroll
           for (int j = 0; j < NB; ++j)
@@ -232,7 +239,7 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
         issue_s(group + 1, (group + 1) & 1);
         load_sb(group + 1, sb_next);
       }
-      issue_a(st + 1, (S + 1) & 1);
+      issue_a(st + 1, (S + 1) & 1, mbc);
       load_b(st + 1, b[(S + 1) & 1]);
       if constexpr (KB == 2) {
         block(int_constant<2 * S>{}, S & 1, group & 1, b[S & 1]);
@@ -252,10 +259,12 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(2
     }
   };
   // a segment's last tile skips the row blocks it does not have, in steps of two
-  if (mb_valid > 6) main_loop(int_constant<8>{});
-  else if (mb_valid > 4) main_loop(int_constant<6>{});
-  else if (mb_valid > 2) main_loop(int_constant<4>{});
-  else main_loop(int_constant<2>{});
+  switch ((mb_valid + 1) / 2) {
+    case 1: main_loop(int_constant<2>{}); break;
+    case 2: main_loop(int_constant<MB < 4 ? MB : 4>{}); break;
+    case 3: main_loop(int_constant<MB < 6 ? MB : 6>{}); break;
+    default: main_loop(int_constant<MB>{}); break;
+  }
   // no load may still be writing this workgroup's LDS when the waves exit
   __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
 
@@ -278,25 +287,54 @@ __global__ void zero_words_kernel(unsigned long long* __restrict__ claims) {
   if (threadIdx.x < kXcds) claims[threadIdx.x] = 0ull;
 }
 
-template <bool kMxAct, int NMAT, bool kOutBf16>
-hipError_t launch_tiled(MxArgs a, hipStream_t stream) {
-  constexpr int GM = NMAT == 2 ? 8 : 4;
+template <bool kMxAct, int NMAT, bool kOutBf16, int kBM, int kBN>
+hipError_t launch_tile(MxArgs a, hipStream_t stream) {
+  // row tiles of an expert that take a channel tile together
+  constexpr int GM = (NMAT == 2 || kMxAct) ? 8 : 4;
   constexpr int CH = kBN / NMAT;
   const int n_tiles = (a.N + CH - 1) / CH;
   const long total = ((long)(a.S + kBM - 1) / kBM + a.E) * n_tiles;
   const long per_xcd = (total + kXcds - 1) / kXcds;
   long blocks = kXcds * per_xcd;
   // The claimed tail costs a launch (3 us) and balances the XCDs over many
-  // rounds of the 512 workgroups that run at once: not for a few rounds.
+  // rounds of the workgroups that run at once: not for a few rounds.
   if (total < 2048) a.claims = nullptr;
   if (a.claims) {
     // the static blocks of the longest queue, then one and a half times its tail
     blocks = kXcds * (per_xcd + min(per_xcd, (long)kClaimTail) / 2);
     hipLaunchKernelGGL(zero_words_kernel, dim3(1), dim3(kWave), 0, stream, a.claims);
   }
-  hipLaunchKernelGGL((mx_tiled_kernel<kMxAct, NMAT, kOutBf16, GM>), dim3((unsigned)blocks), dim3(kWaves * kWave), 0,
-                     stream, a, n_tiles);
+  hipLaunchKernelGGL((mx_tiled_kernel<kMxAct, NMAT, kOutBf16, GM, kBM, kBN>), dim3((unsigned)blocks), dim3(kWaves * kWave),
+                     0, stream, a, n_tiles);
   return hipGetLastError();
+}
+
+// Tile of a pass, in rows x channels, from the rows an expert has on average
+// and the tiles there are (a tile of 128 x 256 runs twice a CU: 512 at once).
+// Measured, in us, as 128x256 / 64x256 / 128x128:
+//   MXFP4 activations: small channel tiles while the weights bound the pass
+//     (SwiGLU, d 4096, f 14336, E 16: at 16 rows an expert 184 / 193 / 174, at 64 198 / 242 / 194, at 128 253 / 320 / 279);
+//   gate/up: 128x256 (same sizes, 32 rows an expert 258 / 298 / 368), but where it
+//     takes a second round that 64x256, three a CU, does not (d 2048, f 1408, E 64, 16
+//     rows: 52 / 41 / 60);
+//   down: small channel tiles where most of the 512 would stay empty (f 14336, d
+//     4096, E 16, 32 rows an expert: 164 / 163 / 135; but d 2048, f 1408, E 64: 32 / 31 / 39);
+//     small row tiles for a few rounds of many rows (128 rows an expert: 304 / 254
+//     / 308; 2999 tokens, d 8192, f 24576, skewed: 1990 / 1878 / 2194; at 64 rows 41 / 48 / 47).
+template <bool kMxAct, int NMAT, bool kOutBf16>
+hipError_t launch_tiled(const MxArgs& a, hipStream_t stream) {
+  const long S = a.S, E = a.E;
+  if constexpr (kMxAct) {
+    if (S <= 64 * E) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, stream);
+  } else if constexpr (NMAT == 2) {
+    const long tiles = E * ((a.N + 127) / 128);
+    if (S <= 48 * E && tiles > 512 && tiles <= 768) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, stream);
+  } else {
+    const long tiles = (S / 128 + E) * ((a.N + 255) / 256);
+    if (tiles <= 384) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, stream);
+    if (S >= 96 * E && tiles < 2048) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, stream);
+  }
+  return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
 }
 
 }  // namespace
