@@ -344,6 +344,7 @@ moe_status check_mxfp4(int64_t rows, int32_t cols, int32_t layout, const void* q
   if (cols < 32 || cols > (1 << 20) || cols % 32) return fail(MOE_ERR_SHAPE, "cols=%d must be a multiple of 32 in [32, 2^20]", cols);
   if (layout == MOE_MX_TILED && (rows % 16 || cols % 128))
     return fail(MOE_ERR_SHAPE, "the tiled layout needs rows=%ld to be a multiple of 16 and cols=%d of 128", (long)rows, cols);
+  if (layout == MOE_MX_TILED && rows * (int64_t)cols / 128 >= (1L << 30)) return fail(MOE_ERR_SHAPE, "matrix too large");
   if (rows == 0) return MOE_OK;
   REQUIRE_PTR(q);
   REQUIRE_PTR(s);

@@ -189,8 +189,8 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(w
       constexpr int J = decltype(jc)::value;
       constexpr int K = J % KB;
       if constexpr (kMxAct) {
-        // half of the row blocks at a time: all of them at once would spill
-        constexpr int HB = (MBV + 1) / 2;
+        // two row blocks at a time: more fragments at once would spill
+        constexpr int HB = 2;
 #pragma unroll
         for (int h = 0; h < MBV; h += HB) {
           uint4 xf[HB];

@@ -67,7 +67,7 @@ def _check(got, ref, bound, what):
 
 # every row length class of the kernel, its edges, and lengths that leave threads without a chunk
 SIZES = [(1, 64), (3, 320), (2, 512), (5, 2048), (4, 2112), (1, 4096), (7, 8192), (2, 8256), (3, 16384), (2, 32768),
-         (2, 32832), (1, 65536), (600, 192), (1030, 1024)]
+         (2, 32832), (1, 65536), (600, 192), (1030, 1024), (1025, 4160), (1024, 16384)]
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
@@ -135,6 +135,26 @@ def test_combine_post(T, d, K, act):
     ro, bo, rn, bn = _bounds(y, 2 * K * U * np.abs(terms).sum(1), res, kw, act)
     _check(out, ro, bo, "out")
     _check(nxt, rn, bn, "next")
+
+
+@pytest.mark.parametrize("T,d,act", [(16400, 2048, "bf16"), (4100, 8192, "bf16"), (1100, 32768, "bf16"),
+                                     (300, 65536, "f32")])
+def test_large_outputs(T, d, act):
+    """Outputs of 64 MiB and more (stored past the caches) are the same as those of a part of the rows on their own."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    y, res = (torch.randn(T, d, generator=g, device="cuda").to(DT[act]) for _ in range(2))
+    w = torch.ones(d, dtype=DT[act], device="cuda")
+    n = m.moe_norm_pre(y, w)
+    out, nxt = m.moe_norm_post(y, res, weight=w, next_weight=w)
+    for lo in (0, T // 2, T - 3):
+        # few rows take another spread of the row over threads: the sums' order differs, the bound is the same
+        rows = slice(lo, lo + 3)
+        ro, bo, rn, bn = _bounds(np64(y[rows]), np.zeros((3, d)), res[rows], dict(weight=w.cpu(), next_weight=w.cpu()), act)
+        _check(out[rows], ro, bo, "out")
+        _check(nxt[rows], rn, bn, "next")
+        ref = onorm.rms(np64(y[rows]), np64(w), 1e-6)
+        err = np.abs(ref) * (d / 2 + 8) * U + 1e-37
+        _check(n[rows], ref, err + _half_step(act) * (np.abs(ref) + err), "pre")
 
 
 def test_nan_and_infinity_stay_in_their_tokens():

@@ -50,7 +50,7 @@ def _hard_rows(rows, cols, src, seed):
 
 
 @pytest.mark.parametrize("src", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,cols", [(1, 32), (7, 96), (2, 4096), (33, 160), (513, 1056)])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (7, 96), (2, 4096), (33, 160), (513, 1056), (2051, 4128)])
 def test_quantize_rows_bit_exact(rows, cols, src):
     w = _hard_rows(rows, cols, src, rows * cols)
     q, s = m.moe_quantize_mxfp4(w.cuda())
