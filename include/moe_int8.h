@@ -45,13 +45,14 @@
  *   - Debug checks: while the environment variable MOE_DEBUG is set (to a
  *     value other than "0"), the calls that take or produce a permutation
  *     also check it, on the host:
- *       moe_expert_ffn, moe_expert_gate_up, moe_expert_down: expert_offsets
- *         starts at 0, never decreases and ends at most at T*K; for the first
- *         two, the sorted rows below off[E] hold distinct slots in [0, T*K);
- *       moe_combine: every slot_to_row entry is -1 or in [0, T*K);
+ *       moe_expert_ffn, moe_expert_gate_up, moe_expert_down,
+ *       moe_expert_ffn_mxfp4, moe_grouped_mm_mxfp4: expert_offsets starts at
+ *         0, never decreases and ends at most at T*K; where sorted_slots is
+ *         given, its rows below off[E] hold distinct slots in [0, T*K);
+ *       moe_combine, moe_combine_post: every slot_to_row entry is -1 or in [0, T*K);
  *       these run BEFORE anything is launched, so bad caller arrays are
  *       reported instead of being read out of bounds by a kernel;
- *       moe_permute, moe_forward, moe_forward_noalloc: after the permutation
+ *       moe_permute, moe_forward, moe_forward_noalloc, moe_block_forward: after the permutation
  *         is computed, also that every id is in [0, E) (all slots placed),
  *         that each expert's rows hold its own slots in ascending order and
  *         that slot_to_row inverts sorted_slots.
@@ -135,8 +136,8 @@ typedef struct moe_shape {
   int32_t weight_fmt;  /* MOE_W_*: encoding of w_gate, w_up, w_down        */
 } moe_shape;
 
-/* ABI version of this header (bumped on any signature change). */
-#define MOE_ABI_VERSION 6
+/* ABI version of this header (bumped on any signature change, and with new calls). */
+#define MOE_ABI_VERSION 7
 int32_t moe_abi_version(void);
 
 /* Static description of a status code. */
@@ -397,7 +398,8 @@ moe_status moe_pack_mxfp4(int64_t rows, int32_t cols, const uint8_t* q, const ui
  *   w_q, w_s, w2_q, w2_s  [E, f, d] tiled codes and scales (w2_*: both NULL for
  *     the plain product).
  *   out [T*K, f] act_dtype; rows past off[E] are left untouched.
- * Products are exact, sums fp32, one rounding. Any segment lengths. */
+ * Products are exact, sums fp32, one rounding. Any segment lengths. Rows of
+ * codes past 32-bit byte offsets (4 GiB) take the STREAM schedule throughout. */
 moe_status moe_grouped_mm_mxfp4(const moe_shape* shape, const uint8_t* a_q, const uint8_t* a_s,
                                 const int32_t* expert_offsets, const int32_t* sorted_slots, const uint8_t* w_q,
                                 const uint8_t* w_s, const uint8_t* w2_q, const uint8_t* w2_s, void* out,
@@ -417,7 +419,9 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* shape, const void* x, const int
                                 hipStream_t stream);
 
 /* ---------------------------------------------------------------- norms around the layer
- * rms(v) = v / sqrt(mean(v^2) + eps) over the d elements of a token, in fp32.
+ * rms(v) = v / sqrt(mean(v^2) + eps) over the d elements of a token, in fp32 (a
+ * sum of squares past the fp32 range is infinite, as from an infinite element:
+ * the token's finite elements become 0).
  *
  * Before the layer: n = rms(x) * weight.
  *   x, n [T, d], weight [d], all act_dtype; n may be x. eps >= 0, finite. */

@@ -242,9 +242,7 @@ bool log_on() {
 void log_pass(const char* call, bool gate_up, const moe_shape* s, const moe::FfnArgs& a) {
   const long S = (long)s->T * s->K;
   char how[192];
-  if (s->weight_fmt == MOE_W_MXFP4 && use_stream(s)) {
-    snprintf(how, sizeof(how), "stream schedule, MXFP4 kernel");
-  } else if (!use_stream(s)) {
+  if (!use_stream(s)) {
     snprintf(how, sizeof(how), "tiled schedule, %s",
              (gate_up ? a.claims_gate_up : a.claims_down) ? "the last tiles of each XCD queue claimed"
                                                           : "static tile order");
@@ -261,7 +259,7 @@ void log_pass(const char* call, bool gate_up, const moe_shape* s, const moe::Ffn
                S > 32L * s->E ? 64 : 32);
     }
   }
-  static const char* const kFmt[] = {"int8", "bf16", "fp8", "", "mxfp4"};
+  static const char* const kFmt[] = {"int8", "bf16", "fp8"};
   fprintf(stderr, "[moe] %s %s: T=%d d=%d f=%d E=%d K=%d act=%s scale=%s weights=%s; %s\n", call,
           gate_up ? "gate/up" : "down", s->T, s->d, s->f, s->E, s->K, s->act_dtype == MOE_BF16 ? "bf16" : "f32",
           s->scale_dtype == MOE_BF16 ? "bf16" : "f32", kFmt[s->weight_fmt], how);
@@ -311,27 +309,32 @@ moe::MxArgs mx_down(const moe::FfnArgs& a) {
   return m;
 }
 
-moe_status run_mx(const char* what, const moe_shape* s, const moe::MxArgs& m, hipStream_t stream) {
+// One product with MXFP4 weights; `call` and `what` name it in the log and in an error.
+moe_status run_mx(const char* call, const char* what, const moe_shape* s, const moe::MxArgs& m, hipStream_t stream) {
   bool by_stream = use_stream(s);
   if (m.a_s && s->ffn_path == MOE_PATH_AUTO) by_stream = m.S <= kMxMxStreamRowsPerExpert * m.E;
   // codes past the tiled kernel's 32-bit offsets (bf16 activations: refused by check_ffn)
   if (!moe::mx_tiled_offsets_fit(m)) by_stream = true;
+  if (log_on())
+    fprintf(stderr, "[moe] %s %s: rows=%d reduction=%d channels=%d E=%d act=%s weights=mxfp4 out=%s; %s schedule%s\n",
+            call, what, m.S, m.Kd, m.N, m.E, m.a_s ? "mxfp4" : "bf16", m.out_bf16 ? "bf16" : "f32",
+            by_stream ? "stream" : "tiled", m.w1 ? ", SwiGLU" : "");
   const hipError_t e = by_stream ? moe::launch_mx_stream(m, stream) : moe::launch_mx_tiled(m, stream);
   if (e != hipSuccess) return hip_fail(e, what);
   return MOE_OK;
 }
 
 moe_status run_gate_up(const char* call, const moe_shape* s, const moe::FfnArgs& a, hipStream_t stream) {
+  if (s->weight_fmt == MOE_W_MXFP4) return run_mx(call, "gate/up", s, mx_gate_up(a), stream);
   if (log_on()) log_pass(call, true, s, a);
-  if (s->weight_fmt == MOE_W_MXFP4) return run_mx("gate/up launch", s, mx_gate_up(a), stream);
   const hipError_t e = use_stream(s) ? moe::launch_stream_gate_up(a, stream) : moe::launch_tiled_gate_up(a, stream);
   if (e != hipSuccess) return hip_fail(e, "gate/up launch");
   return MOE_OK;
 }
 
 moe_status run_down(const char* call, const moe_shape* s, const moe::FfnArgs& a, hipStream_t stream) {
+  if (s->weight_fmt == MOE_W_MXFP4) return run_mx(call, "down", s, mx_down(a), stream);
   if (log_on()) log_pass(call, false, s, a);
-  if (s->weight_fmt == MOE_W_MXFP4) return run_mx("down launch", s, mx_down(a), stream);
   const hipError_t e = use_stream(s) ? moe::launch_stream_down(a, stream) : moe::launch_tiled_down(a, stream);
   if (e != hipSuccess) return hip_fail(e, "down launch");
   return MOE_OK;
@@ -965,7 +968,7 @@ moe_status moe_grouped_mm_mxfp4(const moe_shape* s, const uint8_t* a_q, const ui
   m.N = s->f;
   m.Kd = s->d;
   m.S = s->T * s->K;
-  return run_mx("product launch", s, m, stream);
+  return run_mx("moe_grouped_mm_mxfp4", "product", s, m, stream);
 }
 
 moe_status moe_expert_ffn_mxfp4_workspace_size(const moe_shape* shape, size_t* bytes) {
@@ -1022,7 +1025,7 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* s, const void* x, const int32_t
   m.out_bf16 = true;
   m.N = s->f;
   m.Kd = s->d;
-  st = run_mx("gate/up launch", s, m, stream);
+  st = run_mx("moe_expert_ffn_mxfp4", "gate/up", s, m, stream);
   if (st != MOE_OK) return st;
 
   // rows past off[E] hold whatever the workspace held: their codes are never read
@@ -1040,7 +1043,7 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* s, const void* x, const int32_t
   m.out_bf16 = false;
   m.N = s->d;
   m.Kd = s->f;
-  return run_mx("down launch", s, m, stream);
+  return run_mx("moe_expert_ffn_mxfp4", "down", s, m, stream);
 }
 
 moe_status moe_norm_pre(const moe_shape* s, const void* x, const void* weight, float eps, void* n, hipStream_t stream) {

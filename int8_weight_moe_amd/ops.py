@@ -79,6 +79,11 @@ def _dtype_code(dt: torch.dtype) -> int:
     return _DT[dt]
 
 
+def _check_width(name: str, have: int, want: int) -> None:
+    if have != want:
+        raise ValueError(f"{name} has {have} columns, the experts' weights {want}")
+
+
 def make_shape(T: int, d: int, f: int, E: int, K: int, act: torch.dtype, scale: torch.dtype,
                path: int = MOE_PATH_AUTO, fmt: int = MOE_W_INT8) -> MoeShape:
     return MoeShape(T, d, f, E, K, _dtype_code(act), _dtype_code(scale), path, fmt)
@@ -135,6 +140,7 @@ def moe_expert_ffn(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_slots: 
     """Expert SwiGLU FFNs on the permuted rows. Returns y_rows fp32 [T*K, d] (sorted-row order)."""
     lib = _lib_handle()
     T, d = x.shape
+    _check_width("x", d, experts.d)
     shape = make_shape(T, d, experts.f, experts.E, K, x.dtype, experts.scale_dtype, path, experts.fmt)
     y_rows = torch.empty((T * K, d), dtype=torch.float32, device=x.device)
     need = ffn_workspace_size(shape)
@@ -164,6 +170,7 @@ def moe_expert_gate_up(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_slo
     (same result, bit for bit)."""
     lib = _lib_handle()
     T, d = x.shape
+    _check_width("x", d, experts.d)
     shape = make_shape(T, d, experts.f, experts.E, K, x.dtype, experts.scale_dtype, path, experts.fmt)
     if h is None:
         h = torch.empty((T * K, experts.f), dtype=torch.bfloat16, device=x.device)
@@ -196,6 +203,7 @@ def moe_expert_down(h: torch.Tensor, expert_offsets: torch.Tensor, experts: Int8
     reduction stays inside one workgroup and tiles follow the static order (same
     result, bit for bit)."""
     lib = _lib_handle()
+    _check_width("h", h.shape[1], experts.f)
     shape = make_shape(T, experts.d, experts.f, experts.E, K, act, experts.scale_dtype, path, experts.fmt)
     if y_rows is None:
         y_rows = torch.empty((T * K, experts.d), dtype=torch.float32, device=h.device)
@@ -255,6 +263,7 @@ def moe_forward(x: torch.Tensor, router_w: torch.Tensor, bias: Optional[torch.Te
     """The whole layer. Returns (y [T, d] in x.dtype, topk_ids [T, K], topk_w [T, K])."""
     lib = _lib_handle()
     T, d = x.shape
+    _check_width("x", d, experts.d)
     shape = make_shape(T, d, experts.f, experts.E, K, x.dtype, experts.scale_dtype, path, experts.fmt)
     dev = x.device
     if y is None:
@@ -280,6 +289,7 @@ def moe_forward_noalloc(x: torch.Tensor, router_w: torch.Tensor, bias: Optional[
     that cannot allocate; they are allocated here only when omitted."""
     lib = _lib_handle()
     T, d = x.shape
+    _check_width("x", d, experts.d)
     shape = make_shape(T, d, experts.f, experts.E, K, x.dtype, experts.scale_dtype, path, experts.fmt)
     dev = x.device
     if y is None:
@@ -300,6 +310,7 @@ def moe_mlp_forward(x: torch.Tensor, experts: Int8Experts, path: int = MOE_PATH_
     """Dense int8-weight SwiGLU MLP (one expert, E = K = 1). Returns y [T, d] in x.dtype."""
     lib = _lib_handle()
     T, d = x.shape
+    _check_width("x", d, experts.d)
     if experts.E != 1:
         raise ValueError("the dense MLP takes one expert (E = 1)")
     shape = make_shape(T, d, experts.f, 1, 1, x.dtype, experts.scale_dtype, path, experts.fmt)
@@ -508,7 +519,7 @@ def moe_grouped_mm_mxfp4(a_q: torch.Tensor, a_s: torch.Tensor, expert_offsets: t
     _lib.check(lib.moe_grouped_mm_mxfp4(
         ctypes.byref(shape), _arg("a_q", a_q, u8), _arg("a_s", a_s, u8, (rows, d // 32)),
         _arg("expert_offsets", expert_offsets, torch.int32, (E + 1,)),
-        _arg("sorted_slots", sorted_slots, torch.int32, (rows * K,)), _arg("w_q", w_q, u8),
+        _arg("sorted_slots", sorted_slots, torch.int32, (rows * K,)), _arg("w_q", w_q, u8, w_shape),
         _arg("w_s", w_s, u8, s_shape), _arg("w2_q", w2_q, u8, w_shape), _arg("w2_s", w2_s, u8, s_shape),
         _arg("out", out, out_dtype, (rows * K, f)), _stream()))
     return out
@@ -522,8 +533,7 @@ def moe_expert_ffn_mxfp4(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_s
     if experts.fmt != MOE_W_MXFP4:
         raise ValueError("the experts are not in MXFP4")
     T, d = x.shape
-    if d != experts.d:
-        raise ValueError(f"x has {d} columns, the experts {experts.d}")
+    _check_width("x", d, experts.d)
     shape = make_shape(T, d, experts.f, experts.E, K, x.dtype, experts.scale_dtype, path, experts.fmt)
     n = ctypes.c_size_t(0)
     _lib.check(lib.moe_expert_ffn_mxfp4_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
@@ -631,8 +641,7 @@ def moe_block_forward(residual: torch.Tensor, router_w: torch.Tensor, bias: Opti
     lib = _lib_handle()
     T, d = residual.shape
     dt = residual.dtype
-    if d != experts.d:
-        raise ValueError(f"residual has {d} columns, the experts {experts.d}")
+    _check_width("residual", d, experts.d)
     shape = make_shape(T, d, experts.f, experts.E, K, dt, experts.scale_dtype, path, experts.fmt)
     p = _post(T, d, dt, weight, gate, gate_tokens, residual_scale, block_scale, eps, next_weight, next_eps)
     res = _arg("residual", residual, dt)

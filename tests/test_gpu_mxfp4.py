@@ -232,6 +232,52 @@ def test_nan_and_infinity_stay_in_their_rows(path):
     assert bad[20:, 200].all() and int(bad.sum()) == 3
 
 
+@pytest.mark.parametrize("path", PATHS)
+def test_nan_block_of_an_activation_row(path):
+    """A NaN scale of a row of codes reaches that row's outputs only, from its tokens' slots in both experts."""
+    rng = np.random.default_rng(6)
+    S, off, slots = _slots_for([18, 40], 0, rng, 2)
+    aq, asc = draw_mx(rng, S // 2, 384)
+    asc[3, 7] = 255
+    w = draw_mx(rng, 2, 256, 384)
+    wt = m.moe_pack_mxfp4(dev(w[0]), dev(w[1]))
+    got = m.moe_grouped_mm_mxfp4(dev(aq), dev(asc), dev(off), *wt, torch.float32, sorted_slots=dev(slots), K=2, path=path)
+    bad = got.isnan().cpu().numpy()
+    hit = slots // 2 == 3
+    assert bad[hit].all() and not bad[~hit].any() and hit.sum() == 2
+
+
+def test_log_names_the_schedules(monkeypatch, capfd):
+    monkeypatch.setenv("MOE_LOG", "1")
+    ex = m.quantize_experts_mxfp4(*(torch.randn(1, 128, 128, device="cuda") for _ in range(3)))
+    for T, by in ((4, "stream"), (12, "tiled"), (200, "tiled")):
+        x = torch.randn(T, 128, dtype=torch.bfloat16, device="cuda")
+        off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        m.moe_expert_ffn_mxfp4(x, off, torch.arange(T, dtype=torch.int32, device="cuda"), ex, 1)
+        err = capfd.readouterr().err
+        assert err.count("[moe] moe_expert_ffn_mxfp4") == 2 and err.count(f"; {by} schedule") == 2, err
+    m.moe_mlp_forward(x, ex)
+    err = capfd.readouterr().err
+    assert "moe_mlp_forward gate/up" in err and "act=bf16 weights=mxfp4" in err and "; tiled schedule" in err
+
+
+def test_mismatched_widths_are_refused():
+    ex = m.quantize_experts_mxfp4(*(torch.randn(2, r, c, device="cuda") for r, c in ((256, 128), (256, 128), (128, 256))))
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    srt = torch.arange(4, dtype=torch.int32, device="cuda")
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: m.moe_expert_gate_up(x, off, srt, ex, 1), lambda: m.moe_expert_ffn(x, off, srt, ex, 1),
+                 lambda: m.moe_expert_ffn_mxfp4(x, off, srt, ex, 1), lambda: m.moe_forward(x, x[:2], None, ex, 1),
+                 lambda: m.moe_expert_down(x[:, :128].contiguous(), off, ex, 4, 1),
+                 lambda: m.moe_block_forward(x, x[:2], None, ex, 1, pre_weight=x[0])):
+        with pytest.raises(ValueError, match="columns"):
+            call()
+    with pytest.raises(ValueError, match="contiguous"):
+        m.moe_quantize_mxfp4(torch.zeros(64, 64, device="cuda").t())
+    with pytest.raises(ValueError, match="shape"):
+        m.moe_grouped_mm_mxfp4(*m.moe_quantize_mxfp4(x), off, ex.q_gate, ex.s_gate, torch.float32)
+
+
 def test_two_schedules_agree_and_repeat():
     """Each schedule gives the same bits again, on another stream too."""
     rng = np.random.default_rng(11)
