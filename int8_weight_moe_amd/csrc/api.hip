@@ -96,12 +96,13 @@ size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 // Rows at or below this many per expert (on average) go to the weight-streaming schedule.
 constexpr long kStreamRowsPerExpert = 64;
-// The same for MXFP4 weights with bf16 activations, and with MXFP4 activations.
-// Measured (us, stream / tiled; d 4096, f 14336, 16 experts): gate/up at 8 rows an
-// expert 163 / 188, at 16 196 / 191, at 32 338 / 261, down at 16 114 / 122, at 32 212
-// / 135; both in MXFP4 (SwiGLU) at 8 rows 157 / 168, at 16 178 / 174, at 32 324 / 182.
+// The same with MXFP4 weights: for the down pass (whose schedule the workspaces
+// are sized for), and for the gate/up pass and products of MXFP4 by MXFP4.
+// Measured (us, stream / tiled; d 4096, f 14336, 16 experts): gate/up at 6 rows an
+// expert 160 / 173, at 8 163 / 174, at 10 177 / 175, at 16 196 / 176; both in MXFP4
+// (SwiGLU) at 8 rows 157 / 168, at 16 178 / 174; down at 16 114 / 122, at 32 212 / 135.
 constexpr long kMxStreamRowsPerExpert = 16;
-constexpr long kMxMxStreamRowsPerExpert = 8;
+constexpr long kMxWideStreamRowsPerExpert = 8;
 
 moe_status check_shape(const moe_shape* s) {
   if (!s) return fail(MOE_ERR_NULL, "shape is NULL");
@@ -312,7 +313,8 @@ moe::MxArgs mx_down(const moe::FfnArgs& a) {
 // One product with MXFP4 weights; `call` and `what` name it in the log and in an error.
 moe_status run_mx(const char* call, const char* what, const moe_shape* s, const moe::MxArgs& m, hipStream_t stream) {
   bool by_stream = use_stream(s);
-  if (m.a_s && s->ffn_path == MOE_PATH_AUTO) by_stream = m.S <= kMxMxStreamRowsPerExpert * m.E;
+  if (s->ffn_path == MOE_PATH_AUTO)
+    by_stream = m.S <= (m.a_s || m.w1 ? kMxWideStreamRowsPerExpert : kMxStreamRowsPerExpert) * m.E;
   // codes past the tiled kernel's 32-bit offsets (bf16 activations: refused by check_ffn)
   if (!moe::mx_tiled_offsets_fit(m)) by_stream = true;
   if (log_on())

@@ -316,7 +316,10 @@ hipError_t launch_tile(MxArgs a, hipStream_t stream) {
 //     (SwiGLU, d 4096, f 14336, E 16: at 16 rows an expert 184 / 193 / 174, at 64 198 / 242 / 194, at 128 253 / 320 / 279);
 //   gate/up: 128x256 (same sizes, 32 rows an expert 258 / 298 / 368), but where it
 //     takes a second round that 64x256, three a CU, does not (d 2048, f 1408, E 64, 16
-//     rows: 52 / 41 / 60);
+//     rows: 52 / 41 / 60), and up to 160 rows an expert 64x512 if that leaves enough
+//     tiles: a step then reads twice the weights for its activations (at 17, 32, 64
+//     and 128 rows 239, 258, 335, 502 for 128x256 and 175, 225, 314, 478 for 64x512; at
+//     1024 2679 and 2811);
 //   down: small channel tiles where most of the 512 would stay empty (f 14336, d
 //     4096, E 16, 32 rows an expert: 164 / 163 / 135; but d 2048, f 1408, E 64: 32 / 31 / 39);
 //     small row tiles for a few rounds of many rows (128 rows an expert: 304 / 254
@@ -328,6 +331,7 @@ hipError_t launch_tiled(const MxArgs& a, hipStream_t stream) {
     if (S <= 64 * E) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, stream);
   } else if constexpr (NMAT == 2) {
     const long tiles = E * ((a.N + 127) / 128);
+    if (S <= 160 * E && tiles >= 1536) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 512>(a, stream);
     if (S <= 48 * E && tiles > 512 && tiles <= 768) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, stream);
   } else {
     const long tiles = (S / 128 + E) * ((a.N + 255) / 256);

@@ -135,6 +135,7 @@ LARGE = [
     ([3, 0, 18], 1, 4224, 128),
     ([3, 0, 18], 1, 128, 4224),
     ([2] * 40 + [0] * 23 + [130], 0, 128, 4096),
+    ([70, 3, 64, 129] + [10] * 12, 0, 384, 12416),
 ]
 
 
