@@ -103,6 +103,11 @@ constexpr long kStreamRowsPerExpert = 64;
 // (SwiGLU) at 8 rows 157 / 168, at 16 178 / 174; down at 16 114 / 122, at 32 212 / 135.
 constexpr long kMxStreamRowsPerExpert = 16;
 constexpr long kMxWideStreamRowsPerExpert = 8;
+// With few channels in all, tiles leave most of the GPU idle and the streaming
+// kernel's split reductions do not: both borders are 32 rows then. (gate/up, d
+// 4096, f 1024, E 4, 20 rows 11.9 / 21.5; down, f 4096, d 1024, E 4, 20 rows 10.5 / 22.0.)
+constexpr long kMxFewTilesRowsPerExpert = 32;
+constexpr long kMxFewTilesChannels = 16384;
 
 moe_status check_shape(const moe_shape* s) {
   if (!s) return fail(MOE_ERR_NULL, "shape is NULL");
@@ -314,7 +319,8 @@ moe::MxArgs mx_down(const moe::FfnArgs& a) {
 moe_status run_mx(const char* call, const char* what, const moe_shape* s, const moe::MxArgs& m, hipStream_t stream) {
   bool by_stream = use_stream(s);
   if (s->ffn_path == MOE_PATH_AUTO)
-    by_stream = m.S <= (m.a_s || m.w1 ? kMxWideStreamRowsPerExpert : kMxStreamRowsPerExpert) * m.E;
+    by_stream = m.S <= (m.a_s || m.w1 ? kMxWideStreamRowsPerExpert : kMxStreamRowsPerExpert) * m.E ||
+                (m.S <= kMxFewTilesRowsPerExpert * m.E && (long)m.E * m.N <= kMxFewTilesChannels);
   // codes past the tiled kernel's 32-bit offsets (bf16 activations: refused by check_ffn)
   if (!moe::mx_tiled_offsets_fit(m)) by_stream = true;
   if (log_on())

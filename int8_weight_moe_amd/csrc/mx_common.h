@@ -76,10 +76,6 @@ __device__ __forceinline__ f32x4 mfma_mx(uint4 a, uint4 b, f32x4 c, uint32_t sa,
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, kSa, (int)sa, kSb, (int)sb);
 }
 
-// SwiGLU's gate with fp32 results: the libm exponential and the exact division
-// (a bf16 result is rounded right after silu(), an fp32 one is not).
-__device__ __forceinline__ float silu_f32(float z) { return z / (1.f + expf(-z)); }
-
 // Four consecutive channels of one row from their sums: the sums themselves
 // (NMAT = 1) or silu(first) * second, rounded once to the output type.
 template <bool kOutBf16, int NMAT>
@@ -87,7 +83,7 @@ __device__ __forceinline__ void mx_store4(void* out, long o, const f32x4 (&acc)[
   f32x4 v = acc[0];
   if constexpr (NMAT == 2) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[q] = (kOutBf16 ? silu(v[q]) : silu_f32(v[q])) * acc[1][q];
+    for (int q = 0; q < 4; ++q) v[q] = silu(v[q]) * acc[1][q];
   }
   if constexpr (kOutBf16) {
     bf16x4 b;

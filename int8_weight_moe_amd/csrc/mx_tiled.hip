@@ -229,7 +229,9 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(w
       constexpr int S = decltype(sc)::value;       // step within the group
       const int st = group * SPG + S;
       if (st >= nsteps) return;
-      // this step's loads have landed and every wave is past the buffers that the next ones overwrite
+      // This step's loads have landed and every wave is past the buffers that
+      // the next ones overwrite. (Weights requested two steps ahead, left in
+      // flight here: no faster, a step waits for its activations.)
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
       __builtin_amdgcn_s_barrier();
@@ -296,9 +298,12 @@ hipError_t launch_tile(MxArgs a, hipStream_t stream) {
   const long total = ((long)(a.S + kBM - 1) / kBM + a.E) * n_tiles;
   const long per_xcd = (total + kXcds - 1) / kXcds;
   long blocks = kXcds * per_xcd;
-  // The claimed tail costs a launch (3 us) and balances the XCDs over many
-  // rounds of the workgroups that run at once: not for a few rounds.
-  if (total < 2048) a.claims = nullptr;
+  // The claimed tail costs a launch (3 us) and an atomic in every block past the
+  // static ones, of which there are many if the tile count's bound is loose; it
+  // balances the XCDs over many rounds of long tiles. So: many tiles, several row
+  // tiles an expert, a long reduction. (gate/up of 325 tokens, d 384, f 10496, E 9,
+  // K 4, on 128x128 tiles: 181 us with it.)
+  if (total < 2048 || a.S < 4L * kBM * a.E || a.Kd < 2048) a.claims = nullptr;
   if (a.claims) {
     // the static blocks of the longest queue, then one and a half times its tail
     blocks = kXcds * (per_xcd + min(per_xcd, (long)kClaimTail) / 2);
@@ -309,36 +314,43 @@ hipError_t launch_tile(MxArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Tile of a pass, in rows x channels, from the rows an expert has on average
-// and the tiles there are (a tile of 128 x 256 runs twice a CU: 512 at once).
-// Measured, in us, as 128x256 / 64x256 / 128x128:
-//   MXFP4 activations: small channel tiles while the weights bound the pass
-//     (SwiGLU, d 4096, f 14336, E 16: at 16 rows an expert 184 / 193 / 174, at 64 198 / 242 / 194, at 128 253 / 320 / 279);
-//   gate/up: 128x256 (same sizes, 32 rows an expert 258 / 298 / 368), but where it
-//     takes a second round that 64x256, three a CU, does not (d 2048, f 1408, E 64, 16
-//     rows: 52 / 41 / 60), and up to 160 rows an expert 64x512 if that leaves enough
-//     tiles: a step then reads twice the weights for its activations (at 17, 32, 64
-//     and 128 rows 239, 258, 335, 502 for 128x256 and 175, 225, 314, 478 for 64x512; at
-//     1024 2679 and 2811);
-//   down: small channel tiles where most of the 512 would stay empty (f 14336, d
-//     4096, E 16, 32 rows an expert: 164 / 163 / 135; but d 2048, f 1408, E 64: 32 / 31 / 39);
-//     small row tiles for a few rounds of many rows (128 rows an expert: 304 / 254
-//     / 308; 2999 tokens, d 8192, f 24576, skewed: 1990 / 1878 / 2194; at 64 rows 41 / 48 / 47).
+// Tile of a pass, in rows x channels: the rows from the rows an expert has on
+// average, the channels from the tiles that makes (a tile of 128 x 256 runs
+// twice a CU, one of 64 x 256 three times, the small ones three or four).
+// Measured, in us (d, f as the pass's shape says; E = 16 unless stated):
+//   gate/up, d 4096, f 14336: 64x256 / 128x256 / 64x128 at 32 rows an expert 204 / 222 / 218,
+//     at 64 287 / 283 / 311, at 128 446 / 482 / 491, at 256 795 / 799 / 965, at 1024 2790 /
+//     2669 / 3190; d 2048, f 1408, E 64, 17 rows 40 / 52 / 46; d 2048, f 2816, 512 rows
+//     194 / 164 / 235; few tiles (d 896, f 4224, E 10, 36 rows) 20.8 / 25.2 / 19.9;
+//   down, f 14336, d 4096: 64x256 / 128x256 / 64x128 / 128x128 at 32 rows 164 / 163 / 134 / 134,
+//     at 64 194 / 190 / 183 / 170, at 128 251 / 305 / 282 / 320, at 512 763 / 774 / 847 / 888,
+//     at 1024 1443 / 1443 / 1601 / 1718; f 2816, d 2048, 2048 rows 328 / 323 / 367 / 384;
+//   MXFP4 activations, SwiGLU, d 4096, f 14336: 128x256 / 128x128 at 16 rows 184 / 174, at 64
+//     198 / 194, at 128 253 / 279; few tiles (d 4480, f 1280, E 4, 640 rows) 29.2 / 21.7.
 template <bool kMxAct, int NMAT, bool kOutBf16>
 hipError_t launch_tiled(const MxArgs& a, hipStream_t stream) {
   const long S = a.S, E = a.E;
+  // tiles of `rows` x `channels` if the rows spread evenly
+  auto tiles = [&](int rows, int channels) {
+    const long per_expert = S <= E * rows / 2 ? 2 : 2 * S / (E * rows) + 1;   // halves of a row tile, at least one tile
+    return E * per_expert / 2 * ((a.N + channels / NMAT - 1) / (channels / NMAT));
+  };
   if constexpr (kMxAct) {
-    if (S <= 64 * E) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, stream);
+    if (S <= 64 * E || tiles(128, 256) < 512) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, stream);
+    return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
   } else if constexpr (NMAT == 2) {
-    const long tiles = E * ((a.N + 127) / 128);
-    if (S <= 160 * E && tiles >= 1536) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 512>(a, stream);
-    if (S <= 48 * E && tiles > 512 && tiles <= 768) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, stream);
+    if (S > 160 * E) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
+    if (tiles(64, 256) < 400) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 128>(a, stream);
+    return launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, stream);
   } else {
-    const long tiles = (S / 128 + E) * ((a.N + 255) / 256);
-    if (tiles <= 384) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, stream);
-    if (S >= 96 * E && tiles < 2048) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, stream);
+    if (S > 48 * E && S <= 96 * E) {   // most experts fit 128 rows and not 64
+      if (tiles(128, 256) < 512) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, stream);
+      return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
+    }
+    if (S > 512 * E) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
+    if (tiles(64, 256) < 512) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 128>(a, stream);
+    return launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, stream);
   }
-  return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
 }
 
 }  // namespace

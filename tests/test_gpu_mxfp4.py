@@ -251,7 +251,7 @@ def test_nan_block_of_an_activation_row(path):
 def test_log_names_the_schedules(monkeypatch, capfd):
     monkeypatch.setenv("MOE_LOG", "1")
     ex = m.quantize_experts_mxfp4(*(torch.randn(1, 128, 128, device="cuda") for _ in range(3)))
-    for T, by in ((4, "stream"), (12, "tiled"), (200, "tiled")):
+    for T, by in ((4, "stream"), (32, "stream"), (33, "tiled"), (200, "tiled")):
         x = torch.randn(T, 128, dtype=torch.bfloat16, device="cuda")
         off = torch.tensor([0, T], dtype=torch.int32, device="cuda")
         m.moe_expert_ffn_mxfp4(x, off, torch.arange(T, dtype=torch.int32, device="cuda"), ex, 1)
