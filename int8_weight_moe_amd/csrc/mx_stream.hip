@@ -17,8 +17,8 @@
 // items the reduction is cut into KS slices of whole scale groups, streamed by
 // the KS waves of a workgroup and added through LDS in ascending order.
 // Bound by HBM: down of 64 tokens (d 8192, f 24576, E 16) 279 us, 6171 GB/s of codes,
-// scales and rows; gate/up of one token (d 4096, f 14336, two experts) 25.4 us, 4909
-// GB/s, start and end of the launch included; the MXFP4 product of 17 tokens 73.7 us.
+// scales and rows; gate/up of one token (d 4096, f 14336, two experts) 22.8 us, 5480
+// GB/s, start and end of the launch included; the MXFP4 product of 17 tokens 65.7 us.
 #include "kernels.h"
 #include "mx_common.h"
 
@@ -254,17 +254,24 @@ __global__ __launch_bounds__(block_waves(KS) * kWave) void mx_stream_kernel(MxAr
 // the S at least).
 long stream_items(const MxArgs& a, int NG) { return (long)min(a.E, a.S) * (a.N / (16 * NG)); }
 
-// Slices of the reduction (whole scale groups): doubled until the pass has 4096
-// waves, and on to 8192 as long as a wave keeps 64 KiB of codes to stream.
-// Measured (us) for 1, 2, 4, 8 slices: gate/up of one token (d 4096, f 14336,
-// 1792 items) -, -, 25.3, 29.0; of 32 tokens (7168 items) 164, 148, -, -; down of 32
-// tokens (1024 items, 28 groups) -, 81.8, 82.5, 91.6; of 64 tokens (d 8192, f
-// 24576, 2048 items, 48 groups) 283, 301, 279, -.
-int stream_slices(long items, int groups, long group_bytes) {
+// Slices of the reduction, of whole scale groups (512 columns). Few items are
+// split until HBM is busy; many are split in two, which balances the end of the
+// pass, as long as a slice keeps four groups; in between the waves are kept from
+// a little more than one round of the GPU (some 3000).
+// Measured (us) for 1, 2, 4, 8 slices (items, groups): down of one token, f 14336
+// (256, 28) -, 30.4, 19.8, 15.2; the MXFP4 product of one token, d 14336 (512, 28) -, 24.2,
+// 15.9, 13.0; down of 8, 32 and 100 tokens (1024, 28) 83, 53, 59, - and -, 82, 82, 92 and 156,
+// 96, 103, -; gate/up of one token, d 4096 (1792, 8) -, 22.8, 25.2, 28.7; d 8192 (1536, 16) -,
+// 73.8, 70.9, 77.5; down of 64, f 24576 (2048, 48) 283, 301, 279, 300; gate/up of 32, d 4096
+// (7168, 8) 164, 148, -, -; the MXFP4 product of 17 (7168, 8) 73.7, 65.7, 68.7, 77.7; gate/up of
+// 64, d 8192 (12288, 16) 585, 536, 543, -.
+int stream_slices(long items, int groups) {
+  if (items >= 1024) {
+    if (items >= 1536 && items < 4096 && groups >= 16) return 4;
+    return groups >= 8 ? 2 : 1;
+  }
   int ks = 1;
-  while (ks < 8 && 2 * ks <= groups &&
-         (items * ks < 4096 || (items * ks < 8192 && groups * group_bytes >= 2 * ks * (64L << 10))))
-    ks *= 2;
+  while (ks < 8 && 2 * ks <= groups && (items * ks < 2048 || (items * ks < 4096 && groups / (2 * ks) >= 3))) ks *= 2;
   return ks;
 }
 
@@ -276,7 +283,7 @@ hipError_t launch_ks(const MxArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((mx_stream_kernel<kMxAct, NMAT, NG, RB, KS, kOutBf16, U>),                                 \
                      dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves)),              \
                      dim3(block_waves(KS) * kWave), 0, stream, a)
-  switch (stream_slices(items, groups, NG * NMAT * kMxGroup * 1024L)) {
+  switch (stream_slices(items, groups)) {
     case 1: MOE_MX_STREAM(1); break;
     case 2: MOE_MX_STREAM(2); break;
     case 4: MOE_MX_STREAM(4); break;
