@@ -16,9 +16,9 @@
 // Items are numbered over the experts that have rows. Sums are fp32; with few
 // items the reduction is cut into KS slices of whole scale groups, streamed by
 // the KS waves of a workgroup and added through LDS in ascending order.
-// Bound by HBM: down of 64 tokens (d 8192, f 24576, E 16) 279 us, 6171 GB/s of codes,
-// scales and rows; gate/up of one token (d 4096, f 14336, two experts) 22.8 us, 5480
-// GB/s, start and end of the launch included; the MXFP4 product of 17 tokens 65.7 us.
+// Bound by HBM: down of 64 tokens (d 8192, f 24576, E 16) 279 us, 6170 GB/s of codes,
+// scales and rows; gate/up of one token (d 4096, f 14336, two experts) 23.0 us, 5430
+// GB/s, start and end of the launch included; the MXFP4 product of 17 tokens 71.1 us (65.7 on inputs used before).
 #include "kernels.h"
 #include "mx_common.h"
 

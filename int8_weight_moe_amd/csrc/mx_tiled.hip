@@ -24,9 +24,9 @@
 // Tile order as in ffn_tiled.hip: groups of row tiles of one expert take every
 // channel tile in turn, in eight contiguous XCD queues.
 // Bound by MFMA rate and, in large products, by power: gate/up of 8192 tokens (d
-// 4096, f 14336, E 16) 2671 us, 1441 TFLOP/s, where a library bf16 product of 8192^3
-// reaches 1383; the same with MXFP4 activations 1121 us, 3434 TFLOP/s, the down product
-// of 16384 tokens (d 24576, f 8192) 3369 us, 3916 TFLOP/s (a library MXFP4 product of
+// 4096, f 14336, E 16) 2647 us, 1454 TFLOP/s, where a library bf16 product of 8192^3
+// reaches 1383; the same with MXFP4 activations 1112 us, 3460 TFLOP/s, the down product
+// of 16384 tokens (d 24576, f 8192) 3305 us, 3992 TFLOP/s (a library MXFP4 product of
 // 16384^3: 3364): MFMA busy 57% of the cycles at 1.5 GHz. Not faster: 32x32 MFMAs (5 to
 // 9% slower), 256-row tiles of eight waves (4 to 7%), non-temporal weights (5 to 40%).
 // Rows past the segment read row 0 of the tile and channels past N read channel
