@@ -365,7 +365,8 @@ moe_status moe_pack_rows(int64_t rows, int32_t cols, const int8_t* q, int8_t* pa
  *                 r, columns 32*c .. +32 is byte
  *                   (r/16)*n*64 + 256*(k/4) + m*(16*(c%4) + r%16) + k%4,
  *                   k = c/4, m = min(4, n - 4*(k/4)).
- *                 An expert tensor [E, out, in] is rows = E*out, cols = in. */
+ *                 An expert tensor [E, out, in] is rows = E*out, cols = in.
+ *                 Fewer than 2^37 elements. */
 enum { MOE_MX_ROWS = 0, MOE_MX_TILED = 1 };
 
 /* Quantizer. Per block: b = floor(log2(max |w|)) - 2 + 127, at least 0 (an

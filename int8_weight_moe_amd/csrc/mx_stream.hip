@@ -137,7 +137,7 @@ __global__ __launch_bounds__(block_waves(KS) * kWave) void mx_stream_kernel(MxAr
     // the activations does not wait for the weights requested behind them.
     auto run = [&](auto nrbc) {
       constexpr int NRB = decltype(nrbc)::value;
-      // unit kU of the group at step s0, whose scales are sb; its weights are wb
+      // unit UI of the group at step s0, whose scales are sb; its weights are wb
       auto unit = [&](auto uc, int s0, const uint4 (&wb)[U][NG][NMAT], const uint32_t (&sb)[NG][NMAT],
                       uint4 (&wn)[U][NG][NMAT], uint32_t (&sn)[NG][NMAT]) {
         constexpr int UI = decltype(uc)::value;

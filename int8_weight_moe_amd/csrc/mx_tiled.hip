@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(w
   constexpr int SPG = kMxGroup / KB;               // steps per scale group
   constexpr int ROWB = kMxAct ? 128 : 256;         // bytes of an activation row per step
   constexpr int CPR = ROWB / 16;                   // its 16-byte chunks
-  constexpr int SROWS = kBM < 64 ? 64 : kBM;       // rows of a block's scales in LDS: whole loads of 64
+  static_assert(kBM == 64 || kBM == 128, "row scales: one or two loads of 64 a block");
   constexpr int A_STAGE = kBM * ROWB;
   constexpr int A_INSTR = A_STAGE / 1024 / kWaves; // 1 KiB loads per wave and step
   constexpr int RPI = 1024 / ROWB;                 // rows per load
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(w
   constexpr int HALF = NB / NMAT;                  // of each matrix
   constexpr int CH_TILE = kBN / NMAT;
   __shared__ __attribute__((aligned(1024))) uint8_t As[2][A_STAGE];
-  __shared__ __attribute__((aligned(1024))) uint32_t Ss[2][kMxAct ? kMxGroup * SROWS : 4];
+  __shared__ __attribute__((aligned(1024))) uint32_t Ss[2][kMxAct ? kMxGroup * kBM : 4];
   __shared__ int s_tile;
 
   const int lane = threadIdx.x & 63;
@@ -143,8 +143,8 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(w
   auto issue_s = [&](int group, int buf) {
     if constexpr (kMxAct) {
       const uint32_t blk = (uint32_t)min(group * kMxGroup + wave, n - 1);
-      dma4(a.a_s, s_off[0] + blk * 4u, lds_addr(&Ss[buf][wave * SROWS]));
-      if constexpr (kBM > 64) dma4(a.a_s, s_off[1] + blk * 4u, lds_addr(&Ss[buf][wave * SROWS + 64]));
+      dma4(a.a_s, s_off[0] + blk * 4u, lds_addr(&Ss[buf][wave * kBM]));
+      if constexpr (kBM > 64) dma4(a.a_s, s_off[1] + blk * 4u, lds_addr(&Ss[buf][wave * kBM + 64]));
     }
   };
   auto load_b = [&](int step, uint4 (&b)[NB][KB]) {
@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(w
     issue_a(0, 0, mbc);
     load_b(0, b[0]);
     load_sb(0, sb_next);
-    // one 128-column block of a step: kJ is its place in the scale group
+    // one 128-column block of a step: J is its place in the scale group
     auto block = [&](auto jc, int buf, int gbuf, const uint4 (&w)[NB][KB]) {
       constexpr int J = decltype(jc)::value;
       constexpr int K = J % KB;
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(w
           for (int i = 0; i < HB; ++i) {
             const int r = (h + i) * 16 + li;
             xf[i] = *reinterpret_cast<const uint4*>(&As[buf][r * ROWB + (((4 * K + lg) ^ (r % CPR)) * 16)]);
-            xs[i] = reinterpret_cast<const uint8_t*>(&Ss[gbuf][J * SROWS + r])[lg];
+            xs[i] = reinterpret_cast<const uint8_t*>(&Ss[gbuf][J * kBM + r])[lg];
           }
 #pragma unroll
           for (int j = 0; j < NB; ++j)
