@@ -609,6 +609,8 @@ def moe_combine_post(y_rows: torch.Tensor, slot_to_row: torch.Tensor, topk_w: to
     lib = _lib_handle()
     T, K = topk_w.shape
     d = y_rows.shape[1]
+    if slot_to_row.numel() != T * K:
+        raise ValueError(f"slot_to_row has {slot_to_row.numel()} entries, not {T * K}")
     dt = residual.dtype
     shape = make_shape(T, d, 64, max(K, 1), K, dt, torch.float32)
     p = _post(T, d, dt, weight, gate, gate_tokens, residual_scale, block_scale, eps, next_weight, next_eps)
@@ -616,7 +618,7 @@ def moe_combine_post(y_rows: torch.Tensor, slot_to_row: torch.Tensor, topk_w: to
     out, nxt = _post_outputs(residual, out, next_weight, next_out)
     _lib.check(lib.moe_combine_post(
         ctypes.byref(shape), ctypes.byref(p), _arg("y_rows", y_rows, torch.float32, (T * K, d)),
-        _arg("slot_to_row", slot_to_row.view(-1), torch.int32, (T * K,)), _arg("topk_w", topk_w, torch.float32), res,
+        _arg("slot_to_row", slot_to_row, torch.int32), _arg("topk_w", topk_w, torch.float32), res,
         _arg("out", out, dt, (T, d)), _arg("next_out", nxt, dt, (T, d)), _stream()))
     return out, nxt
 

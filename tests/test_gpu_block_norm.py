@@ -182,3 +182,25 @@ def test_norm_on_a_side_stream_and_empty():
     assert m.moe_norm_pre(e, w).shape == (0, 512)
     out, nxt = m.moe_norm_post(e, e, weight=w, next_weight=w)
     assert out.shape == nxt.shape == (0, 512)
+
+
+def test_refusals_on_the_device():
+    y, w = torch.randn(4, 128, device="cuda"), torch.ones(128, device="cuda")
+    rows, gw = torch.randn(8, 128, device="cuda"), torch.ones(4, 2, device="cuda")
+    s2r = torch.arange(8, dtype=torch.int32, device="cuda")
+    ok = m.moe_combine_post(rows, s2r.view(4, 2), gw, y, weight=w)[0]
+    assert torch.equal(ok, m.moe_combine_post(rows, s2r, gw, y, weight=w)[0])
+    with pytest.raises(ValueError, match="slot_to_row"):
+        m.moe_combine_post(rows, s2r[:7], gw, y, weight=w)
+    with pytest.raises(TypeError, match="residual"):
+        m.moe_norm_post(y, y.to(torch.bfloat16), weight=w)
+    with pytest.raises(ValueError, match="gate has shape"):
+        m.moe_norm_post(y, y, weight=w, gate=torch.ones(2, 128, device="cuda"), gate_tokens=1)
+    with pytest.raises(ValueError, match="contiguous"):
+        m.moe_norm_pre(torch.randn(128, 64, device="cuda").t(), torch.ones(128, device="cuda"))
+    with pytest.raises(m.MoeError) as e:
+        m.moe_norm_pre(y, w, eps=-1.0)
+    assert e.value.status == 2
+    with pytest.raises(m.MoeError) as e:
+        m.moe_norm_post(y, y, weight=w, gate=torch.ones(4, 128, device="cuda"), gate_tokens=0)
+    assert e.value.status == 2
