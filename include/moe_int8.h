@@ -120,7 +120,7 @@ enum { MOE_W_INT8 = 0, MOE_W_BF16 = 1, MOE_W_FP8 = 2, MOE_W_MXFP4 = 4 };
 /* expert-FFN schedule: AUTO picks STREAM when at most 64 rows fall on each
  * expert on average (T*K <= 64*E: decode) and TILED otherwise (prefill); with
  * MXFP4 weights the border is 16 rows for the down pass, 8 for the gate/up
- * pass and for products with MXFP4 activations (32 for either with few output
+ * pass and for products with MXFP4 activations (32 and 20 with few output
  * channels over all experts).
  * Both give results within the same tolerance of the exact layer; they are
  * not bit-identical to each other. Each is deterministic. */

@@ -104,9 +104,12 @@ constexpr long kStreamRowsPerExpert = 64;
 constexpr long kMxStreamRowsPerExpert = 16;
 constexpr long kMxWideStreamRowsPerExpert = 8;
 // With few channels in all, tiles leave most of the GPU idle and the streaming
-// kernel's split reductions do not: both borders are 32 rows then. (gate/up, d
-// 4096, f 1024, E 4, 20 rows 11.9 / 21.5; down, f 4096, d 1024, E 4, 20 rows 10.5 / 22.0.)
+// kernel's split reductions do not: the borders are 32 and 20 rows then. Measured
+// (rows an expert): down, f 4096, d 4096, E 4 at 12 rows 13.6 / 28.9, at 32 26.6 / 32.2; f 8192,
+// d 2048, E 8 at 32 47.9 / 62.6; gate/up, d 4096, f 4096, E 4 at 20 27.7 / 30.7, at 32 48.6 /
+// 33.9; d 8192, f 2048, E 8 at 20 51.3 / 57.5; both in MXFP4 there at 20 29.3 / 30.2, at 32 51.6 / 31.9.
 constexpr long kMxFewTilesRowsPerExpert = 32;
+constexpr long kMxFewTilesWideRowsPerExpert = 20;
 constexpr long kMxFewTilesChannels = 16384;
 
 moe_status check_shape(const moe_shape* s) {
@@ -318,9 +321,12 @@ moe::MxArgs mx_down(const moe::FfnArgs& a) {
 // One product with MXFP4 weights; `call` and `what` name it in the log and in an error.
 moe_status run_mx(const char* call, const char* what, const moe_shape* s, const moe::MxArgs& m, hipStream_t stream) {
   bool by_stream = use_stream(s);
-  if (s->ffn_path == MOE_PATH_AUTO)
-    by_stream = m.S <= (m.a_s || m.w1 ? kMxWideStreamRowsPerExpert : kMxStreamRowsPerExpert) * m.E ||
-                (m.S <= kMxFewTilesRowsPerExpert * m.E && (long)m.E * m.N <= kMxFewTilesChannels);
+  if (s->ffn_path == MOE_PATH_AUTO) {
+    const bool wide = m.a_s || m.w1, few = (long)m.E * m.N <= kMxFewTilesChannels;
+    const long rows = few ? (wide ? kMxFewTilesWideRowsPerExpert : kMxFewTilesRowsPerExpert)
+                          : (wide ? kMxWideStreamRowsPerExpert : kMxStreamRowsPerExpert);
+    by_stream = m.S <= rows * m.E;
+  }
   // codes past the tiled kernel's 32-bit offsets (bf16 activations: refused by check_ffn)
   if (!moe::mx_tiled_offsets_fit(m)) by_stream = true;
   if (log_on())
