@@ -113,7 +113,9 @@ enum { MOE_F32 = 0, MOE_BF16 = 1 };
  *               Codes become bf16 exactly, scale included, so the products are
  *               exact and the sums fp32 as for the others. bf16 activations
  *               (else MOE_ERR_UNSUPPORTED), d and f multiples of 128 (else
- *               MOE_ERR_SHAPE); TILED as for bf16 and fp8.
+ *               MOE_ERR_SHAPE). A pass that reads 4 GiB or more of x (gate/up)
+ *               or h (down) takes the STREAM schedule on AUTO; asked for TILED
+ *               it is refused with MOE_ERR_UNSUPPORTED.
  * Code 3 is not assigned. */
 enum { MOE_W_INT8 = 0, MOE_W_BF16 = 1, MOE_W_FP8 = 2, MOE_W_MXFP4 = 4 };
 

@@ -193,15 +193,27 @@ bool use_stream(const moe_shape* s) {
   return (long)s->T * s->K <= kStreamRowsPerExpert * s->E;
 }
 
+// The passes of the expert FFN that a call runs.
+enum { kGateUpPass = 1, kDownPass = 2, kBothPasses = 3 };
+
 // What the FFN kernels accept beyond check_shape: the bf16 and fp8 weight
 // encodings run with bf16 activations, and their tiled schedule addresses
-// with 32-bit offsets.
-moe_status check_ffn(const moe_shape* s) {
+// with 32-bit offsets. MXFP4 weights: only the rows that a pass reads (x, h) are
+// addressed so; AUTO streams a pass whose rows do not fit (run_mx).
+moe_status check_ffn(const moe_shape* s, int passes) {
   if (s->weight_fmt == MOE_W_INT8) return MOE_OK;
   if (s->act_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "weight_fmt=%d needs bf16 activations", s->weight_fmt);
-  if (s->weight_fmt == MOE_W_MXFP4 && (s->d % 128 || s->f % 128))
-    return fail(MOE_ERR_SHAPE, "MXFP4 weights need d=%d and f=%d to be multiples of 128", s->d, s->f);
+  if (s->weight_fmt == MOE_W_MXFP4) {
+    if (s->d % 128 || s->f % 128)
+      return fail(MOE_ERR_SHAPE, "MXFP4 weights need d=%d and f=%d to be multiples of 128", s->d, s->f);
+    if (s->ffn_path != MOE_PATH_TILED) return MOE_OK;
+    if ((passes & kGateUpPass) && !moe::mx_tiled_offsets_fit(s->T, s->d, false))
+      return fail(MOE_ERR_UNSUPPORTED, "x is too large for the tiled schedule");
+    if ((passes & kDownPass) && !moe::mx_tiled_offsets_fit((long)s->T * s->K, s->f, false))
+      return fail(MOE_ERR_UNSUPPORTED, "h is too large for the tiled schedule");
+    return MOE_OK;
+  }
   const int wbytes = s->weight_fmt == MOE_W_BF16 ? 2 : 1;
   if (!use_stream(s) && !moe::dma_offsets_fit(s->T, (long)s->T * s->K, s->d, s->f, wbytes))
     return fail(MOE_ERR_UNSUPPORTED, "weight_fmt=%d: tensors too large for the tiled schedule", s->weight_fmt);
@@ -327,8 +339,8 @@ moe_status run_mx(const char* call, const char* what, const moe_shape* s, const 
                           : (wide ? kMxWideStreamRowsPerExpert : kMxStreamRowsPerExpert);
     by_stream = m.S <= rows * m.E;
   }
-  // codes past the tiled kernel's 32-bit offsets (bf16 activations: refused by check_ffn)
-  if (!moe::mx_tiled_offsets_fit(m)) by_stream = true;
+  // rows past the tiled kernel's 32-bit offsets (on TILED, bf16 rows are refused by check_ffn)
+  if (!moe::mx_tiled_offsets_fit(m.a_rows, m.Kd, m.a_s != nullptr)) by_stream = true;
   if (log_on())
     fprintf(stderr, "[moe] %s %s: rows=%d reduction=%d channels=%d E=%d act=%s weights=mxfp4 out=%s; %s schedule%s\n",
             call, what, m.S, m.Kd, m.N, m.E, m.a_s ? "mxfp4" : "bf16", m.out_bf16 ? "bf16" : "f32",
@@ -498,7 +510,7 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
                        moe::NormArgs* post = nullptr) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
-  st = check_ffn(s);
+  st = check_ffn(s, kBothPasses);
   if (st != MOE_OK) return st;
   if (s->T == 0) return MOE_OK;   // nothing is read or written
   REQUIRE_PTR(x);
@@ -648,7 +660,7 @@ moe_status moe_expert_ffn(const moe_shape* s, const void* x, const int32_t* expe
                           float* y_rows, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
-  st = check_ffn(s);
+  st = check_ffn(s, kBothPasses);
   if (st != MOE_OK) return st;
   if (s->T == 0) return MOE_OK;   // nothing is read or written
   REQUIRE_PTR(x);
@@ -686,7 +698,7 @@ moe_status moe_expert_gate_up(const moe_shape* s, const void* x, const int32_t* 
                               size_t workspace_bytes, hipStream_t stream) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
-  st = check_ffn(s);
+  st = check_ffn(s, kGateUpPass);
   if (st != MOE_OK) return st;
   if (s->T == 0) return MOE_OK;   // nothing is read or written
   REQUIRE_PTR(x);
@@ -715,7 +727,7 @@ moe_status moe_expert_down(const moe_shape* s, const void* h, const int32_t* exp
                            hipStream_t stream) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
-  st = check_ffn(s);
+  st = check_ffn(s, kDownPass);
   if (st != MOE_OK) return st;
   if (s->T == 0) return MOE_OK;   // nothing is read or written
   REQUIRE_PTR(h);
@@ -814,7 +826,7 @@ moe_status moe_mlp_forward(const moe_shape* s, const void* x, const void* w_gate
                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
-  st = check_ffn(s);
+  st = check_ffn(s, kBothPasses);
   if (st != MOE_OK) return st;
   if (s->E != 1 || s->K != 1) return fail(MOE_ERR_SHAPE, "the dense MLP needs E = K = 1 (E=%d, K=%d)", s->E, s->K);
   if (s->T == 0) return MOE_OK;   // nothing is read or written
@@ -1129,7 +1141,7 @@ moe_status moe_block_forward(const moe_shape* s, const void* residual, const voi
                              float* topk_w_out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
-  if ((st = check_ffn(s)) != MOE_OK) return st;
+  if ((st = check_ffn(s, kBothPasses)) != MOE_OK) return st;
   if ((st = check_post(s, post, residual, out, next)) != MOE_OK) return st;
   if (pre_weight && (st = check_eps("pre_eps", pre_eps)) != MOE_OK) return st;
   if (s->T == 0) return MOE_OK;   // nothing is read or written

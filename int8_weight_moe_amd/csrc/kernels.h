@@ -108,8 +108,9 @@ struct MxArgs {
   int E, N, Kd, S;
 };
 hipError_t launch_mx_stream(const MxArgs& a, hipStream_t stream);
-// Needs the rows of a within 32-bit byte offsets.
-bool mx_tiled_offsets_fit(const MxArgs& a);
+// Whether rows of `cols` numbers (MXFP4 codes, or bf16) lie within 32-bit byte
+// offsets, as launch_mx_tiled needs the rows of a to.
+bool mx_tiled_offsets_fit(long rows, int cols, bool mx);
 hipError_t launch_mx_tiled(const MxArgs& a, hipStream_t stream);
 
 // Norms around the layer (block_norm.hip).

@@ -361,8 +361,8 @@ hipError_t launch_tiled(const MxArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-bool mx_tiled_offsets_fit(const MxArgs& a) {
-  return (uint64_t)a.a_rows * (uint64_t)a.Kd * (a.a_s ? 1 : 4) < (1ull << 33);
+bool mx_tiled_offsets_fit(long rows, int cols, bool mx) {
+  return (uint64_t)rows * (uint64_t)cols * (mx ? 1 : 4) < (1ull << 33);
 }
 
 hipError_t launch_mx_tiled(const MxArgs& a, hipStream_t stream) {
