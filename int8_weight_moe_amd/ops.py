@@ -84,6 +84,43 @@ def _check_width(name: str, have: int, want: int) -> None:
         raise ValueError(f"{name} has {have} columns, the experts' weights {want}")
 
 
+# type of the codes; codes a byte; columns a scale covers (0: the row)
+_CODES = {MOE_W_INT8: (torch.int8, 1, 0), MOE_W_FP8: (torch.uint8, 1, 0), MOE_W_BF16: (torch.bfloat16, 1, 0),
+          MOE_W_MXFP4: (torch.uint8, 2, 32)}
+
+
+def _weights(experts: Int8Experts, *names: str):
+    """Pointers of the codes, then of the scales, of these matrices ("gate", "up", "down"): every tensor has
+    the type and shape that the experts' sizes ask for, and is contiguous on the current device."""
+    E, f, d, fmt = experts.E, experts.f, experts.d, experts.fmt
+    if fmt not in _CODES:
+        raise ValueError(f"unknown weight encoding {fmt}")
+    code, per_byte, block = _CODES[fmt]
+    scale = code if block else experts.scale_dtype
+    ts = []
+    for name in names:
+        out, cols = (d, f) if name == "down" else (f, d)
+        ts.append(("q_" + name, getattr(experts, "q_" + name), code, (E, out, cols // per_byte)))
+    if fmt != MOE_W_BF16:
+        for name in names:
+            out, cols = (d, f) if name == "down" else (f, d)
+            ts.append(("s_" + name, getattr(experts, "s_" + name), scale,
+                       (E, out, cols // block) if block else (E, out)))
+    for name, t, dtype, shape in ts:
+        if t is None or t.dtype != dtype or t.shape != shape:
+            have = None if t is None else f"{t.dtype} {tuple(t.shape)}"
+            raise ValueError(f"the experts' {name} is {have}, not {dtype} {shape}")
+    ptrs = [_arg(name, t, None) for name, t, _, _ in ts]
+    return ptrs if fmt != MOE_W_BF16 else ptrs + [None] * len(names)
+
+
+def _ffn_weights(experts: Int8Experts, *names: str):
+    """_weights for MXFP4; the pointers as they are for the other encodings."""
+    if experts.fmt == MOE_W_MXFP4:
+        return _weights(experts, *names)
+    return [_ptr(getattr(experts, k + name)) for k in ("q_", "s_") for name in names]
+
+
 def make_shape(T: int, d: int, f: int, E: int, K: int, act: torch.dtype, scale: torch.dtype,
                path: int = MOE_PATH_AUTO, fmt: int = MOE_W_INT8) -> MoeShape:
     return MoeShape(T, d, f, E, K, _dtype_code(act), _dtype_code(scale), path, fmt)
@@ -147,9 +184,9 @@ def moe_expert_ffn(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_slots: 
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
     _lib.check(lib.moe_expert_ffn(
-        ctypes.byref(shape), _ptr(x), _ptr(expert_offsets), _ptr(sorted_slots), _ptr(experts.q_gate),
-        _ptr(experts.q_up), _ptr(experts.q_down), _ptr(experts.s_gate), _ptr(experts.s_up),
-        _ptr(experts.s_down), _ptr(y_rows), _ptr(workspace), ctypes.c_size_t(workspace.numel()), _stream()))
+        ctypes.byref(shape), _ptr(x), _ptr(expert_offsets), _ptr(sorted_slots),
+        *_ffn_weights(experts, "gate", "up", "down"), _ptr(y_rows), _ptr(workspace),
+        ctypes.c_size_t(workspace.numel()), _stream()))
     return y_rows
 
 
@@ -179,8 +216,8 @@ def moe_expert_gate_up(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_slo
     if need:
         ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=x.device)
     _lib.check(lib.moe_expert_gate_up(
-        ctypes.byref(shape), _ptr(x), _ptr(expert_offsets), _ptr(sorted_slots), _ptr(experts.q_gate),
-        _ptr(experts.q_up), _ptr(experts.s_gate), _ptr(experts.s_up), _ptr(h), _ptr(ws),
+        ctypes.byref(shape), _ptr(x), _ptr(expert_offsets), _ptr(sorted_slots), *_ffn_weights(experts, "gate", "up"),
+        _ptr(h), _ptr(ws),
         ctypes.c_size_t(ws.numel() if ws is not None else 0), _stream()))
     return h
 
@@ -211,8 +248,8 @@ def moe_expert_down(h: torch.Tensor, expert_offsets: torch.Tensor, experts: Int8
     need = down_workspace_size(shape) if split_workspace else 0
     if need:
         ws = workspace if workspace is not None else torch.empty(need, dtype=torch.uint8, device=h.device)
-    _lib.check(lib.moe_expert_down(ctypes.byref(shape), _ptr(h), _ptr(expert_offsets), _ptr(experts.q_down),
-                                   _ptr(experts.s_down), _ptr(y_rows), _ptr(ws),
+    _lib.check(lib.moe_expert_down(ctypes.byref(shape), _ptr(h), _ptr(expert_offsets),
+                                   *_ffn_weights(experts, "down"), _ptr(y_rows), _ptr(ws),
                                    ctypes.c_size_t(ws.numel() if ws is not None else 0), _stream()))
     return y_rows
 
@@ -275,8 +312,8 @@ def moe_forward(x: torch.Tensor, router_w: torch.Tensor, bias: Optional[torch.Te
     if workspace is None:
         workspace = torch.empty(max(workspace_size(shape), 256), dtype=torch.uint8, device=dev)
     _lib.check(lib.moe_forward(
-        ctypes.byref(shape), _ptr(x), _ptr(router_w), _ptr(bias), _ptr(experts.q_gate), _ptr(experts.q_up),
-        _ptr(experts.q_down), _ptr(experts.s_gate), _ptr(experts.s_up), _ptr(experts.s_down), _ptr(y), _ptr(ids),
+        ctypes.byref(shape), _ptr(x), _ptr(router_w), _ptr(bias),
+        *_ffn_weights(experts, "gate", "up", "down"), _ptr(y), _ptr(ids),
         _ptr(w), _ptr(workspace), ctypes.c_size_t(workspace.numel()), _stream()))
     return y, ids, w
 
@@ -299,8 +336,8 @@ def moe_forward_noalloc(x: torch.Tensor, router_w: torch.Tensor, bias: Optional[
     if w is None:
         w = torch.empty((T, K), dtype=torch.float32, device=dev)
     _lib.check(lib.moe_forward_noalloc(
-        ctypes.byref(shape), _ptr(x), _ptr(router_w), _ptr(bias), _ptr(experts.q_gate), _ptr(experts.q_up),
-        _ptr(experts.q_down), _ptr(experts.s_gate), _ptr(experts.s_up), _ptr(experts.s_down), _ptr(y), _ptr(ids),
+        ctypes.byref(shape), _ptr(x), _ptr(router_w), _ptr(bias),
+        *_ffn_weights(experts, "gate", "up", "down"), _ptr(y), _ptr(ids),
         _ptr(w), _stream()))
     return y, ids, w
 
@@ -321,8 +358,7 @@ def moe_mlp_forward(x: torch.Tensor, experts: Int8Experts, path: int = MOE_PATH_
         _lib.check(lib.moe_mlp_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
         workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=x.device)
     _lib.check(lib.moe_mlp_forward(
-        ctypes.byref(shape), _ptr(x), _ptr(experts.q_gate), _ptr(experts.q_up), _ptr(experts.q_down),
-        _ptr(experts.s_gate), _ptr(experts.s_up), _ptr(experts.s_down), _ptr(y), _ptr(workspace),
+        ctypes.byref(shape), _ptr(x), *_ffn_weights(experts, "gate", "up", "down"), _ptr(y), _ptr(workspace),
         ctypes.c_size_t(workspace.numel()), _stream()))
     return y
 
@@ -534,6 +570,7 @@ def moe_expert_ffn_mxfp4(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_s
         raise ValueError("the experts are not in MXFP4")
     T, d = x.shape
     _check_width("x", d, experts.d)
+    weights = _weights(experts, "gate", "up", "down")
     shape = make_shape(T, d, experts.f, experts.E, K, x.dtype, experts.scale_dtype, path, experts.fmt)
     n = ctypes.c_size_t(0)
     _lib.check(lib.moe_expert_ffn_mxfp4_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
@@ -543,8 +580,7 @@ def moe_expert_ffn_mxfp4(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_s
     _lib.check(lib.moe_expert_ffn_mxfp4(
         ctypes.byref(shape), _arg("x", x, None),
         _arg("expert_offsets", expert_offsets, torch.int32, (experts.E + 1,)),
-        _arg("sorted_slots", sorted_slots, torch.int32, (T * K,)), _ptr(experts.q_gate), _ptr(experts.q_up),
-        _ptr(experts.q_down), _ptr(experts.s_gate), _ptr(experts.s_up), _ptr(experts.s_down), _ptr(y_rows),
+        _arg("sorted_slots", sorted_slots, torch.int32, (T * K,)), *weights, _ptr(y_rows),
         _arg("workspace", workspace, torch.uint8), ctypes.c_size_t(workspace.numel()), _stream()))
     return y_rows
 
@@ -644,6 +680,7 @@ def moe_block_forward(residual: torch.Tensor, router_w: torch.Tensor, bias: Opti
     T, d = residual.shape
     dt = residual.dtype
     _check_width("residual", d, experts.d)
+    weights = _weights(experts, "gate", "up", "down")
     shape = make_shape(T, d, experts.f, experts.E, K, dt, experts.scale_dtype, path, experts.fmt)
     p = _post(T, d, dt, weight, gate, gate_tokens, residual_scale, block_scale, eps, next_weight, next_eps)
     res = _arg("residual", residual, dt)
@@ -656,8 +693,7 @@ def moe_block_forward(residual: torch.Tensor, router_w: torch.Tensor, bias: Opti
     _lib.check(lib.moe_block_forward(
         ctypes.byref(shape), res, _arg("pre_weight", pre_weight, dt, (d,)), pre_eps, _arg("x", x, dt, (T, d)),
         ctypes.byref(p), _arg("router_w", router_w, dt, (experts.E, d)),
-        _arg("bias", bias, torch.float32, (experts.E,)), _ptr(experts.q_gate), _ptr(experts.q_up),
-        _ptr(experts.q_down), _ptr(experts.s_gate), _ptr(experts.s_up), _ptr(experts.s_down),
-        _arg("out", out, dt, (T, d)), _arg("next_out", nxt, dt, (T, d)), _ptr(ids), _ptr(w),
+        _arg("bias", bias, torch.float32, (experts.E,)), *weights, _arg("out", out, dt, (T, d)),
+        _arg("next_out", nxt, dt, (T, d)), _ptr(ids), _ptr(w),
         _arg("workspace", workspace, torch.uint8), ctypes.c_size_t(workspace.numel()), _stream()))
     return out, nxt, ids, w

@@ -1,0 +1,78 @@
+"""The binding's checks of the MXFP4 and block calls (CPU: each call is refused before it reaches the library)."""
+import dataclasses
+
+import pytest
+import torch
+
+import int8_weight_moe_amd as m
+from int8_weight_moe_amd import MOE_W_BF16, MOE_W_FP8, MOE_W_INT8, MOE_W_MXFP4, Int8Experts
+
+E, F, D = 3, 256, 128
+
+
+def _experts(fmt):
+    z = lambda dt, *shape: torch.zeros(*shape, dtype=dt)
+    dims = dict(gate=(F, D), up=(F, D), down=(D, F))
+    if fmt == MOE_W_MXFP4:
+        t = {"q_" + k: z(torch.uint8, E, r, c // 2) for k, (r, c) in dims.items()}
+        t.update({"s_" + k: z(torch.uint8, E, r, c // 32) for k, (r, c) in dims.items()})
+    else:
+        code = {MOE_W_INT8: torch.int8, MOE_W_FP8: torch.uint8, MOE_W_BF16: torch.bfloat16}[fmt]
+        t = {"q_" + k: z(code, E, r, c) for k, (r, c) in dims.items()}
+        t.update({"s_" + k: None if fmt == MOE_W_BF16 else z(torch.bfloat16, E, r) for k, (r, c) in dims.items()})
+    return Int8Experts(**t, fmt=fmt)
+
+
+def _calls(ex):
+    x = torch.zeros(4, D, dtype=torch.bfloat16)
+    off, srt = torch.zeros(E + 1, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    wr = torch.zeros(E, D, dtype=torch.bfloat16)
+    yield lambda: m.moe_block_forward(x, wr, None, ex, 2, pre_weight=x[0])
+    if ex.fmt != MOE_W_MXFP4:
+        return
+    yield lambda: m.moe_expert_ffn_mxfp4(x, off, srt, ex, 2)
+    yield lambda: m.moe_expert_ffn(x, off, srt, ex, 2)
+    yield lambda: m.moe_forward(x, wr, None, ex, 2)
+    yield lambda: m.moe_forward_noalloc(x, wr, None, ex, 2)
+
+
+@pytest.mark.parametrize("fmt", [MOE_W_INT8, MOE_W_FP8, MOE_W_BF16, MOE_W_MXFP4])
+def test_expert_tensors_are_checked_against_each_other(fmt):
+    """One tensor too short, or of another type, is named before any pointer is taken (here: before the device check)."""
+    good = _experts(fmt)
+    names = ["q_up", "q_down"] + ([] if fmt == MOE_W_BF16 else ["s_up", "s_down"])
+    for name in names:
+        t = getattr(good, name)
+        for bad in (t[:, :-16].contiguous(), t[:-1].contiguous(), t.to(torch.float32), None):
+            for call in _calls(dataclasses.replace(good, **{name: bad})):
+                with pytest.raises(ValueError, match=f"the experts' {name} is"):
+                    call()
+    for call in _calls(good):
+        with pytest.raises(ValueError, match="not on the current HIP device"):
+            call()
+
+
+def test_staged_passes_check_the_matrices_they_read():
+    ex = _experts(MOE_W_MXFP4)
+    x = torch.zeros(4, D, dtype=torch.bfloat16)
+    off, srt = torch.zeros(E + 1, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    for name in ("q_up", "s_gate", "s_up"):
+        with pytest.raises(ValueError, match=f"the experts' {name} is"):
+            m.moe_expert_gate_up(x, off, srt, dataclasses.replace(ex, **{name: getattr(ex, name)[:, :, :-1].contiguous()}), 2)
+    for name in ("q_down", "s_down"):
+        with pytest.raises(ValueError, match=f"the experts' {name} is"):
+            m.moe_expert_down(torch.zeros(8, F, dtype=torch.bfloat16), off,
+                              dataclasses.replace(ex, **{name: getattr(ex, name)[:-1].contiguous()}), 4, 2)
+    # a matrix that a pass does not read may be missing
+    with pytest.raises(ValueError, match="not on the current HIP device"):
+        m.moe_expert_gate_up(x, off, srt, dataclasses.replace(ex, q_down=None, s_down=None), 2)
+    one = Int8Experts(*(getattr(ex, k)[:1] for k in ("q_gate", "q_up")), ex.q_down[:1, :-16],
+                      *(getattr(ex, k)[:1] for k in ("s_gate", "s_up", "s_down")), fmt=MOE_W_MXFP4)
+    with pytest.raises(ValueError, match="the experts' q_down is"):
+        m.moe_mlp_forward(x, one)
+
+
+def test_down_takes_experts_without_their_gate_and_up():
+    ex = dataclasses.replace(_experts(MOE_W_MXFP4), q_up=None, s_up=None)
+    with pytest.raises(ValueError, match="not on the current HIP device"):
+        m.moe_expert_down(torch.zeros(8, F, dtype=torch.bfloat16), torch.zeros(E + 1, dtype=torch.int32), ex, 4, 2)
