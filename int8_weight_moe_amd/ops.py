@@ -84,6 +84,13 @@ def _check_width(name: str, have: int, want: int) -> None:
         raise ValueError(f"{name} has {have} columns, the experts' weights {want}")
 
 
+def _check_sizes(*sizes: int) -> None:
+    """The library takes sizes of 32 bits; a larger one would be cut, not refused, on the way to it."""
+    for v in sizes:
+        if v >> 31 > 0:
+            raise ValueError(f"size {v} is past 2^31")
+
+
 # type of the codes; codes a byte; columns a scale covers (0: the row)
 _CODES = {MOE_W_INT8: (torch.int8, 1, 0), MOE_W_FP8: (torch.uint8, 1, 0), MOE_W_BF16: (torch.bfloat16, 1, 0),
           MOE_W_MXFP4: (torch.uint8, 2, 32)}
@@ -123,6 +130,7 @@ def _ffn_weights(experts: Int8Experts, *names: str):
 
 def make_shape(T: int, d: int, f: int, E: int, K: int, act: torch.dtype, scale: torch.dtype,
                path: int = MOE_PATH_AUTO, fmt: int = MOE_W_INT8) -> MoeShape:
+    _check_sizes(T, d, f, E, K)
     return MoeShape(T, d, f, E, K, _dtype_code(act), _dtype_code(scale), path, fmt)
 
 
@@ -478,6 +486,7 @@ def moe_quantize_mxfp4(w: torch.Tensor, tiled: bool = False):
     if w.dim() < 1 or w.shape[-1] % 32:
         raise ValueError(f"the last dimension of {tuple(w.shape)} is not a multiple of 32")
     cols = w.shape[-1]
+    _check_sizes(cols)
     rows = w.numel() // cols if cols else 0
     q = torch.empty((*w.shape[:-1], cols // 2), dtype=torch.uint8, device=w.device)
     s = torch.empty((*w.shape[:-1], cols // 32), dtype=torch.uint8, device=w.device)
@@ -490,6 +499,7 @@ def _mx_shape(q: torch.Tensor, s: torch.Tensor):
     cols = q.shape[-1] * 2
     if q.dim() < 1 or cols % 32 or tuple(s.shape) != (*q.shape[:-1], cols // 32):
         raise ValueError(f"codes {tuple(q.shape)} and scales {tuple(s.shape)} do not belong together")
+    _check_sizes(cols)
     return (q.numel() // q.shape[-1] if cols else 0), cols
 
 
@@ -548,6 +558,7 @@ def moe_grouped_mm_mxfp4(a_q: torch.Tensor, a_s: torch.Tensor, expert_offsets: t
         raise ValueError("K is the slots per row of sorted_slots: 1 without it")
     if (w2_q is None) != (w2_s is None):
         raise ValueError("w2_q and w2_s are given together")
+    _check_sizes(rows, d, f, E, K)
     shape = MoeShape(rows, d, f, E, K, _dtype_code(out_dtype), MOE_BF16, path, MOE_W_MXFP4)
     if out is None:
         out = torch.empty((rows * K, f), dtype=out_dtype, device=a_q.device)
@@ -600,6 +611,8 @@ def moe_norm_pre(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
 
 def _post(T: int, d: int, dtype: torch.dtype, weight, gate, gate_tokens: int, residual_scale: float,
           block_scale: float, eps: float, next_weight, next_eps: Optional[float]) -> MoePost:
+    # past T all tokens share one row, whatever its size; below 1 the library refuses it
+    gate_tokens = min(max(gate_tokens, 0), 0x7fffffff)
     rows = (-(-T // gate_tokens), d) if gate_tokens >= 1 else None
     return MoePost(_arg("weight", weight, dtype, (d,)), _arg("gate", gate, dtype, rows),
                    _arg("next_weight", next_weight, dtype, (d,)), gate_tokens, residual_scale, block_scale, eps,

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import int8_weight_moe_amd as m
+from int8_weight_moe_amd import ops
 from int8_weight_moe_amd import MOE_W_BF16, MOE_W_FP8, MOE_W_INT8, MOE_W_MXFP4, Int8Experts
 
 E, F, D = 3, 256, 128
@@ -76,3 +77,25 @@ def test_down_takes_experts_without_their_gate_and_up():
     ex = dataclasses.replace(_experts(MOE_W_MXFP4), q_up=None, s_up=None)
     with pytest.raises(ValueError, match="not on the current HIP device"):
         m.moe_expert_down(torch.zeros(8, F, dtype=torch.bfloat16), torch.zeros(E + 1, dtype=torch.int32), ex, 4, 2)
+
+
+def test_sizes_past_32_bits_are_not_cut():
+    """A size whose low 32 bits are a small valid one is refused (tensors without memory stand for the large ones)."""
+    big = (1 << 32) + 128
+    w = torch.empty(1, big, dtype=torch.bfloat16, device="meta")
+    q, s = torch.empty(1, big // 2, dtype=torch.uint8, device="meta"), torch.empty(1, big // 32, dtype=torch.uint8, device="meta")
+    off = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: m.moe_quantize_mxfp4(w), lambda: m.moe_dequantize_mxfp4(q, s, torch.bfloat16),
+                 lambda: m.moe_pack_mxfp4(q, s), lambda: m.moe_norm_pre(w, w[0]), lambda: m.moe_norm_post(w, w),
+                 lambda: m.moe_grouped_mm_mxfp4(q, s, off, q[None], s[None], torch.float32),
+                 lambda: m.moe_grouped_mm_mxfp4(q[:, :64], s[:, :4], off, q[None, :, :64], s[None, :, :4],
+                                                torch.float32, sorted_slots=off, K=(1 << 32) + 1)):
+        with pytest.raises(ValueError, match="past 2\\^31"):
+            call()
+
+
+@pytest.mark.parametrize("gate_tokens,kept", [(1, 1), (7, 7), ((1 << 32) + 1, 0x7fffffff), (1 << 31, 0x7fffffff),
+                                              (0, 0), (-1, 0), (-(1 << 32) + 1, 0)])
+def test_gate_tokens_past_32_bits(gate_tokens, kept):
+    """Past every token it is the same as T; below 1 it reaches the library as a value that it refuses."""
+    assert ops._post(5, 64, torch.float32, None, None, gate_tokens, 1.0, 1.0, 1e-6, None, None).gate_tokens == kept
