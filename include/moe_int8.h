@@ -429,7 +429,8 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* shape, const void* x, const int
  * the token's finite elements become 0).
  *
  * Before the layer: n = rms(x) * weight.
- *   x, n [T, d], weight [d], all act_dtype; n may be x. eps >= 0, finite. */
+ *   x, n [T, d], weight [d], all act_dtype; n may be x, and not overlap it
+ *   otherwise (MOE_ERR_UNSUPPORTED). eps >= 0, finite. */
 moe_status moe_norm_pre(const moe_shape* shape, const void* x, const void* weight, float eps, void* n,
                         hipStream_t stream);
 
@@ -448,7 +449,8 @@ typedef struct moe_post {
 } moe_post;
 
 /* y [T, d], residual [T, d], out [T, d], next [T, d] (NULL without next_weight),
- * all act_dtype; out may be residual or y, next may not overlap the others. */
+ * all act_dtype; out may be residual or y, next may be residual or y but not out;
+ * other overlaps are refused (MOE_ERR_UNSUPPORTED). */
 moe_status moe_norm_post(const moe_shape* shape, const moe_post* post, const void* y, const void* residual, void* out,
                          void* next, hipStream_t stream);
 

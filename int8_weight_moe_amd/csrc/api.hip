@@ -420,6 +420,13 @@ moe_status check_eps(const char* what, float eps) {
   return MOE_OK;
 }
 
+// Whether two [T, d] act_dtype arrays share memory without being the same one.
+bool overlap(const moe_shape* s, const void* a, const void* b) {
+  const uintptr_t u = reinterpret_cast<uintptr_t>(a), v = reinterpret_cast<uintptr_t>(b);
+  const uintptr_t bytes = (uintptr_t)s->T * s->d * (s->act_dtype == MOE_BF16 ? 2 : 4);
+  return a && b && u != v && (u < v ? v - u : u - v) < bytes;
+}
+
 moe_status check_post(const moe_shape* s, const moe_post* p, const void* residual, const void* out, const void* next) {
   if (!p) return fail(MOE_ERR_NULL, "post is NULL");
   moe_status st;
@@ -432,7 +439,11 @@ moe_status check_post(const moe_shape* s, const moe_post* p, const void* residua
   if (!aligned16(p->next_weight)) return fail(MOE_ERR_ALIGN, "next_weight is not 16-byte aligned");
   REQUIRE_PTR(residual);
   REQUIRE_PTR(out);
-  if (p->next_weight) REQUIRE_PTR(next);
+  if (overlap(s, out, residual)) return fail(MOE_ERR_UNSUPPORTED, "out overlaps residual and is not residual");
+  if (!p->next_weight) return MOE_OK;
+  REQUIRE_PTR(next);
+  if (next == out || overlap(s, next, out)) return fail(MOE_ERR_UNSUPPORTED, "next overlaps out");
+  if (overlap(s, next, residual)) return fail(MOE_ERR_UNSUPPORTED, "next overlaps residual");
   return MOE_OK;
 }
 
@@ -1080,6 +1091,7 @@ moe_status moe_norm_pre(const moe_shape* s, const void* x, const void* weight, f
   REQUIRE_PTR(x);
   REQUIRE_PTR(weight);
   REQUIRE_PTR(n);
+  if (overlap(s, n, x)) return fail(MOE_ERR_UNSUPPORTED, "n overlaps x and is not x");
   moe::NormArgs a = {};
   a.act_bf16 = s->act_dtype == MOE_BF16;
   a.x = x;
@@ -1100,6 +1112,8 @@ moe_status moe_norm_post(const moe_shape* s, const moe_post* post, const void* y
   if ((st = check_post(s, post, residual, out, next)) != MOE_OK) return st;
   if (s->T == 0) return MOE_OK;   // nothing is read or written
   REQUIRE_PTR(y);
+  if (overlap(s, out, y)) return fail(MOE_ERR_UNSUPPORTED, "out overlaps y and is not y");
+  if (post->next_weight && overlap(s, next, y)) return fail(MOE_ERR_UNSUPPORTED, "next overlaps y");
   moe::NormArgs a = post_args(s, post, residual, out, next);
   a.x = y;
   const hipError_t e = moe::launch_block_norm(a, stream);

@@ -7,7 +7,7 @@ import ctypes
 import pytest
 
 from int8_weight_moe_amd import _lib
-from tests.test_abi_mxfp4 import A, BIG, NULL, UNSUPPORTED, _shape
+from tests.test_abi_mxfp4 import A, B, BIG, NULL, UNSUPPORTED, _post, _shape
 
 
 @pytest.fixture(scope="module")
@@ -54,3 +54,30 @@ def test_rows_past_4_gib_are_streamed_not_refused(lib):
     # the int8 comparators keep their limits
     for fmt in (1, 2):
         assert _gate_up(lib, _shape(weight_fmt=fmt, **big_h)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("act,size", [(1, 32 * 256 * 2), (0, 32 * 256 * 4)])
+def test_norm_outputs_that_overlap_are_refused(lib, act, size):
+    """next over out loses out; arrays a few rows apart are read after they are written."""
+    s = _shape(weight_fmt=0, act_dtype=act)
+    at = lambda n: ctypes.c_void_p(0x10000 + n)
+    nxt = _post(next_weight=A)
+    far = ctypes.c_void_p(0x40000)
+    for d in (16, 512, size - 16):
+        assert lib.moe_norm_pre(s, at(d), A, 1e-6, at(0), None) == UNSUPPORTED
+        assert lib.moe_norm_pre(s, at(0), A, 1e-6, at(d), None) == UNSUPPORTED
+        assert lib.moe_norm_post(s, nxt, far, far, at(0), at(d), None) == UNSUPPORTED       # next, out
+        assert lib.moe_norm_post(s, nxt, far, at(d), at(0), far, None) == UNSUPPORTED       # out, residual
+        assert lib.moe_norm_post(s, nxt, far, at(d), far, at(0), None) == UNSUPPORTED       # next, residual
+        assert lib.moe_norm_post(s, nxt, at(0), far, far, at(d), None) == UNSUPPORTED       # next, y
+        assert lib.moe_norm_post(s, _post(), at(0), far, at(d), None, None) == UNSUPPORTED  # out, y
+        assert lib.moe_combine_post(s, nxt, A, A, A, far, at(0), at(d), None) == UNSUPPORTED
+    assert lib.moe_norm_post(s, nxt, far, far, A, A, None) == UNSUPPORTED
+    assert lib.moe_combine_post(s, nxt, A, A, A, far, B, B, None) == UNSUPPORTED
+    blk = _shape(act_dtype=1)
+    assert lib.moe_block_forward(blk, far, A, 1e-6, None, nxt, A, None, A, A, A, A, A, A, B, B, None, None, A, BIG,
+                                 None) == UNSUPPORTED
+    # side by side, and in place, pass on to the next check
+    assert lib.moe_norm_post(s, nxt, None, at(size), at(0), at(2 * size), None) == NULL
+    assert lib.moe_norm_post(s, nxt, None, at(0), at(0), at(size), None) == NULL
+    assert lib.moe_norm_post(s, nxt, None, at(0), at(size), at(0), None) == NULL

@@ -70,3 +70,19 @@ def test_past_4_gib_schedules_in_the_log(monkeypatch, capfd):
     lines = [l for l in capfd.readouterr().err.splitlines() if l.startswith("[moe] moe_expert_ffn")]
     assert "; tiled schedule" in lines[0] and "; stream schedule" in lines[1], lines
     assert (y == 0).all()
+
+
+def test_norm_outputs_in_place_of_an_input():
+    """next may take residual's or y's memory, out the other's: the bits of separate outputs."""
+    for dt, d in ((torch.bfloat16, 4096), (torch.float32, 320)):
+        g = torch.Generator(device="cuda").manual_seed(d)
+        y, res = (torch.randn(70, d, generator=g, device="cuda").to(dt) for _ in range(2))
+        w = torch.ones(d, dtype=dt, device="cuda")
+        out, nxt = m.moe_norm_post(y, res, weight=w, next_weight=w)
+        for swap in (False, True):
+            a, b = y.clone(), res.clone()
+            o2, n2 = m.moe_norm_post(a, b, weight=w, next_weight=w, out=a if swap else b, next_out=b if swap else a)
+            assert torch.equal(o2, out) and torch.equal(n2, nxt)
+        with pytest.raises(m.MoeError) as e:
+            m.moe_norm_post(y, res, weight=w, next_weight=w, out=out, next_out=out)
+        assert e.value.status == 6
