@@ -110,8 +110,11 @@ enum { MOE_F32 = 0, MOE_BF16 = 1 };
  *               along the row (moe_quantize_mxfp4), a quarter of bf16's bytes.
  *               The w_* pointers hold the tiled codes, the s_* pointers the
  *               tiled scale bytes ([E, out, in/32]; scale_dtype is not used).
- *               Codes become bf16 exactly, scale included, so the products are
- *               exact and the sums fp32 as for the others. bf16 activations
+ *               Codes become bf16, scale included, so the products are exact
+ *               (subnormal operands too) and the sums fp32 as for the others;
+ *               weights of 2^128 and more, past bf16's largest number (codes
+ *               of 4 and 6 under scale byte 253, of 2 and more under 254),
+ *               become infinite. bf16 activations
  *               (else MOE_ERR_UNSUPPORTED), d and f multiples of 128 (else
  *               MOE_ERR_SHAPE). A pass that reads 4 GiB or more of x (gate/up)
  *               or h (down) takes the STREAM schedule on AUTO; asked for TILED
@@ -403,8 +406,9 @@ moe_status moe_pack_mxfp4(int64_t rows, int32_t cols, const uint8_t* q, const ui
  *   w_q, w_s, w2_q, w2_s  [E, f, d] tiled codes and scales (w2_*: both NULL for
  *     the plain product).
  *   out [T*K, f] act_dtype; rows past off[E] are left untouched.
- * Products are exact, sums fp32, one rounding. Any segment lengths. Rows of
- * codes past 32-bit byte offsets (4 GiB) take the STREAM schedule throughout. */
+ * Products are exact (within the range of fp32), sums fp32, one rounding. Any
+ * segment lengths. Rows of codes past 32-bit byte offsets (4 GiB) take the
+ * STREAM schedule throughout. */
 moe_status moe_grouped_mm_mxfp4(const moe_shape* shape, const uint8_t* a_q, const uint8_t* a_s,
                                 const int32_t* expert_offsets, const int32_t* sorted_slots, const uint8_t* w_q,
                                 const uint8_t* w_s, const uint8_t* w2_q, const uint8_t* w2_s, void* out,

@@ -1,8 +1,13 @@
 """MXFP4 calls at the ends of their ranges, on the GPU."""
+import numpy as np
 import pytest
 import torch
 
 import int8_weight_moe_amd as m
+from int8_weight_moe_amd._lib import MOE_PATH_STREAM, MOE_PATH_TILED
+from oracle import mxfp4 as omx
+from tests.helpers import np64
+from tests.mx_helpers import bf16_exact, check, product_bound, segments
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +91,60 @@ def test_norm_outputs_in_place_of_an_input():
         with pytest.raises(m.MoeError) as e:
             m.moe_norm_post(y, res, weight=w, next_weight=w, out=out, next_out=out)
         assert e.value.status == 6
+
+
+# weights' scale bytes, exponent of the activations. Bytes 0 to 2 make weights below bf16's smallest normal number and
+# 2^-128 .. 2^-133 such activations; bytes up to 252 are the largest whose every code is a finite bf16 number. The
+# other side brings the results back to the normal numbers of fp32, so a flushed operand would be seen.
+ENDS = [((0, 0), 100), ((0, 3), 100), ((1, 1), 100), ((2, 2), 100), ((250, 252), -110), ((230, 240), -128),
+        ((230, 240), -133)]
+
+
+@pytest.mark.parametrize("path", [MOE_PATH_STREAM, MOE_PATH_TILED])
+@pytest.mark.parametrize("scales,exp", ENDS)
+def test_products_at_the_ends_of_the_scales(scales, exp, path):
+    """Products stay exact where operands are subnormal or nearly infinite in bf16 (bounds of tests/mx_helpers.py,
+    without their absolute term)."""
+    counts, d, f, S = [20, 3], 256, 256, 23
+    rng = np.random.default_rng(7)
+    off, slots = segments(counts, S, rng)
+    codes = lambda *shape: (rng.integers(0, 256, (*shape[:-1], shape[-1] // 2)).astype(np.uint8))
+    mats = [(codes(2, r, c), rng.integers(scales[0], scales[1] + 1, (2, r, c // 32)).astype(np.uint8))
+            for r, c in ((f, d), (f, d), (d, f))]
+    dev = lambda a: torch.from_numpy(a).cuda()
+    ex = m.pack_mxfp4_experts(*(dev(q) for q, _ in mats), *(dev(s) for _, s in mats))
+    W = [omx.dequantize(*v) for v in mats]
+    h = bf16_exact(np.ldexp(rng.standard_normal((S, f)), exp))
+    y = m.moe_expert_down(h.cuda(), dev(off), ex, S, 1, path=path)
+    ref, bound = product_bound(np64(h), W[2], off, np.arange(S))
+    check(y, ref, bound - 1e-37, S, "down")
+    # 4-bit activations of the same magnitude
+    aq, byte = codes(S, d), max(0, 127 + exp - 2)
+    asc = np.full((S, d // 32), byte, dtype=np.uint8)
+    out = m.moe_grouped_mm_mxfp4(dev(aq), dev(asc), dev(off), *m.moe_pack_mxfp4(dev(mats[0][0]), dev(mats[0][1])),
+                                 torch.float32, path=path)
+    ref, bound = product_bound(omx.dequantize(aq, asc), W[0], off, np.arange(S))
+    check(out, ref, bound - 1e-37, S, "product")
+
+
+@pytest.mark.parametrize("path", [MOE_PATH_STREAM, MOE_PATH_TILED])
+def test_weights_past_bf16(path):
+    """A weight of 2^128 and more is infinite next to bf16 activations, and exact next to 4-bit ones."""
+    w_q = torch.zeros(1, 128, 64, dtype=torch.uint8, device="cuda")
+    w_s = torch.full((1, 128, 4), 127, dtype=torch.uint8, device="cuda")
+    w_q[0, :, 0] = torch.tensor([1, 3, 5, 6, 7, 14, 15, 0], dtype=torch.uint8, device="cuda").repeat(16)
+    w_s[0, :, 0] = 253                                               # 2^126 times the code's number
+    grid = torch.tensor([0.5, 1.5, 3, 4, 6, -4, -6, 0], dtype=torch.float64).repeat(16) * 2.0 ** 126
+    wt = m.moe_pack_mxfp4(w_q, w_s)
+    ex = m.Int8Experts(wt[0], wt[0], wt[0], wt[1], wt[1], wt[1], fmt=m.MOE_W_MXFP4)
+    off = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    h = torch.zeros(2, 128, dtype=torch.bfloat16, device="cuda")
+    h[:, 0] = torch.tensor([2.0 ** -100, 2.0 ** -20], device="cuda")
+    y = m.moe_expert_down(h, off, ex, 2, 1, path=path).cpu().double()
+    want = torch.where(grid.abs() >= 2.0 ** 128, torch.copysign(torch.tensor(torch.inf, dtype=torch.float64), grid), grid)
+    assert torch.equal(y, h[:, :1].cpu().double() * want)
+    a_q = torch.zeros(2, 64, dtype=torch.uint8, device="cuda")
+    a_q[:, 0] = 2                                                    # one
+    a_s = torch.tensor([[27, 127, 127, 127], [107, 127, 127, 127]], dtype=torch.uint8, device="cuda")
+    out = m.moe_grouped_mm_mxfp4(a_q, a_s, off, *wt, torch.float32, path=path).cpu().double()
+    assert torch.equal(out, h[:, :1].cpu().double() * grid)
