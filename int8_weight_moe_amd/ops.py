@@ -248,7 +248,9 @@ def moe_expert_down(h: torch.Tensor, expert_offsets: torch.Tensor, experts: Int8
     reduction stays inside one workgroup and tiles follow the static order (same
     result, bit for bit)."""
     lib = _lib_handle()
-    _check_width("h", h.shape[1], experts.f)
+    have, need = h.numel(), T * K * experts.f   # h is read as T*K rows whatever its shape
+    if have != need and (have < need or (h.dim() == 2 and h.shape[1] != experts.f)):
+        raise ValueError(f"h has {have} numbers {tuple(h.shape)}, not {T * K} rows of {experts.f} columns")
     shape = make_shape(T, experts.d, experts.f, experts.E, K, act, experts.scale_dtype, path, experts.fmt)
     if y_rows is None:
         y_rows = torch.empty((T * K, experts.d), dtype=torch.float32, device=h.device)

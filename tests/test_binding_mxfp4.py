@@ -99,3 +99,21 @@ def test_sizes_past_32_bits_are_not_cut():
 def test_gate_tokens_past_32_bits(gate_tokens, kept):
     """Past every token it is the same as T; below 1 it reaches the library as a value that it refuses."""
     assert ops._post(5, 64, torch.float32, None, None, gate_tokens, 1.0, 1.0, 1e-6, None, None).gate_tokens == kept
+
+
+@pytest.mark.parametrize("fmt", [MOE_W_INT8, MOE_W_BF16, MOE_W_MXFP4])
+def test_down_takes_h_in_any_contiguous_form(fmt):
+    """h is read as T*K rows of f numbers whatever its shape; one that holds fewer, or other rows, is refused."""
+    ex = _experts(fmt)
+    off = torch.zeros(E + 1, dtype=torch.int32)
+    h = torch.zeros(8, F, dtype=torch.bfloat16)
+    down = lambda t: m.moe_expert_down(t, off, ex, 4, 2)
+    with pytest.raises(Exception) as plain:
+        down(h)                                        # past the checks of the width, to the missing GPU
+    for form in (h.view(-1), h.view(4, 2, F), h.view(16, F // 2), torch.zeros(11, F, dtype=torch.bfloat16), torch.zeros(9 * F)):
+        with pytest.raises(type(plain.value)) as e:
+            down(form)
+        assert str(e.value) == str(plain.value)
+    for bad in (h[:, :128].contiguous(), torch.zeros(8, 2 * F), h[:7], h.view(-1)[:-1]):
+        with pytest.raises(ValueError, match="columns"):
+            down(bad)

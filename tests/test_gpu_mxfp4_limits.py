@@ -148,3 +148,14 @@ def test_weights_past_bf16(path):
     a_s = torch.tensor([[27, 127, 127, 127], [107, 127, 127, 127]], dtype=torch.uint8, device="cuda")
     out = m.moe_grouped_mm_mxfp4(a_q, a_s, off, *wt, torch.float32, path=path).cpu().double()
     assert torch.equal(out, h[:, :1].cpu().double() * grid)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "mxfp4"])
+def test_down_of_a_flat_h(fmt):
+    w = [torch.randn(2, r, c, device="cuda").to(torch.bfloat16) for r, c in ((256, 128), (256, 128), (128, 256))]
+    ex = m.quantize_experts_mxfp4(*w) if fmt == "mxfp4" else m.quantize_experts(*w, torch.bfloat16)
+    off = torch.tensor([0, 3, 8], dtype=torch.int32, device="cuda")
+    h = torch.randn(8, 256, device="cuda").to(torch.bfloat16)
+    y = m.moe_expert_down(h, off, ex, 4, 2)
+    for form in (h.view(-1), h.view(4, 2, 256), h.view(16, 128), torch.cat([h, h])):
+        assert torch.equal(m.moe_expert_down(form, off, ex, 4, 2), y)
