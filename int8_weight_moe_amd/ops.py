@@ -462,17 +462,15 @@ def quantize_experts(w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Ten
 
 # ---------------------------------------------------------------- MXFP4 and the norms around the layer
 
-_device = torch._C._cuda_getDevice   # index of the current device
-
-
 def _arg(name: str, t: Optional[torch.Tensor], dtype: Optional[torch.dtype], shape=None):
     """Pointer of a contiguous tensor of this type and shape on the current device (None: NULL)."""
     if t is None:
         return None
+    # the device's index is looked up at the call: a torch without GPU support has no such function
     if ((dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape) and t.is_contiguous()
-            and t.is_cuda and t.get_device() == _device()):
+            and t.is_cuda and t.get_device() == torch._C._cuda_getDevice()):
         return t.data_ptr()
-    if not t.is_cuda or t.get_device() != _device():
+    if not t.is_cuda or t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on {t.device}, not on the current HIP device")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, not {dtype}")

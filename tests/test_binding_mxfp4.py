@@ -1,5 +1,8 @@
 """The binding's checks of the MXFP4 and block calls (CPU: each call is refused before it reaches the library)."""
 import dataclasses
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -117,3 +120,19 @@ def test_down_takes_h_in_any_contiguous_form(fmt):
     for bad in (h[:, :128].contiguous(), torch.zeros(8, 2 * F), h[:7], h.view(-1)[:-1]):
         with pytest.raises(ValueError, match="columns"):
             down(bad)
+
+
+def test_import_on_a_torch_without_gpu_bindings():
+    """The package imports, and says what is missing at the first call, where torch was built without a GPU."""
+    code = ("import torch\n"
+            "for n in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    if hasattr(torch._C, n): delattr(torch._C, n)\n"
+            "import int8_weight_moe_amd as m\n"
+            "try:\n"
+            "    m.moe_norm_pre(torch.zeros(2, 64), torch.ones(64))\n"
+            "except ValueError as e:\n"
+            "    assert 'not on the current HIP device' in str(e)\n"
+            "    print('imported')\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                       capture_output=True, text=True)
+    assert r.returncode == 0 and "imported" in r.stdout, r.stderr
