@@ -397,8 +397,9 @@ moe_status moe_pack_mxfp4(int64_t rows, int32_t cols, const uint8_t* q, const ui
  *   row r of expert e's segment [off[e], off[e+1]):
  *     out[r, n] = sum_k A[row(r), k] * W_e[n, k],                   n < f, k < d
  *     or, with a second matrix, silu(W_e . a) * (W2_e . a).
- *   shape: T tokens, K slots a token (rows of out: T*K), d the reduction, f the
- *     output channels, E experts; weight_fmt MOE_W_MXFP4 (else MOE_ERR_DTYPE);
+ *   shape: T tokens, K slots a token (rows of out: T*K; 1..8, more than E too: a
+ *     shard holds some of a token's experts), d the reduction, f the output
+ *     channels, E experts; weight_fmt MOE_W_MXFP4 (else MOE_ERR_DTYPE);
  *     act_dtype is out's type; scale_dtype is not used; ffn_path as for the
  *     expert FFN; d and f multiples of 128.
  *   a_q, a_s  codes and scales of A, row-major, d columns. With sorted_slots

@@ -112,13 +112,15 @@ constexpr long kMxFewTilesRowsPerExpert = 32;
 constexpr long kMxFewTilesWideRowsPerExpert = 20;
 constexpr long kMxFewTilesChannels = 16384;
 
-moe_status check_shape(const moe_shape* s) {
+// routes: the call's K experts of a token are distinct ones of the E.
+moe_status check_shape(const moe_shape* s, bool routes = true) {
   if (!s) return fail(MOE_ERR_NULL, "shape is NULL");
   if (s->T < 0) return fail(MOE_ERR_SHAPE, "T=%d must be >= 0", s->T);
   if (s->d < 64 || s->d > 65536 || s->d % 64) return fail(MOE_ERR_SHAPE, "d=%d must be a multiple of 64 in [64, 65536]", s->d);
   if (s->f < 64 || s->f > 131072 || s->f % 64) return fail(MOE_ERR_SHAPE, "f=%d must be a multiple of 64 in [64, 131072]", s->f);
   if (s->E < 1 || s->E > 64) return fail(MOE_ERR_SHAPE, "E=%d must be in [1, 64]", s->E);
-  if (s->K < 1 || s->K > s->E || s->K > 8) return fail(MOE_ERR_SHAPE, "K=%d must be in [1, min(E, 8)]", s->K);
+  if (s->K < 1 || s->K > 8 || (routes && s->K > s->E))
+    return fail(MOE_ERR_SHAPE, routes ? "K=%d must be in [1, min(E, 8)]" : "K=%d must be in [1, 8]", s->K);
   if ((long)s->T * s->K > (1L << 26)) return fail(MOE_ERR_SHAPE, "T*K=%ld exceeds 2^26", (long)s->T * s->K);
   if (s->act_dtype != MOE_F32 && s->act_dtype != MOE_BF16) return fail(MOE_ERR_DTYPE, "act_dtype=%d", s->act_dtype);
   if (s->scale_dtype != MOE_F32 && s->scale_dtype != MOE_BF16) return fail(MOE_ERR_DTYPE, "scale_dtype=%d", s->scale_dtype);
@@ -381,8 +383,8 @@ moe_status check_mxfp4(int64_t rows, int32_t cols, int32_t layout, const void* q
 }
 
 // Shape of a product with both operands in MXFP4.
-moe_status check_mx_shape(const moe_shape* s) {
-  const moe_status st = check_shape(s);
+moe_status check_mx_shape(const moe_shape* s, bool routes) {
+  const moe_status st = check_shape(s, routes);
   if (st != MOE_OK) return st;
   if (s->weight_fmt != MOE_W_MXFP4) return fail(MOE_ERR_DTYPE, "weight_fmt=%d: this call takes MXFP4 weights", s->weight_fmt);
   if (s->d % 128 || s->f % 128)
@@ -972,7 +974,7 @@ moe_status moe_grouped_mm_mxfp4(const moe_shape* s, const uint8_t* a_q, const ui
                                 const int32_t* expert_offsets, const int32_t* sorted_slots, const uint8_t* w_q,
                                 const uint8_t* w_s, const uint8_t* w2_q, const uint8_t* w2_s, void* out,
                                 hipStream_t stream) {
-  moe_status st = check_mx_shape(s);
+  moe_status st = check_mx_shape(s, false);
   if (st != MOE_OK) return st;
   if (s->T == 0) return MOE_OK;   // nothing is read or written
   REQUIRE_PTR(a_q);
@@ -1009,7 +1011,7 @@ moe_status moe_grouped_mm_mxfp4(const moe_shape* s, const uint8_t* a_q, const ui
 }
 
 moe_status moe_expert_ffn_mxfp4_workspace_size(const moe_shape* shape, size_t* bytes) {
-  const moe_status st = check_mx_shape(shape);
+  const moe_status st = check_mx_shape(shape, true);
   if (st != MOE_OK) return st;
   if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
   *bytes = mx_ffn_layout(shape).total;
@@ -1021,7 +1023,7 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* s, const void* x, const int32_t
                                 const uint8_t* w_down, const uint8_t* s_gate, const uint8_t* s_up,
                                 const uint8_t* s_down, float* y_rows, void* workspace, size_t workspace_bytes,
                                 hipStream_t stream) {
-  moe_status st = check_mx_shape(s);
+  moe_status st = check_mx_shape(s, true);
   if (st != MOE_OK) return st;
   if (s->T == 0) return MOE_OK;   // nothing is read or written
   REQUIRE_PTR(x);

@@ -7,7 +7,7 @@ import ctypes
 import pytest
 
 from int8_weight_moe_amd import _lib
-from tests.test_abi_mxfp4 import A, B, BIG, NULL, UNSUPPORTED, _post, _shape
+from tests.test_abi_mxfp4 import A, B, BIG, NULL, SHAPE, UNSUPPORTED, _post, _shape
 
 
 @pytest.fixture(scope="module")
@@ -81,3 +81,14 @@ def test_norm_outputs_that_overlap_are_refused(lib, act, size):
     assert lib.moe_norm_post(s, nxt, None, at(size), at(0), at(2 * size), None) == NULL
     assert lib.moe_norm_post(s, nxt, None, at(0), at(0), at(size), None) == NULL
     assert lib.moe_norm_post(s, nxt, None, at(0), at(size), at(0), None) == NULL
+
+
+def test_product_takes_more_slots_a_token_than_experts(lib):
+    """A shard with fewer experts than a token has slots; only the calls that route keep K <= E."""
+    mm = lambda s: lib.moe_grouped_mm_mxfp4(s, A, A, A, A, A, A, None, None, None, None)
+    for E, K in ((1, 2), (2, 8), (7, 8)):
+        assert mm(_shape(E=E, K=K)) == NULL
+        n = ctypes.c_size_t(0)
+        assert lib.moe_expert_ffn_mxfp4_workspace_size(_shape(E=E, K=K), ctypes.byref(n)) == SHAPE
+        assert lib.moe_workspace_size(_shape(E=E, K=K), ctypes.byref(n)) == SHAPE
+    assert mm(_shape(K=9)) == SHAPE and mm(_shape(E=1, K=9)) == SHAPE and mm(_shape(K=0)) == SHAPE

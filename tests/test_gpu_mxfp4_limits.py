@@ -159,3 +159,21 @@ def test_down_of_a_flat_h(fmt):
     y = m.moe_expert_down(h, off, ex, 4, 2)
     for form in (h.view(-1), h.view(4, 2, 256), h.view(16, 128), torch.cat([h, h])):
         assert torch.equal(m.moe_expert_down(form, off, ex, 4, 2), y)
+
+
+@pytest.mark.parametrize("path", [MOE_PATH_STREAM, MOE_PATH_TILED])
+@pytest.mark.parametrize("counts,T,K", [([9], 6, 4), ([20, 33], 40, 8), ([0, 1], 1, 8)])
+def test_product_of_a_shard(counts, T, K, path):
+    """Fewer experts than slots a token: the slots of experts elsewhere lie past the last segment."""
+    rng = np.random.default_rng(T * K)
+    S, d, f, E = T * K, 384, 256, len(counts)
+    off, slots = segments(counts, S, rng)
+    codes = lambda *shape: rng.integers(0, 256, (*shape[:-1], shape[-1] // 2)).astype(np.uint8)
+    scales = lambda *shape: rng.integers(118, 124, (*shape[:-1], shape[-1] // 32)).astype(np.uint8)
+    a, w = (codes(T, d), scales(T, d)), (codes(E, f, d), scales(E, f, d))
+    dev = lambda t: torch.from_numpy(t).cuda()
+    out = m.moe_grouped_mm_mxfp4(dev(a[0]), dev(a[1]), dev(off), *m.moe_pack_mxfp4(dev(w[0]), dev(w[1])), torch.float32,
+                                 sorted_slots=dev(slots), K=K, path=path, out=torch.full((S, f), 7.0, device="cuda"))
+    ref, bound = product_bound(omx.dequantize(*a), omx.dequantize(*w), off, slots // K)
+    check(out, ref, bound, int(off[-1]), "product")
+    assert (out[int(off[-1]):] == 7.0).all()
