@@ -64,7 +64,9 @@
  *     per pass to stderr ("[moe] <call> gate/up|down: <shape>; <schedule>"):
  *     the schedule (stream or tiled), and for the stream schedule the rows per
  *     pass, where the expert segments come from, and whether the down pass
- *     splits its reduction over workgroups. Nothing else changes.
+ *     splits its reduction over workgroups; with MXFP4 weights the channels of
+ *     an item, the rows of a pass and the slices of the reduction, or the tile
+ *     and its order. Nothing else changes.
  */
 #ifndef MOE_INT8_H
 #define MOE_INT8_H

@@ -343,10 +343,20 @@ moe_status run_mx(const char* call, const char* what, const moe_shape* s, const 
   }
   // rows past the tiled kernel's 32-bit offsets (on TILED, bf16 rows are refused by check_ffn)
   if (!moe::mx_tiled_offsets_fit(m.a_rows, m.Kd, m.a_s != nullptr)) by_stream = true;
-  if (log_on())
-    fprintf(stderr, "[moe] %s %s: rows=%d reduction=%d channels=%d E=%d act=%s weights=mxfp4 out=%s; %s schedule%s\n",
-            call, what, m.S, m.Kd, m.N, m.E, m.a_s ? "mxfp4" : "bf16", m.out_bf16 ? "bf16" : "f32",
-            by_stream ? "stream" : "tiled", m.w1 ? ", SwiGLU" : "");
+  if (log_on()) {
+    char how[128];
+    if (by_stream) {
+      const moe::MxStreamPlan p = moe::mx_stream_plan(m);
+      snprintf(how, sizeof(how), "stream schedule, %d-channel items, %d-row passes, reduction in %d slices", p.channels,
+               p.rows, p.slices);
+    } else {
+      const moe::MxTilePlan p = moe::mx_tile_plan(m);
+      snprintf(how, sizeof(how), "tiled schedule, %dx%d tiles, %s", p.rows, p.channels,
+               p.claims ? "the last tiles of each XCD queue claimed" : "static tile order");
+    }
+    fprintf(stderr, "[moe] %s %s: rows=%d reduction=%d channels=%d E=%d act=%s weights=mxfp4 out=%s%s; %s\n", call, what,
+            m.S, m.Kd, m.N, m.E, m.a_s ? "mxfp4" : "bf16", m.out_bf16 ? "bf16" : "f32", m.w1 ? " SwiGLU" : "", how);
+  }
   const hipError_t e = by_stream ? moe::launch_mx_stream(m, stream) : moe::launch_mx_tiled(m, stream);
   if (e != hipSuccess) return hip_fail(e, what);
   return MOE_OK;

@@ -107,6 +107,19 @@ struct MxArgs {
   unsigned long long* claims;   // tile claim words of the tiled kernel ([8], cleared by the launch), or null
   int E, N, Kd, S;
 };
+// What the two launches below take for these sizes: channels of an item (of each
+// matrix), rows a pass and slices of the reduction; rows and channels of a tile
+// (with two matrices half the channels are of each) and whether the queues' last
+// tiles are claimed.
+struct MxStreamPlan {
+  int channels, rows, slices;
+};
+struct MxTilePlan {
+  int rows, channels;
+  bool claims;
+};
+MxStreamPlan mx_stream_plan(const MxArgs& a);
+MxTilePlan mx_tile_plan(const MxArgs& a);
 hipError_t launch_mx_stream(const MxArgs& a, hipStream_t stream);
 // Whether rows of `cols` numbers (MXFP4 codes, or bf16) lie within 32-bit byte
 // offsets, as launch_mx_tiled needs the rows of a to.

@@ -275,15 +275,29 @@ int stream_slices(long items, int groups) {
   return ks;
 }
 
+// Channels per item: wide items read the rows' activations fewer times (a wave
+// reads its rows' bf16 activations from L2 for every item: down of 64 tokens, d
+// 8192, 534, 351 and 279 us for 16, 32 and 64 channels), narrow ones give few
+// items more waves (gate/up of one token: 25.3 us for 16 channels, 27.3 for 32;
+// down of one token: 15.4 us for 32, 20.5 for 64). MXFP4 activations are a
+// quarter of the bytes: 32 channels pay for one matrix with many items (64
+// tokens, d 24576, f 8192: 306 us for 16 channels, 282 for 32; 17 tokens, d 4096,
+// f 14336: 68 and 74). N is a multiple of 128, so every width divides it.
+int stream_width(const MxArgs& a) {
+  if (a.a_s) return !a.w1 && stream_items(a, 2) >= 4096 ? 2 : 1;
+  if (a.w1) return stream_items(a, 2) >= 1024 ? 2 : 1;
+  if (stream_items(a, 4) >= 1024) return 4;
+  return stream_items(a, 2) >= 256 ? 2 : 1;
+}
+
 template <bool kMxAct, int NMAT, int NG, int RB, bool kOutBf16, int U>
-hipError_t launch_ks(const MxArgs& a, hipStream_t stream) {
+hipError_t launch_slices(const MxArgs& a, int slices, hipStream_t stream) {
   const long items = stream_items(a, NG);
-  const int groups = (a.Kd / kMxStep + kMxGroup - 1) / kMxGroup;
 #define MOE_MX_STREAM(KS)                                                                                       \
   hipLaunchKernelGGL((mx_stream_kernel<kMxAct, NMAT, NG, RB, KS, kOutBf16, U>),                                 \
                      dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves)),              \
                      dim3(block_waves(KS) * kWave), 0, stream, a)
-  switch (stream_slices(items, groups)) {
+  switch (slices) {
     case 1: MOE_MX_STREAM(1); break;
     case 2: MOE_MX_STREAM(2); break;
     case 4: MOE_MX_STREAM(4); break;
@@ -293,40 +307,42 @@ hipError_t launch_ks(const MxArgs& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Channels per item: wide items read the rows' activations fewer times (a wave
-// reads its rows' bf16 activations from L2 for every item: down of 64 tokens, d
-// 8192, 534, 351 and 279 us for 16, 32 and 64 channels), narrow ones give few
-// items more waves (gate/up of one token: 25.3 us for 16 channels, 27.3 for 32;
-// down of one token: 15.4 us for 32, 20.5 for 64). MXFP4 activations are a
-// quarter of the bytes: 32 channels pay for one matrix with many items (64
-// tokens, d 24576, f 8192: 306 us for 16 channels, 282 for 32; 17 tokens, d 4096,
-// f 14336: 68 and 74). N is a multiple of 128, so every width divides it.
 template <bool kMxAct, int NMAT, int RB, bool kOutBf16>
-hipError_t launch_width(const MxArgs& a, hipStream_t stream) {
+hipError_t launch_width(const MxArgs& a, const MxStreamPlan& p, hipStream_t stream) {
   constexpr int U = RB == 1 ? 2 : 1;   // two row blocks: more steps at once would spill
   if constexpr (kMxAct) {
     if constexpr (NMAT == 1)
-      if (stream_items(a, 2) >= 4096) return launch_ks<true, 1, 2, RB, kOutBf16, 2>(a, stream);
-    return launch_ks<true, NMAT, 1, RB, kOutBf16, 2>(a, stream);
+      if (p.channels == 32) return launch_slices<true, 1, 2, RB, kOutBf16, 2>(a, p.slices, stream);
+    return launch_slices<true, NMAT, 1, RB, kOutBf16, 2>(a, p.slices, stream);
   } else if constexpr (NMAT == 2) {
-    if (stream_items(a, 2) >= 1024) return launch_ks<false, 2, 2, RB, kOutBf16, U>(a, stream);
-    return launch_ks<false, 2, 1, RB, kOutBf16, 1>(a, stream);
+    if (p.channels == 32) return launch_slices<false, 2, 2, RB, kOutBf16, U>(a, p.slices, stream);
+    return launch_slices<false, 2, 1, RB, kOutBf16, 1>(a, p.slices, stream);
   } else {
-    if (stream_items(a, 4) >= 1024) return launch_ks<false, 1, 4, RB, kOutBf16, U>(a, stream);
-    if (stream_items(a, 2) >= 256) return launch_ks<false, 1, 2, RB, kOutBf16, U>(a, stream);
-    return launch_ks<false, 1, 1, RB, kOutBf16, U>(a, stream);
+    if (p.channels == 64) return launch_slices<false, 1, 4, RB, kOutBf16, U>(a, p.slices, stream);
+    if (p.channels == 32) return launch_slices<false, 1, 2, RB, kOutBf16, U>(a, p.slices, stream);
+    return launch_slices<false, 1, 1, RB, kOutBf16, U>(a, p.slices, stream);
   }
 }
 
-// Row blocks per pass: one for up to eight rows an expert on average (an expert
-// with more than 16 streams its weights again), else two.
 template <bool kMxAct, int NMAT, bool kOutBf16>
 hipError_t launch_rows(const MxArgs& a, hipStream_t stream) {
-  return a.S <= 8L * a.E ? launch_width<kMxAct, NMAT, 1, kOutBf16>(a, stream)
-                         : launch_width<kMxAct, NMAT, 2, kOutBf16>(a, stream);
+  const MxStreamPlan p = mx_stream_plan(a);
+  return p.rows == 16 ? launch_width<kMxAct, NMAT, 1, kOutBf16>(a, p, stream)
+                      : launch_width<kMxAct, NMAT, 2, kOutBf16>(a, p, stream);
 }
 
 }  // namespace
+
+MxStreamPlan mx_stream_plan(const MxArgs& a) {
+  MxStreamPlan p;
+  const int ng = stream_width(a);
+  p.channels = 16 * ng;
+  // one row block per pass for up to eight rows an expert on average (an expert
+  // with more than 16 streams its weights again), else two
+  p.rows = a.S <= 8L * a.E ? 16 : 32;
+  p.slices = stream_slices(stream_items(a, ng), (a.Kd / kMxStep + kMxGroup - 1) / kMxGroup);
+  return p;
+}
 
 hipError_t launch_mx_stream(const MxArgs& a, hipStream_t stream) {
   if (a.a_s) {

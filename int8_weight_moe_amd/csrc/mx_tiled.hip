@@ -295,29 +295,14 @@ __global__ void zero_words_kernel(unsigned long long* __restrict__ claims) {
   if (threadIdx.x < kXcds) claims[threadIdx.x] = 0ull;
 }
 
-template <bool kMxAct, int NMAT, bool kOutBf16, int kBM, int kBN>
-hipError_t launch_tile(MxArgs a, hipStream_t stream) {
-  // row tiles of an expert that take a channel tile together
-  constexpr int GM = (NMAT == 2 || kMxAct) ? 8 : 4;
-  constexpr int CH = kBN / NMAT;
-  const int n_tiles = (a.N + CH - 1) / CH;
-  const long total = ((long)(a.S + kBM - 1) / kBM + a.E) * n_tiles;
-  const long per_xcd = (total + kXcds - 1) / kXcds;
-  long blocks = kXcds * per_xcd;
-  // The claimed tail costs a launch (3 us) and an atomic in every block past the
-  // static ones, of which there are many if the tile count's bound is loose; it
-  // balances the XCDs over many rounds of long tiles. So: many tiles, several row
-  // tiles an expert, a long reduction. (gate/up of 325 tokens, d 384, f 10496, E 9,
-  // K 4, on 128x128 tiles: 181 us with it.)
-  if (total < 2048 || a.S < 4L * kBM * a.E || a.Kd < 2048) a.claims = nullptr;
-  if (a.claims) {
-    // the static blocks of the longest queue, then one and a half times its tail
-    blocks = kXcds * (per_xcd + min(per_xcd, (long)kClaimTail) / 2);
-    hipLaunchKernelGGL(zero_words_kernel, dim3(1), dim3(kWave), 0, stream, a.claims);
-  }
-  hipLaunchKernelGGL((mx_tiled_kernel<kMxAct, NMAT, kOutBf16, GM, kBM, kBN>), dim3((unsigned)blocks), dim3(kWaves * kWave),
-                     0, stream, a, n_tiles);
-  return hipGetLastError();
+// Channel tiles of a row of tiles `channels` wide, and the most tiles that any
+// segments make.
+int tile_columns(const MxArgs& a, int channels) {
+  const int ch = a.w1 ? channels / 2 : channels;
+  return (a.N + ch - 1) / ch;
+}
+long tile_bound(const MxArgs& a, int rows, int channels) {
+  return ((long)(a.S + rows - 1) / rows + a.E) * tile_columns(a, channels);
 }
 
 // Tile of a pass, in rows x channels: the rows from the rows an expert has on
@@ -333,36 +318,72 @@ hipError_t launch_tile(MxArgs a, hipStream_t stream) {
 //     at 1024 1443 / 1443 / 1601 / 1718; f 2816, d 2048, 2048 rows 328 / 323 / 367 / 384;
 //   MXFP4 activations, SwiGLU, d 4096, f 14336: 128x256 / 128x128 at 16 rows 184 / 174, at 64
 //     198 / 194, at 128 253 / 279; few tiles (d 4480, f 1280, E 4, 640 rows) 29.2 / 21.7.
-template <bool kMxAct, int NMAT, bool kOutBf16>
-hipError_t launch_tiled(const MxArgs& a, hipStream_t stream) {
+void pick_tile(const MxArgs& a, MxTilePlan& p) {
   const long S = a.S, E = a.E;
   // tiles of `rows` x `channels` if the rows spread evenly
   auto tiles = [&](int rows, int channels) {
     const long per_expert = S <= E * rows / 2 ? 2 : 2 * S / (E * rows) + 1;   // halves of a row tile, at least one tile
-    return E * per_expert / 2 * ((a.N + channels / NMAT - 1) / (channels / NMAT));
+    return E * per_expert / 2 * tile_columns(a, channels);
   };
-  if constexpr (kMxAct) {
-    if (S <= 64 * E || tiles(128, 256) < 512) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, stream);
-    return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
-  } else if constexpr (NMAT == 2) {
-    if (S > 160 * E) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
-    if (tiles(64, 256) < 400) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 128>(a, stream);
-    return launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, stream);
-  } else {
-    if (S > 48 * E && S <= 96 * E) {   // most experts fit 128 rows and not 64
-      if (tiles(128, 256) < 512) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, stream);
-      return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
-    }
-    if (S > 512 * E) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, stream);
-    if (tiles(64, 256) < 512) return launch_tile<kMxAct, NMAT, kOutBf16, 64, 128>(a, stream);
-    return launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, stream);
+  auto tile = [&](int rows, int channels) {
+    p.rows = rows;
+    p.channels = channels;
+  };
+  if (a.a_s) return tile(128, S <= 64 * E || tiles(128, 256) < 512 ? 128 : 256);
+  if (a.w1) return S > 160 * E ? tile(128, 256) : tile(64, tiles(64, 256) < 400 ? 128 : 256);
+  // most experts fit 128 rows and not 64
+  if (S > 48 * E && S <= 96 * E) return tile(128, tiles(128, 256) < 512 ? 128 : 256);
+  return S > 512 * E ? tile(128, 256) : tile(64, tiles(64, 256) < 512 ? 128 : 256);
+}
+
+template <bool kMxAct, int NMAT, bool kOutBf16, int kBM, int kBN>
+hipError_t launch_tile(MxArgs a, const MxTilePlan& p, hipStream_t stream) {
+  // row tiles of an expert that take a channel tile together
+  constexpr int GM = (NMAT == 2 || kMxAct) ? 8 : 4;
+  const int n_tiles = tile_columns(a, kBN);
+  const long per_xcd = (tile_bound(a, kBM, kBN) + kXcds - 1) / kXcds;
+  long blocks = kXcds * per_xcd;
+  if (!p.claims) a.claims = nullptr;
+  if (a.claims) {
+    // the static blocks of the longest queue, then one and a half times its tail
+    blocks = kXcds * (per_xcd + min(per_xcd, (long)kClaimTail) / 2);
+    hipLaunchKernelGGL(zero_words_kernel, dim3(1), dim3(kWave), 0, stream, a.claims);
   }
+  hipLaunchKernelGGL((mx_tiled_kernel<kMxAct, NMAT, kOutBf16, GM, kBM, kBN>), dim3((unsigned)blocks), dim3(kWaves * kWave),
+                     0, stream, a, n_tiles);
+  return hipGetLastError();
+}
+
+template <bool kMxAct, int NMAT, bool kOutBf16>
+hipError_t launch_tiled(const MxArgs& a, hipStream_t stream) {
+  const MxTilePlan p = mx_tile_plan(a);
+  const bool wide = p.channels == 256;
+  if (p.rows == 128) {
+    if (wide) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 256>(a, p, stream);
+    if constexpr (kMxAct || NMAT == 1) return launch_tile<kMxAct, NMAT, kOutBf16, 128, 128>(a, p, stream);
+  } else if constexpr (!kMxAct) {
+    return wide ? launch_tile<kMxAct, NMAT, kOutBf16, 64, 256>(a, p, stream)
+                : launch_tile<kMxAct, NMAT, kOutBf16, 64, 128>(a, p, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
 
 bool mx_tiled_offsets_fit(long rows, int cols, bool mx) {
   return (uint64_t)rows * (uint64_t)cols * (mx ? 1 : 4) < (1ull << 33);
+}
+
+MxTilePlan mx_tile_plan(const MxArgs& a) {
+  MxTilePlan p;
+  pick_tile(a, p);
+  // The claimed tail costs a launch (3 us) and an atomic in every block past the
+  // static ones, of which there are many if the tile count's bound is loose; it
+  // balances the XCDs over many rounds of long tiles. So: many tiles, several row
+  // tiles an expert, a long reduction. (gate/up of 325 tokens, d 384, f 10496, E 9,
+  // K 4, on 128x128 tiles: 181 us with it.)
+  p.claims = a.claims && tile_bound(a, p.rows, p.channels) >= 2048 && a.S >= 4L * p.rows * a.E && a.Kd >= 2048;
+  return p;
 }
 
 hipError_t launch_mx_tiled(const MxArgs& a, hipStream_t stream) {
