@@ -290,21 +290,33 @@ int stream_width(const MxArgs& a) {
   return stream_items(a, 2) >= 256 ? 2 : 1;
 }
 
+// The most slices that stream_slices gives items of 16*NG channels: wide ones
+// are chosen for 1024 items and more, with MXFP4 activations for 4096.
+constexpr int most_slices(bool mx_act, int nmat, int ng) {
+  if (mx_act) return ng == 2 ? 2 : 8;
+  return ng == 4 || (nmat == 2 && ng == 2) ? 4 : 8;
+}
+
 template <bool kMxAct, int NMAT, int NG, int RB, bool kOutBf16, int U>
 hipError_t launch_slices(const MxArgs& a, int slices, hipStream_t stream) {
   const long items = stream_items(a, NG);
-#define MOE_MX_STREAM(KS)                                                                                       \
-  hipLaunchKernelGGL((mx_stream_kernel<kMxAct, NMAT, NG, RB, KS, kOutBf16, U>),                                 \
-                     dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves)),              \
-                     dim3(block_waves(KS) * kWave), 0, stream, a)
+  hipError_t e = hipErrorInvalidValue;
+  auto launch = [&](auto ksc) {
+    constexpr int KS = decltype(ksc)::value;
+    if constexpr (KS <= most_slices(kMxAct, NMAT, NG)) {
+      hipLaunchKernelGGL((mx_stream_kernel<kMxAct, NMAT, NG, RB, KS, kOutBf16, U>),
+                         dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves)),
+                         dim3(block_waves(KS) * kWave), 0, stream, a);
+      e = hipGetLastError();
+    }
+  };
   switch (slices) {
-    case 1: MOE_MX_STREAM(1); break;
-    case 2: MOE_MX_STREAM(2); break;
-    case 4: MOE_MX_STREAM(4); break;
-    default: MOE_MX_STREAM(8); break;
+    case 1: launch(int_constant<1>{}); break;
+    case 2: launch(int_constant<2>{}); break;
+    case 4: launch(int_constant<4>{}); break;
+    case 8: launch(int_constant<8>{}); break;
   }
-#undef MOE_MX_STREAM
-  return hipGetLastError();
+  return e;
 }
 
 template <bool kMxAct, int NMAT, int RB, bool kOutBf16>
