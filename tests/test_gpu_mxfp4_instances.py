@@ -11,8 +11,7 @@ import pytest
 import torch
 
 import int8_weight_moe_amd as m
-from int8_weight_moe_amd import ops
-from int8_weight_moe_amd._lib import MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_TILED, MOE_W_MXFP4
+from int8_weight_moe_amd._lib import MOE_PATH_STREAM, MOE_PATH_TILED, MOE_W_MXFP4
 from tests.test_gpu_mxfp4_limits import draw, values
 
 pytestmark = pytest.mark.gpu
@@ -227,3 +226,57 @@ def test_claimed_tail_with_one_crowded_expert():
     got = case.run(MOE_PATH_TILED)
     case.check(got, "crowded")
     assert torch.equal(case.run(MOE_PATH_TILED, workspace=False), got)
+
+
+# ------------------------------------------------------------------ the borders between the schedules
+
+def _schedules(capfd, monkeypatch, call):
+    monkeypatch.setenv("MOE_LOG", "1")
+    capfd.readouterr()
+    r = call()
+    names = [l.split(" schedule")[0] for l in _logged(capfd)]
+    monkeypatch.delenv("MOE_LOG")
+    return r, names
+
+
+# (experts, width of d and f): 16384 output channels over all experts, and 18432. Per call the rows an expert on both
+# sides of each border, with the schedules of the gate/up and the down pass. 4-bit activations: both borders are one.
+FEW_CHANNELS, MORE_CHANNELS = (8, 2048), (16, 1152)
+BORDERS = [
+    (FEW_CHANNELS, 20, "stream stream", "stream stream"), (FEW_CHANNELS, 21, "tiled stream", "tiled tiled"),
+    (FEW_CHANNELS, 32, "tiled stream", "tiled tiled"), (FEW_CHANNELS, 33, "tiled tiled", "tiled tiled"),
+    (MORE_CHANNELS, 8, "stream stream", "stream stream"), (MORE_CHANNELS, 9, "tiled stream", "tiled tiled"),
+    (MORE_CHANNELS, 16, "tiled stream", "tiled tiled"), (MORE_CHANNELS, 17, "tiled tiled", "tiled tiled"),
+]
+
+
+@pytest.mark.parametrize("size,rows,bf16,mx", BORDERS)
+def test_borders_of_the_schedules(capfd, monkeypatch, size, rows, bf16, mx):
+    """AUTO on both sides of each border: the schedules taken, the numbers, and the layer made of the same passes.
+
+    Between the borders the gate/up pass is tiled with a workspace that is laid out for a streamed down pass.
+    """
+    E, n = size
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    S = rows * E if rows % 4 == 0 else (rows - 1) * E + 1         # a border is full, or passed by one row
+    x = torch.randn(S, n, generator=gen, device="cuda").to(torch.bfloat16)
+    wr = (torch.randn(E, n, generator=gen, device="cuda") * 0.05).to(torch.bfloat16)
+    mats = [draw((E, n), n, gen, 116, 121) for _ in range(3)]
+    ex = m.pack_mxfp4_experts(*(q for q, _ in mats), *(s for _, s in mats))
+    (y, ids, gw), names = _schedules(capfd, monkeypatch, lambda: m.moe_forward(x, wr, None, ex, 1))
+    assert " ".join(names) == bf16
+    off, slots, s2r = m.moe_permute(ids, E)
+    counts = (off[1:] - off[:-1]).tolist()
+    y_rows, names = _schedules(capfd, monkeypatch, lambda: m.moe_expert_ffn(x, off, slots, ex, 1))
+    assert " ".join(names) == bf16
+    assert torch.equal(m.moe_combine(y_rows, s2r, gw, torch.bfloat16), y)
+    h = m.moe_expert_gate_up(x, off, slots, ex, 1)
+    assert torch.equal(m.moe_expert_down(h, off, ex, S, 1), y_rows)
+    _check(h, x.double(), slots, counts, mats[:2], n, True, "gate/up")
+    _check(y_rows, h.double(), torch.arange(S, device="cuda"), counts, mats[2:], n, False, "down")
+    # with 4-bit activations
+    y_rows, names = _schedules(capfd, monkeypatch, lambda: m.moe_expert_ffn_mxfp4(x, off, slots, ex, 1))
+    assert " ".join(names) == mx
+    hq, hs = m.moe_quantize_mxfp4(m.moe_grouped_mm_mxfp4(*m.moe_quantize_mxfp4(x), off, ex.q_gate, ex.s_gate, torch.bfloat16,
+                                                         sorted_slots=slots, w2_q=ex.q_up, w2_s=ex.s_up))
+    _check(y_rows, values(hq, hs), torch.arange(S, device="cuda"), counts, mats[2:], n, False, "4-bit down")
