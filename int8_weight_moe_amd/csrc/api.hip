@@ -108,6 +108,9 @@ constexpr long kMxWideStreamRowsPerExpert = 8;
 // (rows an expert): down, f 4096, d 4096, E 4 at 12 rows 13.6 / 28.9, at 32 26.6 / 32.2; f 8192,
 // d 2048, E 8 at 32 47.9 / 62.6; gate/up, d 4096, f 4096, E 4 at 20 27.7 / 30.7, at 32 48.6 /
 // 33.9; d 8192, f 2048, E 8 at 20 51.3 / 57.5; both in MXFP4 there at 20 29.3 / 30.2, at 32 51.6 / 31.9.
+// Measured at 16384 channels and not between there and 65536; the length of the reduction has no part in
+// it, which leaves one expert of many rows short of workgroups (dense layer, d 8192, f 24576: 124 us at
+// 32 tokens, 260 at 33, where int8 weights take 187 and 145).
 constexpr long kMxFewTilesRowsPerExpert = 32;
 constexpr long kMxFewTilesWideRowsPerExpert = 20;
 constexpr long kMxFewTilesChannels = 16384;

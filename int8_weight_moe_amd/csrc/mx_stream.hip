@@ -16,9 +16,9 @@
 // Items are numbered over the experts that have rows. Sums are fp32; with few
 // items the reduction is cut into KS slices of whole scale groups, streamed by
 // the KS waves of a workgroup and added through LDS in ascending order.
-// Bound by HBM: down of 64 tokens (d 8192, f 24576, E 16) 279 us, 6170 GB/s of codes,
-// scales and rows; gate/up of one token (d 4096, f 14336, two experts) 23.0 us, 5430
-// GB/s, start and end of the launch included; the MXFP4 product of 17 tokens 71.1 us (65.7 on inputs used before).
+// Bound by HBM: down of 64 tokens (d 8192, f 24576, E 16) 283 us, 6080 GB/s of codes,
+// scales and rows; gate/up of one token (d 4096, f 14336, two experts) 23.2 us, 5370
+// GB/s, start and end of the launch included; the MXFP4 product of 17 tokens 68.5 us.
 #include "kernels.h"
 #include "mx_common.h"
 
@@ -281,8 +281,8 @@ int stream_slices(long items, int groups) {
 // items more waves (gate/up of one token: 25.3 us for 16 channels, 27.3 for 32;
 // down of one token: 15.4 us for 32, 20.5 for 64). MXFP4 activations are a
 // quarter of the bytes: 32 channels pay for one matrix with many items (64
-// tokens, d 24576, f 8192: 306 us for 16 channels, 282 for 32; 17 tokens, d 4096,
-// f 14336: 68 and 74). N is a multiple of 128, so every width divides it.
+// tokens, d 24576, f 8192: 343 us for 16 channels, 282 for 32; 17 tokens, d 4096,
+// f 14336: 69.4 and 68.3). N is a multiple of 128, so every width divides it.
 int stream_width(const MxArgs& a) {
   if (a.a_s) return !a.w1 && stream_items(a, 2) >= 4096 ? 2 : 1;
   if (a.w1) return stream_items(a, 2) >= 1024 ? 2 : 1;

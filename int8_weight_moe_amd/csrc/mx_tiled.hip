@@ -15,19 +15,22 @@
 //                is 256 bytes of a bf16 row (128 columns) or 128 bytes of codes
 //                (256 columns). The 16-byte chunks of a row are XOR-swizzled by
 //                the row number, so the fragment reads (16 rows at one chunk)
-//                meet no bank conflict. MXFP4 scales of the rows: a dword (four
-//                scale groups) per row and block, four blocks at a time.
+//                meet no bank conflict with MXFP4 rows (counted: 0); with bf16
+//                rows conflicts take 18% of the busy cycles. MXFP4 scales of the
+//                rows: a dword (four scale groups) per row and block, four
+//                blocks at a time.
 // bf16 activations: the codes become bf16 in registers, exactly, scale
 // included, and feed 16x16x32 bf16 MFMAs; MXFP4: the 16x16x128 scaled MFMA takes
 // both operands as read. Channels are MFMA rows and tokens MFMA columns, so a
 // lane ends with four consecutive channels of one row. Sums are fp32.
 // Tile order as in ffn_tiled.hip: groups of row tiles of one expert take every
 // channel tile in turn, in eight contiguous XCD queues.
-// Bound by MFMA rate and, in large products, by power: gate/up of 8192 tokens (d
-// 4096, f 14336, E 16) 2647 us, 1454 TFLOP/s, where a library bf16 product of 8192^3
-// reaches 1383; the same with MXFP4 activations 1112 us, 3460 TFLOP/s, the down product
-// of 16384 tokens (d 24576, f 8192) 3305 us, 3992 TFLOP/s (a library MXFP4 product of
-// 16384^3: 3364): MFMA busy 57% of the cycles at 1.5 GHz. Not faster: 32x32 MFMAs (5 to
+// Bound by the MFMA rate at the clock that power leaves (1.5 to 1.8 of 2.4 GHz) and by
+// the waits at each step: gate/up of 8192 tokens (d 4096, f 14336, E 16) 2727 us, 1411
+// TFLOP/s, MFMA busy 72% of the cycles at 1.7 GHz, where a library bf16 product of that
+// size reaches 1436; the same with MXFP4 activations 1143 us, 3366 TFLOP/s, 44% at 1.8 GHz;
+// the down product of 16384 tokens (d 24576, f 8192) 3366 us, 3919 TFLOP/s, 57% at 1.5 GHz
+// (a library MXFP4 product of 16384^3: 3462). Not faster: 32x32 MFMAs (5 to
 // 9% slower), 256-row tiles of eight waves (4 to 7%), non-temporal weights (5 to 40%).
 // Rows past the segment read row 0 of the tile and channels past N read channel
 // 0; their results are not stored.
