@@ -419,8 +419,8 @@ moe_status moe_grouped_mm_mxfp4(const moe_shape* shape, const uint8_t* a_q, cons
 
 /* The expert FFN with MXFP4 weights AND activations, on the permuted rows:
  * x is quantized per token, gate/up with SwiGLU gives h (bf16), h is quantized
- * per row, down gives y_rows. As moe_expert_ffn with 4-bit products (four times
- * the bf16 rate) and the rounding of 4-bit activations.
+ * per row, down gives y_rows. As moe_expert_ffn with 4-bit products (2.5
+ * times as fast at prefill) and the rounding of 4-bit activations.
  *   weight_fmt MOE_W_MXFP4; act_dtype is x's type; d, f multiples of 128;
  *   workspace >= moe_expert_ffn_mxfp4_workspace_size bytes. */
 moe_status moe_expert_ffn_mxfp4_workspace_size(const moe_shape* shape, size_t* bytes);

@@ -177,3 +177,87 @@ def test_product_of_a_shard(counts, T, K, path):
     ref, bound = product_bound(omx.dequantize(*a), omx.dequantize(*w), off, slots // K)
     check(out, ref, bound, int(off[-1]), "product")
     assert (out[int(off[-1]):] == 7.0).all()
+
+
+# ------------------------------------------------------------------ far rows: the same bits as on their own
+
+def _halves(n, k=64):
+    return slice(0, k), slice(n // 2, n // 2 + k), slice(n - k, n)
+
+
+@pytest.mark.parametrize("rows", [50000, 100000, 140000])
+def test_far_rows_of_codes(rows):
+    """Codes of 1.5, 3.1 and 4.3 GiB (past 2^31 bytes; past 2^32 the streaming kernel takes them on every schedule):
+    exact sums, so every row gives what it gives on its own, on either schedule."""
+    d, f = 65536, 128
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    a_q, a_s = draw((rows,), d, gen, 120, 122)
+    # one element in 64 of a weight row is not zero: at most 1024 products of halves and steps of 2, exact in fp32
+    w_q, w_s = draw((1, f), d, gen, 120, 121)
+    w_q = torch.where(torch.arange(d // 2, device="cuda") % 32 == 5, w_q & 15, 0).to(torch.uint8)
+    wt = m.moe_pack_mxfp4(w_q, w_s)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    out = m.moe_grouped_mm_mxfp4(a_q, a_s, off, *wt, torch.float32, path=MOE_PATH_TILED)
+    for r in _halves(rows):
+        ref = (values(a_q[r], a_s[r]) @ values(w_q[0], w_s[0]).t().contiguous()).float()
+        assert torch.equal(out[r], ref)
+
+
+def test_far_rows_of_h_on_the_tiled_schedule():
+    """h of 3 GiB: byte offsets past 2^31 in the tiled kernel."""
+    S, f, d, E = 65536, 24576, 128, 2
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, s = draw((E, d), f, gen)
+    wt = m.moe_pack_mxfp4(q, s)
+    gate = torch.empty(1, dtype=torch.uint8, device="cuda").expand(E, f, d // 2)
+    ex = m.Int8Experts(gate, gate, wt[0], gate, gate, wt[1], fmt=m.MOE_W_MXFP4)
+    h = torch.randn(S, f, generator=gen, device="cuda", dtype=torch.bfloat16)
+    off = torch.tensor([0, 1000, S], dtype=torch.int32, device="cuda")
+    y = m.moe_expert_down(h, off, ex, S, 1, path=MOE_PATH_TILED)
+    for r in (slice(0, 64), slice(1000, 1064), slice(S - 64, S)):
+        a, w = h[r].double(), values(q[0 if r.start == 0 else 1], s[0 if r.start == 0 else 1]).t().contiguous()
+        assert ((y[r].double() - a @ w).abs() <= f * 2.0 ** -23 * (a.abs() @ w.abs())).all()
+
+
+def test_far_rows_of_the_quantizer():
+    """2^33 numbers and some more in one call (two launches), both ways; and tiled rows past 2^32 numbers."""
+    cols, rows = 1024, (1 << 23) + 100
+    w = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    for r in (*_halves(rows), slice((1 << 23) - 32, (1 << 23) + 32)):
+        w[r] = torch.randn(64, cols, device="cuda").to(torch.bfloat16)
+    q, s = m.moe_quantize_mxfp4(w)
+    back = m.moe_dequantize_mxfp4(q, s, torch.bfloat16)
+    for r in (*_halves(rows), slice((1 << 23) - 32, (1 << 23) + 32)):
+        q1, s1 = m.moe_quantize_mxfp4(w[r])
+        assert torch.equal(q[r], q1) and torch.equal(s[r], s1)
+        assert torch.equal(back[r], m.moe_dequantize_mxfp4(q1, s1, torch.bfloat16)) and back[r].any()
+    del w, q, s, back
+    cols, rows = 8192, 16 * 40000
+    w = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    for r in _halves(rows):
+        w[r] = torch.randn(64, cols, device="cuda").to(torch.bfloat16)
+    q, s = m.moe_quantize_mxfp4(w, tiled=True)
+    back = m.moe_dequantize_mxfp4(q, s, torch.bfloat16, tiled=True)
+    rq, rs = m.moe_quantize_mxfp4(w)
+    pq, ps = m.moe_pack_mxfp4(rq, rs)
+    assert torch.equal(q, pq) and torch.equal(s, ps)
+    for r in _halves(rows):
+        q1, s1 = m.moe_quantize_mxfp4(w[r], tiled=True)
+        assert torch.equal(q[r], q1) and torch.equal(s[r], s1) and q1.any()
+        assert torch.equal(back[r], m.moe_dequantize_mxfp4(q1, s1, torch.bfloat16, tiled=True))
+
+
+def test_far_tokens_of_the_norms():
+    """Past 2^31 elements: a token's numbers are those of the same token in a short batch of the same kernel's spread."""
+    T, d = 40000, 65536
+    y, res = (torch.zeros(T, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for t in (y, res):
+        for r in _halves(T):
+            t[r] = torch.randn(64, d, device="cuda").to(torch.bfloat16)
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    n = m.moe_norm_pre(y, w)
+    out, nxt = m.moe_norm_post(y, res, weight=w, next_weight=w)
+    for r in _halves(T):
+        assert torch.equal(n[r], m.moe_norm_pre(y[r], w)) and n[r].any()
+        o1, n1 = m.moe_norm_post(y[r], res[r], weight=w, next_weight=w)
+        assert torch.equal(out[r], o1) and torch.equal(nxt[r], n1)
