@@ -457,13 +457,14 @@ typedef struct moe_post {
 
 /* y [T, d], residual [T, d], out [T, d], next [T, d] (NULL without next_weight),
  * all act_dtype; out may be residual or y, next may be residual or y but not out;
- * other overlaps are refused (MOE_ERR_UNSUPPORTED). */
+ * other overlaps of these, and of out or next with post's arrays, are refused
+ * (MOE_ERR_UNSUPPORTED). */
 moe_status moe_norm_post(const moe_shape* shape, const moe_post* post, const void* y, const void* residual, void* out,
                          void* next, hipStream_t stream);
 
 /* The same with y taken from the experts' rows, as moe_combine does (K = 1..8,
  * a slot with row -1 contributes nothing) but unrounded: one pass in place of
- * the combine and the norm. */
+ * the combine and the norm. out and next may not overlap y_rows either. */
 moe_status moe_combine_post(const moe_shape* shape, const moe_post* post, const float* y_rows,
                             const int32_t* slot_to_row, const float* topk_w, const void* residual, void* out,
                             void* next, hipStream_t stream);

@@ -462,6 +462,29 @@ moe_status check_post(const moe_shape* s, const moe_post* p, const void* residua
   return MOE_OK;
 }
 
+// What every token's workgroup reads (post's arrays, the experts' rows) may not
+// lie where another's writes out and next.
+moe_status check_post_reads(const moe_shape* s, const moe_post* p, const float* y_rows, const void* out,
+                            const void* next) {
+  const size_t elem = s->act_dtype == MOE_BF16 ? 2 : 4, row = s->d * elem, bytes = s->T * row;
+  const size_t gate_rows = p->gate ? ((size_t)s->T + p->gate_tokens - 1) / p->gate_tokens : 0;
+  const struct {
+    const char* name;
+    const void* ptr;
+    size_t bytes;
+  } reads[] = {{"weight", p->weight, row},
+               {"gate", p->gate, gate_rows * row},
+               {"next_weight", p->next_weight, row},
+               {"y_rows", y_rows, (size_t)s->T * s->K * s->d * 4}};
+  for (const auto& r : reads)
+    for (const void* w : {out, p->next_weight ? next : nullptr}) {
+      const uintptr_t u = reinterpret_cast<uintptr_t>(r.ptr), v = reinterpret_cast<uintptr_t>(w);
+      if (r.ptr && w && u < v + bytes && v < u + r.bytes)
+        return fail(MOE_ERR_UNSUPPORTED, "%s overlaps %s", w == out ? "out" : "next", r.name);
+    }
+  return MOE_OK;
+}
+
 moe::NormArgs post_args(const moe_shape* s, const moe_post* p, const void* residual, void* out, void* next) {
   moe::NormArgs a = {};
   a.act_bf16 = s->act_dtype == MOE_BF16;
@@ -1129,6 +1152,7 @@ moe_status moe_norm_post(const moe_shape* s, const moe_post* post, const void* y
   REQUIRE_PTR(y);
   if (overlap(s, out, y)) return fail(MOE_ERR_UNSUPPORTED, "out overlaps y and is not y");
   if (post->next_weight && overlap(s, next, y)) return fail(MOE_ERR_UNSUPPORTED, "next overlaps y");
+  if ((st = check_post_reads(s, post, nullptr, out, next)) != MOE_OK) return st;
   moe::NormArgs a = post_args(s, post, residual, out, next);
   a.x = y;
   const hipError_t e = moe::launch_block_norm(a, stream);
@@ -1145,6 +1169,7 @@ moe_status moe_combine_post(const moe_shape* s, const moe_post* post, const floa
   REQUIRE_PTR(y_rows);
   REQUIRE_PTR(slot_to_row);
   REQUIRE_PTR(topk_w);
+  if ((st = check_post_reads(s, post, y_rows, out, next)) != MOE_OK) return st;
   if (debug_on() && (st = debug_rows(s, slot_to_row, stream)) != MOE_OK) return st;
   moe::NormArgs a = post_args(s, post, residual, out, next);
   a.y_rows = y_rows;
@@ -1193,6 +1218,7 @@ moe_status moe_block_forward(const moe_shape* s, const void* residual, const voi
   if (!aligned16(topk_ids_out)) return fail(MOE_ERR_ALIGN, "topk_ids_out is not 16-byte aligned");
   if (!aligned16(topk_w_out)) return fail(MOE_ERR_ALIGN, "topk_w_out is not 16-byte aligned");
   if (!aligned16(x)) return fail(MOE_ERR_ALIGN, "x is not 16-byte aligned");
+  if ((st = check_post_reads(s, post, nullptr, out, next)) != MOE_OK) return st;
   moe::NormArgs pa = post_args(s, post, residual, out, next);
   if (pre_weight) {
     moe::NormArgs a = {};

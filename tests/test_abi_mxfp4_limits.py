@@ -92,3 +92,27 @@ def test_product_takes_more_slots_a_token_than_experts(lib):
         assert lib.moe_expert_ffn_mxfp4_workspace_size(_shape(E=E, K=K), ctypes.byref(n)) == SHAPE
         assert lib.moe_workspace_size(_shape(E=E, K=K), ctypes.byref(n)) == SHAPE
     assert mm(_shape(K=9)) == SHAPE and mm(_shape(E=1, K=9)) == SHAPE and mm(_shape(K=0)) == SHAPE
+
+
+def test_norm_outputs_over_what_other_tokens_read_are_refused(lib):
+    """out or next over the experts' rows, the weights or a shared gate would change what later tokens read."""
+    s = _shape(weight_fmt=0)                                            # 32 tokens of 512 bytes; y_rows 64 of 1 KiB
+    at = lambda n: ctypes.c_void_p(0x100000 + n)
+    far = lambda i: ctypes.c_void_p(0x200000 + 0x10000 * i)
+    combine = lambda post, y_rows, out, nxt: lib.moe_combine_post(s, post, y_rows, far(0), far(1), far(2), out, nxt, None)
+    both = _post(weight=far(3), next_weight=far(4))
+    for d in (0, 16, 64 * 1024 - 16):
+        assert combine(both, at(0), at(d), far(5)) == UNSUPPORTED and b"y_rows" in lib.moe_last_error()
+        assert combine(both, at(0), far(5), at(d)) == UNSUPPORTED
+    assert combine(both, at(32 * 512 - 16), at(0), far(5)) == UNSUPPORTED
+    for name, size in (("weight", 512), ("next_weight", 512), ("gate", 11 * 512)):
+        arrays = dict(weight=far(3), next_weight=far(4), gate_tokens=3)
+        arrays[name] = at(0)
+        post = _post(**arrays)
+        for out, nxt in ((at(size - 16), far(5)), (far(5), at(size - 16)), (at(-32 * 512 + 16), far(5))):
+            assert lib.moe_norm_post(s, post, far(6), far(7), out, nxt, None) == UNSUPPORTED, name
+            assert name.encode() in lib.moe_last_error()
+            assert combine(post, far(8), out, nxt) == UNSUPPORTED, name
+    blk = _shape()
+    assert lib.moe_block_forward(blk, far(0), far(1), 1e-6, None, _post(weight=at(0)), A, None, A, A, A, A, A, A, at(16),
+                                 None, None, None, A, BIG, None) == UNSUPPORTED
