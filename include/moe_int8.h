@@ -146,7 +146,7 @@ typedef struct moe_shape {
 } moe_shape;
 
 /* ABI version of this header (bumped on any signature change, and with new calls). */
-#define MOE_ABI_VERSION 7
+#define MOE_ABI_VERSION 8
 int32_t moe_abi_version(void);
 
 /* Static description of a status code. */
@@ -429,6 +429,63 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* shape, const void* x, const int
                                 const uint8_t* w_down, const uint8_t* s_gate, const uint8_t* s_up,
                                 const uint8_t* s_down, float* y_rows, void* workspace, size_t workspace_bytes,
                                 hipStream_t stream);
+
+/* ---------------------------------------------------------------- gated routing
+ * moe_route with a choice of scores, a bias that counts for the choice only (it
+ * balances the experts' load), groups of experts, and weights as they are or
+ * renormalised, scaled:
+ *   l_e = x . router_w[e] (+ router_bias[e]);  s = softmax(l) over the E experts, or s_e = sigmoid(l_e)
+ *   c_e = s_e + select_bias[e]
+ *   a group is E / groups consecutive experts; its value is the largest c in it,
+ *     or the sum of its two largest; the group_topk groups of the largest values stay
+ *   of their experts the K with the largest c are taken, in descending order;
+ *   w_k = s_k, divided by the sum of the K if renorm (0 if that is 0), times scale.
+ * Ties, among groups too, go to the lower index. An expert whose c is -inf (a
+ * bias of -inf takes it out of service) or NaN is never taken, and counts as
+ * -inf for its group; where fewer than K are left, the other ids are -1 with
+ * weight 0 (moe_permute does not place such slots, and they add nothing to the
+ * combine). A token whose scores are no numbers gets ids of -1.
+ * The values that decide the choice are compared in 64 bits, from exact inputs;
+ * the weights come from logits with fp32 sums. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 };
+
+typedef struct moe_gate {
+  const float* select_bias; /* [E], or NULL: 0                                     */
+  int32_t score;            /* MOE_SCORE_*                                         */
+  int32_t groups;           /* 1..64, divides E; 1: no groups                      */
+  int32_t group_topk;       /* 1..groups, group_topk * E / groups >= K             */
+  int32_t group_by;         /* MOE_GROUP_*; TOP2 with two experts a group at least */
+  int32_t renorm;           /* 0 or 1                                              */
+  float scale;              /* finite                                              */
+} moe_gate;
+
+/* As moe_route; here shape->E may be up to 256 (a GPU that holds some of them
+ * permutes ids less its first expert's: ids outside [0, its experts) are not placed). */
+moe_status moe_route_gated(const moe_shape* shape, const moe_gate* gate, const void* x, const void* router_w,
+                           const float* router_bias, int32_t* topk_ids, float* topk_w, hipStream_t stream);
+
+/* ---------------------------------------------------------------- int8 activations
+ * Products of int8 rows, a scale each (moe_quantize_rows with fp32 scales), and the
+ * layer's int8 weights, with both operands as they are in the int8 MFMA.
+ *
+ * Grouped by expert: row r of expert e's segment [off[e], off[e+1]):
+ *     p[r, n] = a_s[row(r)] * w_s[e, n] * sum_k a_q[row(r), k] * w_q[e, n, k],    n < f, k < d
+ *     out = p, or with a second matrix silu(p) * p2.
+ *   shape: T tokens, K slots a token (rows of out: T*K; 1..8, more than E too: a
+ *     shard holds some of a token's experts), d the reduction, f the output
+ *     channels, E experts; weight_fmt MOE_W_INT8 (else MOE_ERR_DTYPE); act_dtype is
+ *     out's type, scale_dtype that of w_s, w2_s; ffn_path as for the expert FFN.
+ *   a_q, a_s  [rows, d] int8 row-major, [rows] fp32. With sorted_slots [T*K]: rows
+ *     = T, row(r) = sorted_slots[r] / K; NULL: rows = T*K, row(r) = r.
+ *   w_q, w_s, w2_q, w2_s  [E, f, d] tiled codes (moe_pack_rows) and [E, f] scales
+ *     (w2_*: both NULL for the plain product).
+ *   out [T*K, f] act_dtype, not overlapping any input; rows past off[E] are left untouched.
+ * The sums are exact in int32; a sum becomes fp32 and takes its two scales there.
+ * Any segment lengths. The schedules give the same bits. */
+moe_status moe_grouped_mm_int8(const moe_shape* shape, const int8_t* a_q, const float* a_s,
+                               const int32_t* expert_offsets, const int32_t* sorted_slots, const int8_t* w_q,
+                               const void* w_s, const int8_t* w2_q, const void* w2_s, void* out, hipStream_t stream);
 
 /* ---------------------------------------------------------------- norms around the layer
  * rms(v) = v / sqrt(mean(v^2) + eps) over the d elements of a token, in fp32 (a

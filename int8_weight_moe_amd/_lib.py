@@ -11,7 +11,7 @@ import os
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe_int8.so")
 
-ABI_VERSION = 7
+ABI_VERSION = 8
 MOE_OK = 0
 STATUS_NAMES = {
     0: "MOE_OK", 1: "MOE_ERR_NULL", 2: "MOE_ERR_SHAPE", 3: "MOE_ERR_DTYPE", 4: "MOE_ERR_ALIGN",
@@ -22,6 +22,8 @@ MOE_F32, MOE_BF16 = 0, 1
 MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_TILED = 0, 1, 2
 MOE_W_INT8, MOE_W_BF16, MOE_W_FP8, MOE_W_MXFP4 = 0, 1, 2, 4
 MOE_MX_ROWS, MOE_MX_TILED = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
 
 # every symbol the header declares
 EXPORTS = (
@@ -32,6 +34,7 @@ EXPORTS = (
     "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_pack_mxfp4", "moe_grouped_mm_mxfp4",
     "moe_expert_ffn_mxfp4_workspace_size", "moe_expert_ffn_mxfp4", "moe_norm_pre", "moe_norm_post",
     "moe_combine_post", "moe_block_workspace_size", "moe_block_forward",
+    "moe_route_gated", "moe_grouped_mm_int8",
 )
 
 
@@ -47,6 +50,12 @@ class MoePost(ctypes.Structure):
                 ("eps", ctypes.c_float), ("next_eps", ctypes.c_float)]
 
 
+class MoeGate(ctypes.Structure):
+    _fields_ = [("select_bias", ctypes.c_void_p), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("group_topk", ctypes.c_int32), ("group_by", ctypes.c_int32), ("renorm", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {message}")
@@ -56,6 +65,7 @@ class MoeError(RuntimeError):
 _P = ctypes.c_void_p
 _SHAPE = ctypes.POINTER(MoeShape)
 _POST = ctypes.POINTER(MoePost)
+_GATE = ctypes.POINTER(MoeGate)
 _I32, _I64, _F32, _SIZE = ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
 _SIGS = {
     "moe_abi_version": (ctypes.c_int32, []),
@@ -86,6 +96,8 @@ _SIGS = {
     "moe_grouped_mm_mxfp4": (_I32, [_SHAPE] + [_P] * 10),
     "moe_expert_ffn_mxfp4_workspace_size": (_I32, [_SHAPE, ctypes.POINTER(_SIZE)]),
     "moe_expert_ffn_mxfp4": (_I32, [_SHAPE] + [_P] * 11 + [_SIZE, _P]),
+    "moe_route_gated": (_I32, [_SHAPE, _GATE] + [_P] * 6),
+    "moe_grouped_mm_int8": (_I32, [_SHAPE] + [_P] * 10),
     "moe_norm_pre": (_I32, [_SHAPE, _P, _P, _F32, _P, _P]),
     "moe_norm_post": (_I32, [_SHAPE, _POST, _P, _P, _P, _P, _P]),
     "moe_combine_post": (_I32, [_SHAPE, _POST, _P, _P, _P, _P, _P, _P, _P]),

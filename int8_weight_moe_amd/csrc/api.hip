@@ -116,12 +116,12 @@ constexpr long kMxFewTilesWideRowsPerExpert = 20;
 constexpr long kMxFewTilesChannels = 16384;
 
 // routes: the call's K experts of a token are distinct ones of the E.
-moe_status check_shape(const moe_shape* s, bool routes = true) {
+moe_status check_shape(const moe_shape* s, bool routes = true, int max_experts = 64) {
   if (!s) return fail(MOE_ERR_NULL, "shape is NULL");
   if (s->T < 0) return fail(MOE_ERR_SHAPE, "T=%d must be >= 0", s->T);
   if (s->d < 64 || s->d > 65536 || s->d % 64) return fail(MOE_ERR_SHAPE, "d=%d must be a multiple of 64 in [64, 65536]", s->d);
   if (s->f < 64 || s->f > 131072 || s->f % 64) return fail(MOE_ERR_SHAPE, "f=%d must be a multiple of 64 in [64, 131072]", s->f);
-  if (s->E < 1 || s->E > 64) return fail(MOE_ERR_SHAPE, "E=%d must be in [1, 64]", s->E);
+  if (s->E < 1 || s->E > max_experts) return fail(MOE_ERR_SHAPE, "E=%d must be in [1, %d]", s->E, max_experts);
   if (s->K < 1 || s->K > 8 || (routes && s->K > s->E))
     return fail(MOE_ERR_SHAPE, routes ? "K=%d must be in [1, min(E, 8)]" : "K=%d must be in [1, 8]", s->K);
   if ((long)s->T * s->K > (1L << 26)) return fail(MOE_ERR_SHAPE, "T*K=%ld exceeds 2^26", (long)s->T * s->K);
@@ -405,6 +405,71 @@ moe_status check_mx_shape(const moe_shape* s, bool routes) {
   return MOE_OK;
 }
 
+bool finite_f32(float v) { return v - v == 0.f; }
+
+// Shape of a product of int8 rows and int8 weights.
+moe_status check_i8_shape(const moe_shape* s, bool routes) {
+  const moe_status st = check_shape(s, routes);
+  if (st != MOE_OK) return st;
+  if (s->weight_fmt != MOE_W_INT8) return fail(MOE_ERR_DTYPE, "weight_fmt=%d: this call takes int8 weights", s->weight_fmt);
+  return MOE_OK;
+}
+
+// One product of int8 rows and weights; `call` and `what` name it in the log and in an error.
+moe_status run_i8(const char* call, const char* what, const moe_shape* s, const moe::I8Args& m, hipStream_t stream) {
+  if (log_on()) {
+    const moe::I8StreamPlan p = moe::i8_stream_plan(m);
+    fprintf(stderr, "[moe] %s %s: rows=%d reduction=%d channels=%d E=%d act=int8 weights=int8 out=%s%s; stream schedule, "
+            "%d-channel items, %d-row passes, reduction in %d slices\n", call, what, m.S, m.Kd, m.N, m.E,
+            m.out_bf16 ? "bf16" : "f32", m.w1 ? " SwiGLU" : "", p.channels, p.rows, p.slices);
+  }
+  const hipError_t e = moe::launch_i8_stream(m, stream);
+  if (e != hipSuccess) return hip_fail(e, what);
+  return MOE_OK;
+}
+
+// What a gate may be for this shape; select_bias is checked where it is read.
+moe_status check_gate(const moe_shape* s, const moe_gate* g) {
+  if (!g) return fail(MOE_ERR_NULL, "gate is NULL");
+  if (g->score != MOE_SCORE_SOFTMAX && g->score != MOE_SCORE_SIGMOID) return fail(MOE_ERR_SHAPE, "score=%d", g->score);
+  if (g->groups < 1 || g->groups > 64 || s->E % g->groups)
+    return fail(MOE_ERR_SHAPE, "groups=%d must be in [1, 64] and divide E=%d", g->groups, s->E);
+  if (g->group_topk < 1 || g->group_topk > g->groups)
+    return fail(MOE_ERR_SHAPE, "group_topk=%d must be in [1, groups=%d]", g->group_topk, g->groups);
+  if (g->group_topk * (s->E / g->groups) < s->K)
+    return fail(MOE_ERR_SHAPE, "%d groups of %d experts hold fewer than K=%d", g->group_topk, s->E / g->groups, s->K);
+  if (g->group_by != MOE_GROUP_MAX && g->group_by != MOE_GROUP_TOP2) return fail(MOE_ERR_SHAPE, "group_by=%d", g->group_by);
+  if (g->group_by == MOE_GROUP_TOP2 && g->groups > 1 && s->E / g->groups < 2)
+    return fail(MOE_ERR_SHAPE, "MOE_GROUP_TOP2 needs two experts a group, E=%d and groups=%d give one", s->E, g->groups);
+  if (g->renorm != 0 && g->renorm != 1) return fail(MOE_ERR_SHAPE, "renorm=%d must be 0 or 1", g->renorm);
+  if (!finite_f32(g->scale)) return fail(MOE_ERR_SHAPE, "scale=%g must be finite", (double)g->scale);
+  if (s->T > 0 && !aligned16(g->select_bias)) return fail(MOE_ERR_ALIGN, "select_bias is not 16-byte aligned");
+  return MOE_OK;
+}
+
+moe::GateArgs gate_args(const moe_shape* s, const moe_gate* g, const void* x, const void* router_w,
+                        const float* router_bias, int32_t* topk_ids, float* topk_w) {
+  moe::GateArgs a;
+  a.x = x;
+  a.router_w = router_w;
+  a.router_bias = router_bias;
+  a.select_bias = g->select_bias;
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  a.act_bf16 = s->act_dtype == MOE_BF16;
+  a.sigmoid = g->score == MOE_SCORE_SIGMOID;
+  a.top2 = g->group_by == MOE_GROUP_TOP2;
+  a.renorm = g->renorm != 0;
+  a.T = s->T;
+  a.d = s->d;
+  a.E = s->E;
+  a.K = s->K;
+  a.groups = g->groups;
+  a.group_topk = g->group_topk;
+  a.scale = g->scale;
+  return a;
+}
+
 // moe_block_forward's workspace: moe_forward's, then the normalised input.
 size_t block_x_bytes(const moe_shape* s) {
   return round_up((size_t)s->T * s->d * (s->act_dtype == MOE_BF16 ? 2 : 4));
@@ -427,8 +492,6 @@ MxFfnLayout mx_ffn_layout(const moe_shape* s) {
   L.total = o;
   return L;
 }
-
-bool finite_f32(float v) { return v - v == 0.f; }
 
 moe_status check_eps(const char* what, float eps) {
   if (!finite_f32(eps) || eps < 0.f) return fail(MOE_ERR_SHAPE, "%s=%g must be finite and not negative", what, (double)eps);
@@ -1119,6 +1182,61 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* s, const void* x, const int32_t
   m.N = s->d;
   m.Kd = s->f;
   return run_mx("moe_expert_ffn_mxfp4", "down", s, m, stream);
+}
+
+moe_status moe_route_gated(const moe_shape* s, const moe_gate* gate, const void* x, const void* router_w,
+                           const float* router_bias, int32_t* topk_ids, float* topk_w, hipStream_t stream) {
+  moe_status st = check_shape(s, true, 256);
+  if (st != MOE_OK) return st;
+  if ((st = check_gate(s, gate)) != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(router_w);
+  REQUIRE_PTR(topk_ids);
+  REQUIRE_PTR(topk_w);
+  if (!aligned16(router_bias)) return fail(MOE_ERR_ALIGN, "router_bias is not 16-byte aligned");
+  const hipError_t e = moe::launch_route_gated(gate_args(s, gate, x, router_w, router_bias, topk_ids, topk_w), stream);
+  if (e != hipSuccess) return hip_fail(e, "router launch");
+  return MOE_OK;
+}
+
+moe_status moe_grouped_mm_int8(const moe_shape* s, const int8_t* a_q, const float* a_s, const int32_t* expert_offsets,
+                               const int32_t* sorted_slots, const int8_t* w_q, const void* w_s, const int8_t* w2_q,
+                               const void* w2_s, void* out, hipStream_t stream) {
+  moe_status st = check_i8_shape(s, false);
+  if (st != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  REQUIRE_PTR(a_q);
+  REQUIRE_PTR(a_s);
+  REQUIRE_PTR(expert_offsets);
+  if (!aligned16(sorted_slots)) return fail(MOE_ERR_ALIGN, "sorted_slots is not 16-byte aligned");
+  REQUIRE_PTR(w_q);
+  REQUIRE_PTR(w_s);
+  if (w2_q || w2_s) {
+    REQUIRE_PTR(w2_q);
+    REQUIRE_PTR(w2_s);
+  }
+  REQUIRE_PTR(out);
+  if (debug_on() && (st = debug_inputs(s, expert_offsets, sorted_slots, stream)) != MOE_OK) return st;
+  moe::I8Args m;
+  m.a = a_q;
+  m.a_s = a_s;
+  m.offsets = expert_offsets;
+  m.sorted_slots = sorted_slots;
+  m.topk = s->K;
+  m.a_rows = sorted_slots ? s->T : (long)s->T * s->K;
+  m.w0 = w_q;
+  m.w1 = w2_q;
+  m.s0 = w_s;
+  m.s1 = w2_s;
+  m.scale_bf16 = s->scale_dtype == MOE_BF16;
+  m.out = out;
+  m.out_bf16 = s->act_dtype == MOE_BF16;
+  m.E = s->E;
+  m.N = s->f;
+  m.Kd = s->d;
+  m.S = s->T * s->K;
+  return run_i8("moe_grouped_mm_int8", "product", s, m, stream);
 }
 
 moe_status moe_norm_pre(const moe_shape* s, const void* x, const void* weight, float eps, void* n, hipStream_t stream) {

@@ -1,0 +1,193 @@
+// Products of int8 weights and int8 rows with few rows per expert (decode): the
+// weights are streamed from HBM once.
+//
+//   out[r, n] = a_s[row(r)] * w_s[n] * sum_k a_q[row(r), k] * w_q[n, k],   or   silu(p0) * p1
+//
+// for the rows r of every expert's segment. A wave owns one (expert, 16*NG output
+// channels) item and takes 16*RB rows a pass, with the channels as MFMA rows and
+// the tokens as MFMA columns. Per 64-wide step it reads one 1 KiB block per 16
+// channels and matrix (16 bytes a lane) and 16 bytes a lane of the rows, U steps
+// at a time: the rows of these steps are requested, then the weights of the next
+// ones, then the steps are computed (loads return in order, so waiting for the
+// rows does not wait for the weights behind them).
+// Items are numbered over the experts that have rows. With few items the
+// reduction is cut into KS slices, streamed by the KS waves of a workgroup and
+// added through LDS (integers: exact in any order).
+#include "i8_common.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kStreamWaves = 4;
+constexpr int block_waves(int KS) { return KS > 1 ? KS : kStreamWaves; }
+
+template <int NMAT, int NG, int RB, int KS, int U>
+__global__ __launch_bounds__(block_waves(KS) * kWave) void i8_stream_kernel(I8Args a) {
+  constexpr int IPW = block_waves(KS) / KS;   // items per workgroup
+  __shared__ i32x4 red[KS > 1 ? KS - 1 : 1][NG][NMAT][kWave];
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int li = lane & 15;
+  const int lg = lane >> 4;
+  const int N = a.N, n = a.Kd / kI8Step;      // steps of a row
+
+  const int gpe = N / (16 * NG);
+  const int item = blockIdx.x * IPW + wave / KS;
+  const int kslice = wave % KS;
+  const int te = item / gpe;
+  const int grp = item - te * gpe;
+  int e, row0, nrows;
+  // KS > 1: the workgroup is one item, so all its waves return here together
+  if (!find_touched_expert(a.offsets, a.E, te, e, row0, nrows)) return;
+  const int ch_base = grp * 16 * NG;
+
+  const int8_t* wp[NG][NMAT];
+#pragma unroll
+  for (int ng = 0; ng < NG; ++ng) {
+    const long block = (((long)e * N + ch_base + ng * 16) >> 4) * n;
+    wp[ng][0] = a.w0 + block * 1024 + 16 * lane;
+    if constexpr (NMAT == 2) wp[ng][1] = a.w1 + block * 1024 + 16 * lane;
+  }
+  const int s_begin = (int)((long)kslice * n / KS), s_end = (int)((long)(kslice + 1) * n / KS);
+
+  uint4 w[2][U][NG][NMAT];
+  auto load_w = [&](int s, uint4 (&wb)[U][NG][NMAT]) {
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (s + j < s_end)
+#pragma unroll
+        for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+          for (int m = 0; m < NMAT; ++m) wb[j][ng][m] = load_nt16(wp[ng][m] + (long)(s + j) * 1024);
+  };
+
+  for (int p0 = 0; p0 < nrows; p0 += 16 * RB) {
+    const int nrb = min(RB, (nrows - p0 + 15) >> 4);
+    // the first weights are requested before the row numbers are looked up
+    load_w(s_begin, w[0]);
+    const int8_t* ap[RB];
+    long src[RB];
+    bool aok[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int r = p0 + rb * 16 + li;
+      aok[rb] = r < nrows;
+      src[rb] = 0;
+      if (aok[rb]) src[rb] = a.sorted_slots ? a.sorted_slots[row0 + r] / a.topk : row0 + r;
+      ap[rb] = a.a + src[rb] * a.Kd + 16 * lg;
+    }
+    i32x4 acc[RB][NG][NMAT];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+        for (int m = 0; m < NMAT; ++m) acc[rb][ng][m] = i32x4{0, 0, 0, 0};
+
+    auto run = [&](auto nrbc) {
+      constexpr int NRB = decltype(nrbc)::value;   // row blocks present
+      auto unit = [&](int s, const uint4 (&wb)[U][NG][NMAT], uint4 (&wn)[U][NG][NMAT]) {
+        uint4 av[U][NRB];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+          for (int rb = 0; rb < NRB; ++rb) {
+            av[j][rb] = make_uint4(0, 0, 0, 0);
+            if (s + j < s_end && aok[rb]) av[j][rb] = *reinterpret_cast<const uint4*>(ap[rb] + (long)(s + j) * kI8Step);
+          }
+        load_w(s + U, wn);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+          if (s + j >= s_end) break;
+#pragma unroll
+          for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+            for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+              for (int rb = 0; rb < NRB; ++rb)
+                acc[rb][ng][m] = mfma_i8(as_i32x4(wb[j][ng][m]), as_i32x4(av[j][rb]), acc[rb][ng][m]);
+        }
+      };
+      for (int s = s_begin; s < s_end; s += 2 * U) {
+        unit(s, w[0], w[1]);
+        if (s + U < s_end) unit(s + U, w[1], w[0]);
+      }
+    };
+    if (RB == 1 || nrb == 1) {
+      run(int_constant<1>{});
+    } else {
+      run(int_constant<RB>{});
+    }
+
+    if constexpr (KS > 1) {
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb) {
+        if (rb < nrb) {
+          if (kslice > 0) {
+#pragma unroll
+            for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+              for (int m = 0; m < NMAT; ++m) red[kslice - 1][ng][m][lane] = acc[rb][ng][m];
+          }
+          __syncthreads();
+          if (kslice == 0) {
+            for (int j = 0; j < KS - 1; ++j)
+#pragma unroll
+              for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+                for (int m = 0; m < NMAT; ++m) acc[rb][ng][m] += red[j][ng][m][lane];
+          }
+          __syncthreads();
+        }
+      }
+      if (kslice > 0) continue;
+    }
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+      const int r = p0 + rb * 16 + li;
+      if (rb >= nrb || r >= nrows) continue;
+      const float as = a.a_s[src[rb]];
+#pragma unroll
+      for (int ng = 0; ng < NG; ++ng) {
+        const int ch = ch_base + ng * 16 + 4 * lg;
+        float4 ws[NMAT];
+        ws[0] = i8_scale4(a.s0, a.scale_bf16, (long)e * N + ch);
+        if constexpr (NMAT == 2) ws[1] = i8_scale4(a.s1, a.scale_bf16, (long)e * N + ch);
+        i8_store4<NMAT>(a.out, a.out_bf16, (long)(row0 + r) * N + ch, acc[rb][ng], ws, as);
+      }
+    }
+  }
+}
+
+// Items of 16*NG channels over the experts that can have rows (each has one of
+// the S at least).
+long stream_items(const I8Args& a, int NG) { return (long)min(a.E, a.S) * (a.N / (16 * NG)); }
+
+template <int NMAT, int NG, int RB, int KS, int U>
+hipError_t launch(const I8Args& a, hipStream_t stream) {
+  const long items = stream_items(a, NG);
+  hipLaunchKernelGGL((i8_stream_kernel<NMAT, NG, RB, KS, U>),
+                     dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves)),
+                     dim3(block_waves(KS) * kWave), 0, stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+I8StreamPlan i8_stream_plan(const I8Args& a) {
+  I8StreamPlan p;
+  p.channels = 16;
+  p.rows = a.S <= 8L * a.E ? 16 : 32;
+  p.slices = 1;
+  return p;
+}
+
+hipError_t launch_i8_stream(const I8Args& a, hipStream_t stream) {
+  const I8StreamPlan p = i8_stream_plan(a);
+  if (a.w1) return p.rows == 16 ? launch<2, 1, 1, 1, 2>(a, stream) : launch<2, 1, 2, 1, 2>(a, stream);
+  return p.rows == 16 ? launch<1, 1, 1, 1, 2>(a, stream) : launch<1, 1, 2, 1, 2>(a, stream);
+}
+
+}  // namespace moe

@@ -126,6 +126,43 @@ hipError_t launch_mx_stream(const MxArgs& a, hipStream_t stream);
 bool mx_tiled_offsets_fit(long rows, int cols, bool mx);
 hipError_t launch_mx_tiled(const MxArgs& a, hipStream_t stream);
 
+// Products of int8 weights and int8 rows, grouped by expert (i8_common.h).
+struct I8Args {
+  const int8_t* a;              // [., Kd] codes of the rows
+  const float* a_s;             // their scales
+  const int32_t* offsets;       // [E + 1]
+  const int32_t* sorted_slots;  // [S]: sorted row r reads row sorted_slots[r] / topk of a; null: row r
+  int topk;
+  long a_rows;                  // rows of a
+  const int8_t *w0, *w1;        // [E, N, Kd] codes, tiled; w1: out = silu(p0) * p1; null: out = p0
+  const void *s0, *s1;          // [E, N] scales
+  bool scale_bf16;              // else fp32
+  void* out;                    // [S, N]
+  bool out_bf16;                // else fp32
+  int E, N, Kd, S;
+};
+// What launch_i8_stream takes for these sizes: channels of an item (of each
+// matrix), rows a pass and slices of the reduction.
+struct I8StreamPlan {
+  int channels, rows, slices;
+};
+I8StreamPlan i8_stream_plan(const I8Args& a);
+hipError_t launch_i8_stream(const I8Args& a, hipStream_t stream);
+
+// Gated routing (route_gated.hip).
+struct GateArgs {
+  const void* x;             // [T, d]
+  const void* router_w;      // [E, d]
+  const float* router_bias;  // [E] or null
+  const float* select_bias;  // [E] or null
+  int32_t* topk_ids;         // [T, K]
+  float* topk_w;             // [T, K]
+  bool act_bf16, sigmoid, top2, renorm;
+  int T, d, E, K, groups, group_topk;
+  float scale;
+};
+hipError_t launch_route_gated(const GateArgs& a, hipStream_t stream);
+
 // Norms around the layer (block_norm.hip).
 struct NormArgs {
   bool act_bf16;               // x, residual, weights, gate, out, next

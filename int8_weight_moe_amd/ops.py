@@ -14,8 +14,9 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import (MOE_BF16, MOE_F32, MOE_MX_ROWS, MOE_MX_TILED, MOE_PATH_AUTO, MOE_PATH_STREAM,  # noqa: F401
-                   MOE_PATH_TILED, MOE_W_BF16, MOE_W_FP8, MOE_W_INT8, MOE_W_MXFP4, MoeError, MoePost, MoeShape)
+from ._lib import (MOE_BF16, MOE_F32, MOE_GROUP_MAX, MOE_GROUP_TOP2, MOE_MX_ROWS, MOE_MX_TILED,  # noqa: F401
+                   MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_TILED, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_W_BF16,
+                   MOE_W_FP8, MOE_W_INT8, MOE_W_MXFP4, MoeError, MoeGate, MoePost, MoeShape)
 
 _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -594,6 +595,87 @@ def moe_expert_ffn_mxfp4(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_s
         _arg("sorted_slots", sorted_slots, torch.int32, (T * K,)), *weights, _ptr(y_rows),
         _arg("workspace", workspace, torch.uint8), ctypes.c_size_t(workspace.numel()), _stream()))
     return y_rows
+
+
+# ---------------------------------------------------------------- gated routing, int8 activations
+
+@dataclasses.dataclass
+class Gate:
+    """How a router's scores become the choice of experts and their weights (moe_route_gated).
+
+    score MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID; select_bias [E] fp32 is added to
+    the scores for the choice only (-inf takes an expert out of service); groups of
+    E / groups consecutive experts, of which the group_topk of the largest value stay
+    (group_by MOE_GROUP_MAX: the largest choice value of the group, MOE_GROUP_TOP2:
+    the sum of its two largest); renorm: the weights are divided by their sum; scale
+    multiplies them.
+    """
+    score: int = MOE_SCORE_SOFTMAX
+    select_bias: Optional[torch.Tensor] = None
+    groups: int = 1
+    group_topk: int = 1
+    group_by: int = MOE_GROUP_MAX
+    renorm: bool = True
+    scale: float = 1.0
+
+    def struct(self, E: int) -> MoeGate:
+        _check_sizes(self.groups, self.group_topk)
+        return MoeGate(_arg("select_bias", self.select_bias, torch.float32, (E,)), self.score, self.groups,
+                       self.group_topk, self.group_by, 1 if self.renorm else 0, self.scale)
+
+
+def moe_route_gated(x: torch.Tensor, router_w: torch.Tensor, bias: Optional[torch.Tensor], K: int, gate: Gate,
+                    ids: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None):
+    """Router with a Gate: x [T, d], router_w [E, d] (E up to 256), bias [E] fp32 added to the logits or None.
+    Returns (topk_ids int32 [T, K], topk_w fp32 [T, K]); ids of -1 (weight 0) where fewer than K experts can
+    be taken."""
+    lib = _lib_handle()
+    T, d = x.shape
+    E = router_w.shape[0]
+    shape = make_shape(T, d, 64, E, K, x.dtype, torch.float32)
+    g = gate.struct(E)
+    if ids is None:
+        ids = torch.empty((T, K), dtype=torch.int32, device=x.device)
+    if w is None:
+        w = torch.empty((T, K), dtype=torch.float32, device=x.device)
+    _lib.check(lib.moe_route_gated(ctypes.byref(shape), ctypes.byref(g), _arg("x", x, None),
+                                   _arg("router_w", router_w, x.dtype, (E, d)), _arg("bias", bias, torch.float32, (E,)),
+                                   _arg("ids", ids, torch.int32, (T, K)), _arg("w", w, torch.float32, (T, K)),
+                                   _stream()))
+    return ids, w
+
+
+def moe_grouped_mm_int8(a_q: torch.Tensor, a_s: torch.Tensor, expert_offsets: torch.Tensor, w_q: torch.Tensor,
+                        w_s: torch.Tensor, out_dtype: torch.dtype, sorted_slots: Optional[torch.Tensor] = None,
+                        K: int = 1, w2_q: Optional[torch.Tensor] = None, w2_s: Optional[torch.Tensor] = None,
+                        path: int = MOE_PATH_AUTO, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Products grouped by expert of int8 rows and int8 matrices, with a scale for each row and each channel.
+
+    a_q [rows, d] int8, a_s [rows] fp32 (moe_quantize_rows with fp32 scales); w_q
+    [E, f, d] tiled codes (moe_pack_rows), w_s [E, f] fp32 or bf16. With sorted_slots
+    [rows*K] sorted row r reads a's row sorted_slots[r] // K, else its own row r (K =
+    1). With w2_*: silu(W a) * (W2 a). Returns out [rows*K, f] in out_dtype (rows past
+    the last segment are left as they are: uninitialised unless `out` is given)."""
+    lib = _lib_handle()
+    if a_q.dim() != 2 or w_q.dim() != 3:
+        raise ValueError("a_q must be [rows, d] and w_q [E, f, d]")
+    rows, d = a_q.shape
+    E, f = w_q.shape[0], w_q.shape[1]
+    if sorted_slots is None and K != 1:
+        raise ValueError("K is the slots per row of sorted_slots: 1 without it")
+    if (w2_q is None) != (w2_s is None):
+        raise ValueError("w2_q and w2_s are given together")
+    _check_sizes(rows, d, f, E, K)
+    shape = MoeShape(rows, d, f, E, K, _dtype_code(out_dtype), _dtype_code(w_s.dtype), path, MOE_W_INT8)
+    if out is None:
+        out = torch.empty((rows * K, f), dtype=out_dtype, device=a_q.device)
+    i8, i32, w_shape, s_shape = torch.int8, torch.int32, (E, f, d), (E, f)
+    _lib.check(lib.moe_grouped_mm_int8(
+        ctypes.byref(shape), _arg("a_q", a_q, i8), _arg("a_s", a_s, torch.float32, (rows,)),
+        _arg("expert_offsets", expert_offsets, i32, (E + 1,)), _arg("sorted_slots", sorted_slots, i32, (rows * K,)),
+        _arg("w_q", w_q, i8, w_shape), _arg("w_s", w_s, w_s.dtype, s_shape), _arg("w2_q", w2_q, i8, w_shape),
+        _arg("w2_s", w2_s, w_s.dtype, s_shape), _arg("out", out, out_dtype, (rows * K, f)), _stream()))
+    return out
 
 
 def moe_norm_pre(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,

@@ -19,6 +19,8 @@ Modules:
            or bf16 weights with unit scales).
   mxfp4 -- MXFP4 encoding, quantizer, tiled layout and grouped products.
   norm  -- the RMS norms before and after the layer.
+  gate  -- gated routing: scores, choice bias, groups, weights.
+  int8  -- grouped products of int8 rows and int8 matrices.
 
 Readings taken where the paper is silent:
   * gate = softmax over all n logits, keep the K largest, renormalise;
@@ -31,4 +33,4 @@ Readings taken where the paper is silent:
 Every function's parity is pinned by tests that do not reuse its own formula:
 see tests/test_oracle_*.py.
 """
-from . import quant, fp8, moe, mxfp4, norm  # noqa: F401
+from . import quant, fp8, moe, mxfp4, norm, gate, int8  # noqa: F401
