@@ -115,6 +115,9 @@ constexpr long kMxFewTilesRowsPerExpert = 32;
 constexpr long kMxFewTilesWideRowsPerExpert = 20;
 constexpr long kMxFewTilesChannels = 16384;
 
+// Rows an expert on average up to which a product of int8 rows streams its weights.
+constexpr long kI8StreamRowsPerExpert = 32;
+
 // routes: the call's K experts of a token are distinct ones of the E.
 moe_status check_shape(const moe_shape* s, bool routes = true, int max_experts = 64) {
   if (!s) return fail(MOE_ERR_NULL, "shape is NULL");
@@ -417,13 +420,20 @@ moe_status check_i8_shape(const moe_shape* s, bool routes) {
 
 // One product of int8 rows and weights; `call` and `what` name it in the log and in an error.
 moe_status run_i8(const char* call, const char* what, const moe_shape* s, const moe::I8Args& m, hipStream_t stream) {
+  bool by_stream = s->ffn_path == MOE_PATH_STREAM || (s->ffn_path == MOE_PATH_AUTO && m.S <= kI8StreamRowsPerExpert * m.E);
+  // rows past the tiled kernel's 32-bit offsets
+  if (!moe::i8_tiled_offsets_fit(m.a_rows, m.Kd)) by_stream = true;
   if (log_on()) {
-    const moe::I8StreamPlan p = moe::i8_stream_plan(m);
-    fprintf(stderr, "[moe] %s %s: rows=%d reduction=%d channels=%d E=%d act=int8 weights=int8 out=%s%s; stream schedule, "
-            "%d-channel items, %d-row passes, reduction in %d slices\n", call, what, m.S, m.Kd, m.N, m.E,
-            m.out_bf16 ? "bf16" : "f32", m.w1 ? " SwiGLU" : "", p.channels, p.rows, p.slices);
+    char how[128] = "tiled schedule";
+    if (by_stream) {
+      const moe::I8StreamPlan p = moe::i8_stream_plan(m);
+      snprintf(how, sizeof(how), "stream schedule, %d-channel items, %d-row passes, reduction in %d slices", p.channels,
+               p.rows, p.slices);
+    }
+    fprintf(stderr, "[moe] %s %s: rows=%d reduction=%d channels=%d E=%d act=int8 weights=int8 out=%s%s; %s\n", call, what,
+            m.S, m.Kd, m.N, m.E, m.out_bf16 ? "bf16" : "f32", m.w1 ? " SwiGLU" : "", how);
   }
-  const hipError_t e = moe::launch_i8_stream(m, stream);
+  const hipError_t e = by_stream ? moe::launch_i8_stream(m, stream) : moe::launch_i8_tiled(m, stream);
   if (e != hipSuccess) return hip_fail(e, what);
   return MOE_OK;
 }

@@ -148,6 +148,9 @@ struct I8StreamPlan {
 };
 I8StreamPlan i8_stream_plan(const I8Args& a);
 hipError_t launch_i8_stream(const I8Args& a, hipStream_t stream);
+// Whether rows of `cols` codes lie within 32-bit byte offsets, as launch_i8_tiled needs the rows of a to.
+bool i8_tiled_offsets_fit(long rows, int cols);
+hipError_t launch_i8_tiled(const I8Args& a, hipStream_t stream);
 
 // Gated routing (route_gated.hip).
 struct GateArgs {
