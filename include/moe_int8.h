@@ -442,7 +442,7 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* shape, const void* x, const int
  *   w_k = s_k, divided by the sum of the K if renorm (0 if that is 0), times scale.
  * Ties, among groups too, go to the lower index. An expert whose c is -inf (a
  * bias of -inf takes it out of service) or NaN is never taken, and counts as
- * -inf for its group; where fewer than K are left, the other ids are -1 with
+ * -inf for its group (as does a sum that is no number); where fewer than K are left, the other ids are -1 with
  * weight 0 (moe_permute does not place such slots, and they add nothing to the
  * combine). A token whose scores are no numbers gets ids of -1.
  * The values that decide the choice are compared in 64 bits, from exact inputs;

@@ -31,7 +31,8 @@ def choose(s, K, select_bias=None, groups=1, group_topk=1, top2=False, renorm=Tr
         value = []
         for g in range(groups):
             best = sorted(c[g * n:(g + 1) * n], reverse=True)
-            value.append(best[0] + best[1] if top2 else best[0])
+            v = best[0] + best[1] if top2 else best[0]
+            value.append(v if v > -math.inf else -math.inf)
         kept = sorted(range(groups), key=lambda g: (-value[g], g))[:group_topk]
         c = [v if e // n in kept else -math.inf for e, v in enumerate(c)]
     order = sorted(range(E), key=lambda e: (-c[e], e))[:K]
