@@ -28,7 +28,6 @@ namespace moe {
 namespace {
 
 constexpr int kMaxExperts = 256;
-constexpr int kWaves = 16;
 
 // What an MFMA's sum of 32 products (a chain of eight fp32 ones) is taken to be off
 // by, in 2^-23 of the sum of their magnitudes. Measured over random and one-sided sums
@@ -125,7 +124,7 @@ struct TokenState {
   float* x_norm;       // [tokens]  |x|, rounded up
   float* w_norm;       // [stride]  |w_e|, rounded up
   uint32_t* refined;   // [tokens][8] bit e: the logit is a 64-bit one
-  uint32_t* work;      // (token << 16 | expert) to refine
+  uint16_t* work;      // (token << 8 | expert) to refine
   int* n_work;
   int stride;
 };
@@ -326,7 +325,7 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
     const bool all = !a.sigmoid && a.select_bias;
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
-      if (all ? open[j] : marks[j]) s.work[atomicAdd(s.n_work, 1)] = (uint32_t)t << 16 | (uint32_t)e_of[j];
+      if (all ? open[j] : marks[j]) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | e_of[j]);
     return false;
   }
 
@@ -351,7 +350,7 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
 
 // The choice of the workgroup's tokens (kTok of them at most, n present) once their logits lie in LDS. All waves call
 // it, after a barrier; wave v takes tokens v, v + kWaves, ...
-template <typename Act, int kTok, int kSlots>
+template <typename Act, int kWaves, int kTok, int kSlots>
 __device__ __forceinline__ void choose_all(const GateArgs& a, const TokenState& s, int tok0, int n, float units) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -376,8 +375,7 @@ __device__ __forceinline__ void choose_all(const GateArgs& a, const TokenState& 
     const int work = *s.n_work;
     if (work == 0) break;
     for (int i = wave; i < work; i += kWaves) {
-      const uint32_t p = s.work[i];
-      const int t = p >> 16, e = p & 0xffff;
+      const int t = s.work[i] >> 8, e = s.work[i] & 255;
       const double v = dot64(static_cast<const Act*>(a.x) + (long)(tok0 + t) * a.d,
                              static_cast<const Act*>(a.router_w) + (long)e * a.d, a.d);
       if (lane == 0) {
@@ -401,26 +399,29 @@ __device__ __forceinline__ void choose_all(const GateArgs& a, const TokenState& 
 // Sum of a logit's parts, written with its bias; what is no number, or near the end of fp32's range, is left to fp64.
 __device__ __forceinline__ void put_logit(const GateArgs& a, const TokenState& s, int t, int e, double v) {
   s.logit[t * s.stride + e] = a.router_bias ? v + a.router_bias[e] : v;
-  if (!(fabs(v) < 0x1p120)) s.work[atomicAdd(s.n_work, 1)] = (uint32_t)t << 16 | (uint32_t)e;
+  if (!(fabs(v) < 0x1p120)) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | e);
 }
 
 // ------------------------------------------------------------------ up to 64 experts
 constexpr int kTok = 16;
+constexpr int kSlices = 16;
 
 // One workgroup scores tpw <= 16 tokens against every expert (the MFMA tile keeps
-// 16 rows; rows past tpw stay zero), EB blocks of 16 experts. Wave w takes the
-// 32-wide chunks w, w + 16, ... of the hidden dimension, U of them requested
-// together. A token's sums do not depend on tpw.
-template <typename Act, int EB>
-__global__ __launch_bounds__(kWaves* kWave) void route_gated_kernel(GateArgs a, int tpw) {
+// 16 rows; rows past tpw stay zero), EB blocks of 16 experts. Slice s of the hidden
+// dimension is its 32-wide chunks s, s + 16, ...; wave w takes the slices w, w + kWaves, ..., U
+// chunks requested together, and the slices' sums meet in LDS. A token's sums
+// depend neither on tpw nor on kWaves.
+template <typename Act, int EB, int kWaves>
+__global__ __launch_bounds__(kWaves* kWave, 4) void route_gated_kernel(GateArgs a, int tpw) {
   constexpr int EP = 16 * EB;
-  constexpr int U = EB == 4 ? 2 : sizeof(Act) == 2 ? 8 / EB : 4 / EB;
+  constexpr int U = sizeof(Act) == 2 ? 4 / EB : EB == 1 ? 2 : 1;   // more would spill
   constexpr int kSlots = EB <= 2 ? 1 : 2;   // a group has more than 32 / groups lanes
-  __shared__ float part[kWaves][kTok][EP];
-  __shared__ float norm_part[kWaves][kTok + EP];
+  __shared__ float part[kSlices][kTok][EP];
+  __shared__ float norm_part[kSlices][kTok + EP];
   __shared__ double logit[kTok][EP];
   __shared__ float x_norm[kTok], w_norm[EP];
-  __shared__ uint32_t refined[kTok][8], work[kTok * EP];
+  __shared__ uint32_t refined[kTok][8];
+  __shared__ uint16_t work[kTok * EP];
   __shared__ int n_work;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -432,228 +433,372 @@ __global__ __launch_bounds__(kWaves* kWave) void route_gated_kernel(GateArgs a, 
   const Act* x = static_cast<const Act*>(a.x) + (long)(tok0 + min(li, n - 1)) * d + 8 * lg;
   const bool x_ok = li < n;
   const Act* wr = static_cast<const Act*>(a.router_w) + 8 * lg;
-
-  double acc[EB][4];
-#pragma unroll
-  for (int eb = 0; eb < EB; ++eb)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[eb][r] = 0;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  f32x4 xx = zero, ww[EB];    // bf16: tiles of x.x and w.w, whose diagonals are the norms
-  float xs = 0.f, wsum[EB];   // fp32: a lane's part of them
-#pragma unroll
-  for (int eb = 0; eb < EB; ++eb) {
-    ww[eb] = zero;
-    wsum[eb] = 0.f;
-  }
   const int chunks = d >> 5;
-  for (int c0 = wave; c0 < chunks; c0 += kWaves * U) {
-    if constexpr (sizeof(Act) == 2) {
-      bf16x8 u[U], v[U][EB];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int c = c0 + i * kWaves;
-        u[i] = x_ok && c < chunks ? as_bf16x8(*reinterpret_cast<const uint4*>(x + 32 * c)) : zero_bf16x8();
-#pragma unroll
-        for (int eb = 0; eb < EB; ++eb) {
-          const int e = eb * 16 + li;
-          v[i][eb] = e < a.E && c < chunks ? as_bf16x8(*reinterpret_cast<const uint4*>(wr + (long)e * d + 32 * c)) : zero_bf16x8();
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        xx = mfma_bf16(u[i], u[i], xx);
-#pragma unroll
-        for (int eb = 0; eb < EB; ++eb) {
-          const f32x4 p = mfma_bf16(u[i], v[i][eb], zero);
-          ww[eb] = mfma_bf16(v[i][eb], v[i][eb], ww[eb]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[eb][r] += (double)p[r];
-        }
-      }
-    } else {
-      f32x4 u[U][2], v[U][EB][2];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int c = c0 + i * kWaves;
-        u[i][0] = u[i][1] = zero;
-        if (x_ok && c < chunks) {
-          const f32x4* p = reinterpret_cast<const f32x4*>(x + 32 * c);
-          u[i][0] = p[0];
-          u[i][1] = p[1];
-        }
-#pragma unroll
-        for (int eb = 0; eb < EB; ++eb) {
-          const int e = eb * 16 + li;
-          v[i][eb][0] = v[i][eb][1] = zero;
-          if (e < a.E && c < chunks) {
-            const f32x4* p = reinterpret_cast<const f32x4*>(wr + (long)e * d + 32 * c);
-            v[i][eb][0] = p[0];
-            v[i][eb][1] = p[1];
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) xs += u[i][j >> 2][j & 3] * u[i][j >> 2][j & 3];
-#pragma unroll
-        for (int eb = 0; eb < EB; ++eb) {
-          f32x4 p = zero;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float y = v[i][eb][j >> 2][j & 3];
-            p = mfma_f32(u[i][j >> 2][j & 3], y, p);
-            wsum[eb] += y * y;
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[eb][r] += (double)p[r];
-        }
-      }
-    }
-  }
 
-  // lane l holds tokens 4*lg + r of expert 16*eb + li
+#pragma unroll 1
+  for (int slice = wave; slice < kSlices; slice += kWaves) {
+    double acc[EB][4];
 #pragma unroll
-  for (int eb = 0; eb < EB; ++eb)
+    for (int eb = 0; eb < EB; ++eb)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) part[wave][4 * lg + r][eb * 16 + li] = (float)acc[eb][r];
-  if constexpr (sizeof(Act) == 2) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (4 * lg + r == li) {
-        norm_part[wave][li] = xx[r];
-#pragma unroll
-        for (int eb = 0; eb < EB; ++eb) norm_part[wave][kTok + eb * 16 + li] = ww[eb][r];
-      }
-  } else {
-    xs += __shfl_xor(xs, 16);
-    xs += __shfl_xor(xs, 32);
-    if (lg == 0) norm_part[wave][li] = xs;
+      for (int r = 0; r < 4; ++r) acc[eb][r] = 0;
+    f32x4 xx = zero, ww[EB];    // bf16: tiles of x.x and w.w, whose diagonals are the norms
+    float xs = 0.f, wsum[EB];   // fp32: a lane's part of them
 #pragma unroll
     for (int eb = 0; eb < EB; ++eb) {
-      wsum[eb] += __shfl_xor(wsum[eb], 16);
-      wsum[eb] += __shfl_xor(wsum[eb], 32);
-      if (lg == 0) norm_part[wave][kTok + eb * 16 + li] = wsum[eb];
+      ww[eb] = zero;
+      wsum[eb] = 0.f;
+    }
+    if constexpr (sizeof(Act) == 2) {
+      bf16x8 u[2][U], v[2][U][EB];
+      auto load = [&](int c0, bf16x8 (&un)[U], bf16x8 (&vn)[U][EB]) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int c = c0 + i * kSlices;
+          un[i] = x_ok && c < chunks ? as_bf16x8(*reinterpret_cast<const uint4*>(x + 32 * c)) : zero_bf16x8();
+#pragma unroll
+          for (int eb = 0; eb < EB; ++eb) {
+            const int e = eb * 16 + li;
+            vn[i][eb] = e < a.E && c < chunks ? as_bf16x8(*reinterpret_cast<const uint4*>(wr + (long)e * d + 32 * c)) : zero_bf16x8();
+          }
+        }
+      };
+      auto add = [&](const bf16x8 (&un)[U], const bf16x8 (&vn)[U][EB]) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          xx = mfma_bf16(un[i], un[i], xx);
+#pragma unroll
+          for (int eb = 0; eb < EB; ++eb) {
+            const f32x4 p = mfma_bf16(un[i], vn[i][eb], zero);
+            ww[eb] = mfma_bf16(vn[i][eb], vn[i][eb], ww[eb]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[eb][r] += (double)p[r];
+          }
+        }
+      };
+      load(slice, u[0], v[0]);
+      for (int c0 = slice; c0 < chunks; c0 += 2 * kSlices * U) {
+        load(c0 + kSlices * U, u[1], v[1]);
+        add(u[0], v[0]);
+        if (c0 + kSlices * U >= chunks) break;
+        load(c0 + 2 * kSlices * U, u[0], v[0]);
+        add(u[1], v[1]);
+      }
+    } else {
+      f32x4 u[2][U][2], v[2][U][EB][2];
+      auto load = [&](int c0, f32x4 (&un)[U][2], f32x4 (&vn)[U][EB][2]) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const int c = c0 + i * kSlices;
+          un[i][0] = un[i][1] = zero;
+          if (x_ok && c < chunks) {
+            const f32x4* p = reinterpret_cast<const f32x4*>(x + 32 * c);
+            un[i][0] = p[0];
+            un[i][1] = p[1];
+          }
+#pragma unroll
+          for (int eb = 0; eb < EB; ++eb) {
+            const int e = eb * 16 + li;
+            vn[i][eb][0] = vn[i][eb][1] = zero;
+            if (e < a.E && c < chunks) {
+              const f32x4* p = reinterpret_cast<const f32x4*>(wr + (long)e * d + 32 * c);
+              vn[i][eb][0] = p[0];
+              vn[i][eb][1] = p[1];
+            }
+          }
+        }
+      };
+      auto add = [&](const f32x4 (&un)[U][2], const f32x4 (&vn)[U][EB][2]) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          f32x4 p[EB];
+#pragma unroll
+          for (int eb = 0; eb < EB; ++eb) p[eb] = zero;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float y = un[i][j >> 2][j & 3];
+            xs += y * y;
+#pragma unroll
+            for (int eb = 0; eb < EB; ++eb) {
+              const float z = vn[i][eb][j >> 2][j & 3];
+              p[eb] = mfma_f32(y, z, p[eb]);
+              wsum[eb] += z * z;
+            }
+          }
+#pragma unroll
+          for (int eb = 0; eb < EB; ++eb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[eb][r] += (double)p[eb][r];
+        }
+      };
+      load(slice, u[0], v[0]);
+      for (int c0 = slice; c0 < chunks; c0 += 2 * kSlices * U) {
+        load(c0 + kSlices * U, u[1], v[1]);
+        add(u[0], v[0]);
+        if (c0 + kSlices * U >= chunks) break;
+        load(c0 + 2 * kSlices * U, u[0], v[0]);
+        add(u[1], v[1]);
+      }
+    }
+
+    // lane l holds tokens 4*lg + r of expert 16*eb + li
+#pragma unroll
+    for (int eb = 0; eb < EB; ++eb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) part[slice][4 * lg + r][eb * 16 + li] = (float)acc[eb][r];
+    if constexpr (sizeof(Act) == 2) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (4 * lg + r == li) {
+          norm_part[slice][li] = xx[r];
+#pragma unroll
+          for (int eb = 0; eb < EB; ++eb) norm_part[slice][kTok + eb * 16 + li] = ww[eb][r];
+        }
+    } else {
+      xs += __shfl_xor(xs, 16);
+      xs += __shfl_xor(xs, 32);
+      if (lg == 0) norm_part[slice][li] = xs;
+#pragma unroll
+      for (int eb = 0; eb < EB; ++eb) {
+        wsum[eb] += __shfl_xor(wsum[eb], 16);
+        wsum[eb] += __shfl_xor(wsum[eb], 32);
+        if (lg == 0) norm_part[slice][kTok + eb * 16 + li] = wsum[eb];
+      }
     }
   }
   const TokenState s = {&logit[0][0], x_norm, w_norm, &refined[0][0], work, &n_work, EP};
   if (threadIdx.x < kTok * 8) (&refined[0][0])[threadIdx.x] = 0;
   if (threadIdx.x == 0) n_work = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < kTok * EP; i += kWaves * kWave) {
+  for (int i = threadIdx.x; i < n * EP; i += kWaves * kWave) {
     const int t = i / EP, e = i % EP;
     double v = 0;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += (double)part[k][t][e];
-    if (t < n && e < a.E) put_logit(a, s, t, e, v);
+    for (int k = 0; k < kSlices; ++k) v += (double)part[k][t][e];
+    if (e < a.E) put_logit(a, s, t, e, v);
   }
   if (threadIdx.x < kTok + EP) {
     float v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += norm_part[k][threadIdx.x];
+    for (int k = 0; k < kSlices; ++k) v += norm_part[k][threadIdx.x];
     // the sum of squares is off by less than a thousandth
     v = sqrtf(v) * 1.01f;
     if (threadIdx.x < kTok) x_norm[threadIdx.x] = v;
     else w_norm[threadIdx.x - kTok] = v;
   }
   __syncthreads();
-  // the parts of the waves are rounded to fp32 once more
-  choose_all<Act, kTok, kSlots>(a, s, tok0, n, kMfmaUnits + 1.f);
+  // the parts of the slices are rounded to fp32 once more
+  choose_all<Act, kWaves, kTok, kSlots>(a, s, tok0, n, kMfmaUnits + 1.f);
 }
 
 // ------------------------------------------------------------------ up to 256 experts
-// One workgroup scores 16 tokens; wave w takes the experts 16*w .. +16 over the whole hidden dimension.
-template <typename Act>
-__global__ __launch_bounds__(kWaves* kWave) void route_gated_wide_kernel(GateArgs a, int tpw) {
-  constexpr int EP = kMaxExperts;
-  constexpr int U = 4;
-  __shared__ double logit[kTok][EP];
-  __shared__ float x_norm[kTok], w_norm[EP];
-  __shared__ uint32_t refined[kTok][8], work[kTok * EP];
+constexpr int kWideWaves = 16;
+constexpr int kRowBytes = 256;   // of a token's row in a step
+
+// One workgroup scores 16*TB tokens. Its 16 waves take a block of 16 experts each (KS = 1), or half of the chunks of
+// one (KS = 2, up to 128 experts), and share the tokens' rows through LDS (direct loads, double buffered; 16-byte pieces
+// XOR-swizzled by the row). The weights go to the registers of the one wave that needs them, a step ahead.
+template <typename Act, int TB, int KS>
+__global__ __launch_bounds__(kWideWaves* kWave) void route_gated_wide_kernel(GateArgs a) {
+  constexpr int EP = kMaxExperts / KS;
+  constexpr int TOK = 16 * TB;
+  constexpr int CS = kRowBytes / (32 * (int)sizeof(Act));   // 32-wide chunks of a step: 4 or 2
+  constexpr int WC = CS / KS;                               // of a wave
+  constexpr int STAGE = TOK * kRowBytes;
+  __shared__ __attribute__((aligned(1024))) uint8_t xs[2][STAGE];
+  __shared__ double logit[TOK][EP];
+  __shared__ float x_norm[TOK], w_norm[EP];
+  __shared__ uint32_t refined[TOK][8];
+  __shared__ uint16_t work[TOK * EP];
   __shared__ int n_work;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15;
   const int lg = lane >> 4;
-  const int tok0 = blockIdx.x * tpw;
-  const int n = min(tpw, a.T - tok0);
+  const int tok0 = blockIdx.x * TOK;
+  const int n = min(TOK, a.T - tok0);
   const int d = a.d;
-  const int e = wave * 16 + li;
+  const int ks = wave / (16 / KS);
+  const int e = (wave % (16 / KS)) * 16 + li;
+  const bool active = (wave % (16 / KS)) * 16 < a.E;
   const TokenState s = {&logit[0][0], x_norm, w_norm, &refined[0][0], work, &n_work, EP};
-  if (threadIdx.x < kTok * 8) (&refined[0][0])[threadIdx.x] = 0;
+  if (threadIdx.x < TOK * 8) (&refined[0][0])[threadIdx.x] = 0;
+  if (threadIdx.x < TOK) x_norm[threadIdx.x] = 0.f;
+  if (threadIdx.x < EP) w_norm[threadIdx.x] = 0.f;
   if (threadIdx.x == 0) n_work = 0;
-  __syncthreads();
-  if (wave * 16 < a.E) {
-    const Act* x = static_cast<const Act*>(a.x) + (long)(tok0 + min(li, n - 1)) * d + 8 * lg;
-    const Act* wr = static_cast<const Act*>(a.router_w) + (long)min(e, a.E - 1) * d + 8 * lg;
-    double acc[4] = {0, 0, 0, 0};
-    float xs = 0.f, wsum = 0.f;
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4 xx = zero, ww = zero;
-    const int chunks = d >> 5;
-    for (int c0 = 0; c0 < chunks; c0 += U) {
+
+  const uint8_t* x = static_cast<const uint8_t*>(a.x) + (long)tok0 * d * sizeof(Act);
+  const Act* wr = static_cast<const Act*>(a.router_w) + (long)min(e, a.E - 1) * d + 8 * lg;
+  const int chunks = d >> 5;
+  const int nsteps = (chunks + CS - 1) / CS;
+  // waves 0 .. 4*TB - 1 copy four rows each; the last step of bf16 rows may be half a step: its other half re-reads the first
+  const int row = wave * 4 + (lane >> 4);
+  const int piece = li ^ (row & 15);
+  const uint32_t x_off = (uint32_t)min(row, n - 1) * (uint32_t)(d * (int)sizeof(Act)) + 16u * piece;
+  auto issue_x = [&](int step, int buf) {
+    if (wave >= 4 * TB || step >= nsteps) return;
+    uint32_t off = x_off + (uint32_t)step * kRowBytes;
+    if (step * CS + CS > chunks && piece >= 8) off -= 128;
+    dma16(x, off, lds_addr(&xs[buf][0]) + wave * 1024);
+  };
+  constexpr int V = sizeof(Act) == 2 ? 1 : 2;   // 16-byte loads of a lane's 8 elements
+  auto load_w = [&](int step, uint4 (&b)[WC][V]) {
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
-        if (c0 + i >= chunks) break;
-        if constexpr (sizeof(Act) == 2) {
-          const bf16x8 u = as_bf16x8(*reinterpret_cast<const uint4*>(x + 32 * (c0 + i)));
-          const bf16x8 v = as_bf16x8(*reinterpret_cast<const uint4*>(wr + 32 * (c0 + i)));
-          const f32x4 p = mfma_bf16(u, v, zero);
-          ww = mfma_bf16(v, v, ww);
-          if (wave == 0) xx = mfma_bf16(u, u, xx);
+    for (int i = 0; i < WC; ++i) {
+      const int c = min(step * CS + i * KS + ks, chunks - 1);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] += (double)p[r];
+      for (int h = 0; h < V; ++h) b[i][h] = reinterpret_cast<const uint4*>(wr + 32 * (long)c)[h];
+    }
+  };
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  double acc[TB][4];
+#pragma unroll
+  for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[tb][r] = 0;
+  f32x4 xx = zero, ww = zero;
+  float xsum = 0.f, wsum = 0.f;
+  // a lane's 8 elements of chunk c of a step, token block tb
+  auto x_piece = [&](int buf, int tb, int c, int h) {
+    const int r = tb * 16 + li;
+    const int p = V == 1 ? 4 * c + lg : 8 * c + 2 * lg + h;
+    return *reinterpret_cast<const uint4*>(&xs[buf][r * kRowBytes + 16 * (p ^ li)]);
+  };
+  auto step_of = [&](int st, int buf, const uint4 (&b)[WC][V], uint4 (&bn)[WC][V]) {
+    // this step's rows have landed, and every wave is past the buffer that the next ones overwrite
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+    __builtin_amdgcn_s_barrier();
+    issue_x(st + 1, 1 - buf);
+    if (active && st + 1 < nsteps) load_w(st + 1, bn);
+    if (active) {
+      f32x4 p[TB];
+#pragma unroll
+      for (int i = 0; i < WC; ++i) {
+        const int c = i * KS + ks;
+        if (st * CS + c >= chunks) break;
+        // sums of two chunks with bf16, of one (a chain of eight) with fp32
+        if (V == 2 || i % 2 == 0)
+#pragma unroll
+          for (int tb = 0; tb < TB; ++tb) p[tb] = zero;
+        if constexpr (V == 1) {
+          const bf16x8 w = as_bf16x8(b[i][0]);
+          ww = mfma_bf16(w, w, ww);
+#pragma unroll
+          for (int tb = 0; tb < TB; ++tb) p[tb] = mfma_bf16(as_bf16x8(x_piece(buf, tb, c, 0)), w, p[tb]);
         } else {
-          const f32x4* q = reinterpret_cast<const f32x4*>(x + 32 * (c0 + i));
-          const f32x4* b = reinterpret_cast<const f32x4*>(wr + 32 * (c0 + i));
-          f32x4 p = zero;
+          const f32x4 w[2] = {__builtin_bit_cast(f32x4, b[i][0]), __builtin_bit_cast(f32x4, b[i][V - 1])};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float y = q[j >> 2][j & 3], z = b[j >> 2][j & 3];
-            p = mfma_f32(y, z, p);
-            xs += y * y;
-            wsum += z * z;
+          for (int h = 0; h < 2; ++h) {
+            f32x4 u[TB];
+#pragma unroll
+            for (int tb = 0; tb < TB; ++tb) u[tb] = __builtin_bit_cast(f32x4, x_piece(buf, tb, c, h));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              wsum += w[h][j] * w[h][j];
+#pragma unroll
+              for (int tb = 0; tb < TB; ++tb) p[tb] = mfma_f32(u[tb][j], w[h][j], p[tb]);
+            }
           }
+        }
+        if (V == 2 || i % 2 == 1 || i == WC - 1 || st * CS + c + KS >= chunks)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] += (double)p[r];
+          for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[tb][r] += (double)p[tb][r];
+      }
+    }
+    // the tokens' norms: wave tb takes token block tb
+    if (wave < TB) {
+#pragma unroll
+      for (int c = 0; c < CS; ++c) {
+        if (st * CS + c >= chunks) break;
+#pragma unroll
+        for (int h = 0; h < V; ++h) {
+          const uint4 q = x_piece(buf, wave, c, h);
+          if constexpr (V == 1) {
+            xx = mfma_bf16(as_bf16x8(q), as_bf16x8(q), xx);
+          } else {
+            const f32x4 u = __builtin_bit_cast(f32x4, q);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) xsum += u[j] * u[j];
+          }
         }
       }
     }
+  };
+  uint4 b[2][WC][V];
+  issue_x(0, 0);
+  if (active) load_w(0, b[0]);
+  for (int st = 0; st < nsteps; st += 2) {
+    step_of(st, 0, b[0], b[1]);
+    if (st + 1 < nsteps) step_of(st + 1, 1, b[1], b[0]);
+  }
+
+  // norms (1.01: the sum of squares is off by less than a thousandth), and the slices' sums
+  if constexpr (V == 2) {
+    xsum += __shfl_xor(xsum, 16);
+    xsum += __shfl_xor(xsum, 32);
+    wsum += __shfl_xor(wsum, 16);
+    wsum += __shfl_xor(wsum, 32);
+  }
 #pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (4 * lg + r < n && e < a.E) put_logit(a, s, 4 * lg + r, e, acc[r]);
-    if constexpr (sizeof(Act) == 2) {
+  for (int r = 0; r < 4; ++r) {
+    if (V == 1 ? 4 * lg + r != li : lg > 0 || r > 0) continue;
+    if (wave < TB) x_norm[wave * 16 + li] = sqrtf(V == 1 ? xx[r] : xsum) * 1.01f;
+    if (active && KS == 1) w_norm[e] = sqrtf(V == 1 ? ww[r] : wsum) * 1.01f;
+    if (active && KS == 2) atomicAdd(&w_norm[e], V == 1 ? ww[r] : wsum);   // squares; two addends
+  }
+  if (KS == 2 && active && ks == 1) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (4 * lg + r == li) {
-          w_norm[e] = sqrtf(ww[r]) * 1.01f;
-          if (wave == 0) x_norm[li] = sqrtf(xx[r]) * 1.01f;
-        }
-    } else {
-      xs += __shfl_xor(xs, 16);
-      xs += __shfl_xor(xs, 32);
-      wsum += __shfl_xor(wsum, 16);
-      wsum += __shfl_xor(wsum, 32);
-      if (lg == 0) {
-        w_norm[e] = sqrtf(wsum) * 1.01f;
-        if (wave == 0) x_norm[li] = sqrtf(xs) * 1.01f;
-      }
-    }
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) logit[tb * 16 + 4 * lg + r][e] = acc[tb][r];
   }
   __syncthreads();
-  choose_all<Act, kTok, 8>(a, s, tok0, n, kMfmaUnits);
+  if (KS == 2 && threadIdx.x < EP) w_norm[threadIdx.x] = sqrtf(w_norm[threadIdx.x]) * 1.01f;
+  if (active && ks == 0) {
+#pragma unroll
+    for (int tb = 0; tb < TB; ++tb)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = tb * 16 + 4 * lg + r;
+        if (t < n && e < a.E) put_logit(a, s, t, e, KS == 2 ? acc[tb][r] + logit[t][e] : acc[tb][r]);
+      }
+  }
+  __syncthreads();
+  const float units = V == 1 ? 2 * kMfmaUnits : kMfmaUnits;
+  // slots of a lane: experts of a group over its lanes, 8 at most; 4 if the groups are a power of two, as they mostly are
+  const ChoiceMap map(a, lane);
+  if (map.size <= 4 * map.lanes) choose_all<Act, kWideWaves, TOK, 4>(a, s, tok0, n, units);
+  else choose_all<Act, kWideWaves, TOK, 8>(a, s, tok0, n, units);
+}
+
+template <typename Act, int EB>
+void launch_narrow(const GateArgs& a, hipStream_t stream) {
+  // as few tokens a workgroup as leave no CU without one, so that a small batch's reads of router_w are spread
+  const int tpw = min(kTok, (a.T + 255) / 256);
+  const dim3 grid((a.T + tpw - 1) / tpw);
+  // few workgroups: the most waves each; many: two workgroups a CU, one of which loads while the other chooses
+  if (grid.x <= 256) hipLaunchKernelGGL((route_gated_kernel<Act, EB, 16>), grid, dim3(16 * kWave), 0, stream, a, tpw);
+  else hipLaunchKernelGGL((route_gated_kernel<Act, EB, 8>), grid, dim3(8 * kWave), 0, stream, a, tpw);
+}
+
+template <typename Act, int TB>
+void launch_wide(const GateArgs& a, hipStream_t stream) {
+  const dim3 grid((a.T + 16 * TB - 1) / (16 * TB)), block(kWideWaves * kWave);
+  if (a.E <= 128) hipLaunchKernelGGL((route_gated_wide_kernel<Act, TB, 2>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((route_gated_wide_kernel<Act, TB, 1>), grid, block, 0, stream, a);
 }
 
 template <typename Act>
 void launch(const GateArgs& a, hipStream_t stream) {
-  // as few tokens a workgroup as leave no CU without one, so that a small batch's reads of router_w are spread
-  const int tpw = min(kTok, (a.T + 255) / 256);
-  const dim3 grid((a.T + tpw - 1) / tpw), block(kWaves * kWave);
-  if (a.E <= 16) hipLaunchKernelGGL((route_gated_kernel<Act, 1>), grid, block, 0, stream, a, tpw);
-  else if (a.E <= 32) hipLaunchKernelGGL((route_gated_kernel<Act, 2>), grid, block, 0, stream, a, tpw);
-  else if (a.E <= 64) hipLaunchKernelGGL((route_gated_kernel<Act, 4>), grid, block, 0, stream, a, tpw);
-  else hipLaunchKernelGGL((route_gated_wide_kernel<Act>), grid, block, 0, stream, a, tpw);
+  if (a.E <= 16) launch_narrow<Act, 1>(a, stream);
+  else if (a.E <= 32) launch_narrow<Act, 2>(a, stream);
+  else if (a.E <= 64) launch_narrow<Act, 4>(a, stream);
+  else if (a.T <= 256 * 16) launch_wide<Act, 1>(a, stream);
+  else launch_wide<Act, 2>(a, stream);
 }
 
 }  // namespace
