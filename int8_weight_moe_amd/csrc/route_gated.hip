@@ -9,11 +9,11 @@
 //   w_k = s_k (/ their sum) * scale
 //
 // Logits: MFMA tiles of tokens x experts, the hidden dimension split over the
-// waves of a workgroup. The sums of 32 products that an MFMA (fp32 inputs: eight)
-// makes are added in fp64, so a logit is off by at most
-//     delta = kMfmaUnits * 2^-23 * |x| |w_e|
-// (the MFMA: see there; sum |x_i w_i| <= |x| |w_e|). |x|^2 and |w_e|^2 are taken
-// on the way.
+// waves of a workgroup, in blocks of 128 bytes of a row (whole cache lines). A
+// block's sums are added in fp64, so a logit is off by at most
+//     delta = units * 2^-23 * |x| |w_e|
+// (units: what the MFMAs' own sums round, see kMfmaUnits; sum |x_i w_i| <= |x| |w_e|).
+// |x|^2 and |w_e|^2 are taken on the way.
 // Choice: one wave a token, first in fp32 with an error bound eps_e on every c_e
 // (delta through the score's derivative, the evaluation, the bias's rounding). A
 // decision between two values whose intervals overlap is not taken: the experts it
@@ -29,10 +29,12 @@ namespace {
 
 constexpr int kMaxExperts = 256;
 
-// What an MFMA's sum of 32 products (a chain of eight fp32 ones) is taken to be off
-// by, in 2^-23 of the sum of their magnitudes. Measured over random and one-sided sums
-// with 24 bits between the terms: 2.3 at most.
-constexpr float kMfmaUnits = 8.f;
+// What an MFMA sum is taken to be off by, in 2^-23 of the sum of its terms'
+// magnitudes: the 16x16x32 bf16 MFMA adds four groups of eight products, each
+// sum rounded (2 units; measured over one-sided and mixed sums with up to 24
+// bits between the terms: 2.5); a chain of two 16x16x4 fp32 MFMAs rounds eight sums
+// (4 units; measured for a chain of eight: 9.9).
+constexpr float kMfmaUnits = 4.f;
 constexpr float kUnit = 0x1p-23f;
 
 __device__ __forceinline__ void load8d(const __bf16* p, double (&v)[8]) {
@@ -101,7 +103,18 @@ __device__ __forceinline__ double dot64(const Act* __restrict__ a, const Act* __
 __device__ __forceinline__ float exp_of(float v) { return expf(v); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
 
-// Largest and second largest of a lane's values and those of the lanes of its group (lanes_per_group consecutive ones).
+// A lane's value, in every lane (lane: the same in all of them).
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+  const long long b = __double_as_longlong(v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)b, lane), hi = __builtin_amdgcn_readlane((int)(b >> 32), lane);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+// Largest and second largest value of a group, whose values lie in consecutive lanes.
 template <typename Real>
 struct Top2 {
   Real first = -INFINITY, second = -INFINITY;
@@ -116,6 +129,10 @@ struct Top2 {
       first = fmax(first, f);
     }
   }
+  __device__ Real value(bool top2) const {
+    const Real sum = top2 ? first + second : first;
+    return sum > -INFINITY ? sum : (Real)-INFINITY;   // +inf and -inf too
+  }
 };
 
 // A workgroup's tokens between their logits and their choice, in LDS.
@@ -129,8 +146,8 @@ struct TokenState {
   int stride;
 };
 
-// Experts of a lane in the choice: groups lie in lanes_per_group consecutive lanes
-// each, expert i of group g in lane g*lanes + i%lanes, slot i/lanes.
+// Experts of a lane in the choice: a group lies in `lanes` consecutive lanes, its
+// expert i in lane i % lanes of them, slot i / lanes.
 struct ChoiceMap {
   int size, lanes, group, i0;
   __device__ ChoiceMap(const GateArgs& a, int lane) {
@@ -142,20 +159,21 @@ struct ChoiceMap {
   }
 };
 
-// One token's choice by one wave, in fp32 or (kFinal) fp64. Returns whether it is taken (and written); else the experts
-// that it hangs on are appended to the work.
+// One token's choice by one wave, in fp32 or fp64. Returns whether it is taken (and written); else the experts that it
+// hangs on are appended to the work.
 template <typename Real, int kSlots>
 __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, int t, int32_t* ids, float* w, float units) {
   constexpr bool kDouble = sizeof(Real) == 8;
+  constexpr Real kNone = -INFINITY;
   const int lane = threadIdx.x & 63;
   const ChoiceMap map(a, lane);
   const double* logit = s.logit + t * s.stride;
   const float xn = s.x_norm[t];
-  Real score[kSlots], arg[kSlots], c[kSlots], lo[kSlots], hi[kSlots];   // arg: the exponential's argument
+  Real arg[kSlots], c[kSlots], eps[kSlots];   // arg: the exponential's argument; c +- eps: the value that decides
   float delta[kSlots];
   int e_of[kSlots];
-  bool open[kSlots];         // not refined
-  Real m = -INFINITY;
+  bool open[kSlots];                          // not refined
+  Real m = kNone;
   float dmax = 0.f;
 #pragma unroll
   for (int j = 0; j < kSlots; ++j) {
@@ -165,9 +183,9 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
     e_of[j] = e;
     open[j] = false;
     delta[j] = 0.f;
-    score[j] = 0;
+    arg[j] = 0;
     if (valid) {
-      score[j] = (Real)logit[e];
+      arg[j] = (Real)logit[e];
       open[j] = !((s.refined[t * 8 + (e >> 5)] >> (e & 31)) & 1u);
       if (open[j]) {
         const float wn = s.w_norm[e];
@@ -175,171 +193,174 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
         // norms that say nothing: past the fp32 range, or lost below it
         if (!(delta[j] < INFINITY) || ((xn < 0x1p-45f || wn < 0x1p-45f) && logit[e] != 0)) delta[j] = INFINITY;
       }
-      m = fmax(m, score[j]);
+      m = fmax(m, arg[j]);
       dmax = fmaxf(dmax, delta[j]);
     }
   }
+  Real z = 1;
   if (!a.sigmoid) {
     m = wave_max(m);
     // the sum of all exponentials matters next to a bias only: it scales every score alike
     dmax = a.select_bias ? wave_max(dmax) : 0.f;
-    Real z = 0;
+    z = 0;
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
       if (e_of[j] >= 0) {
-        arg[j] = score[j] - m;
-        score[j] = exp_of(arg[j]);
-        z += score[j];
+        arg[j] -= m;
+        c[j] = exp_of(arg[j]);
+        z += c[j];
       }
     z = wave_sum(z);
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j) score[j] /= z;
   }
 #pragma unroll
   for (int j = 0; j < kSlots; ++j) {
-    c[j] = lo[j] = hi[j] = -INFINITY;
-    if (e_of[j] < 0) continue;
-    Real part;               // the score's change with its logit
-    float from = delta[j];
-    if (a.sigmoid) {
-      arg[j] = score[j];
-      score[j] = 1 / (1 + exp_of(-score[j]));
-      part = score[j] * (1 - score[j]);
-    } else {
-      part = score[j];
-      from += dmax;
+    Real v = kNone, err = 0;
+    if (e_of[j] >= 0) {
+      const Real score = a.sigmoid ? 1 / (1 + exp_of(-arg[j])) : c[j] / z;
+      const Real b = a.select_bias ? (Real)a.select_bias[e_of[j]] : (Real)0;
+      v = score + b;
+      // the score's change with its logit: s (1 - s), or s; exp(x) - 1 <= 1.3 x up to 0.5
+      const float from = a.sigmoid ? delta[j] : delta[j] + dmax;
+      const Real part = a.sigmoid ? score * (1 - score) : score;
+      err = from <= 0.5f ? part * (Real)(1.3f * from) : (Real)INFINITY;
+      if constexpr (!kDouble) {
+        // the exponential and its argument's rounding, the sum of exponentials, the division; then the sum with b
+        err += score * ((16 + fabsf(arg[j])) * kUnit) + (score + fabsf(b)) * kUnit;
+        err = fmaxf(err, 0x1p-120f);           // scores lost below the fp32 range
+      }
+      if (!(v > kNone)) v = kNone;
+      if (v == kNone || v == INFINITY) err = 0;   // by the bias, whatever the score
     }
-    const Real b = a.select_bias ? (Real)a.select_bias[e_of[j]] : (Real)0;
-    const Real v = score[j] + b;
-    if (!(v > -INFINITY)) continue;
-    // exp(x) - 1 <= 1.3 x up to 0.5
-    Real eps = from <= 0.5f ? part * (Real)(1.3f * from) : (Real)INFINITY;
-    if constexpr (!kDouble) {
-      // the exponential and its argument's rounding, the sum of exponentials, the division; then the sum with b
-      eps += score[j] * ((16 + fabsf(arg[j])) * kUnit) + (score[j] + fabsf(b)) * kUnit;
-      eps = fmaxf(eps, 0x1p-120f);   // scores lost below the fp32 range
-    }
-    if (v == INFINITY) eps = 0;      // by its bias, whatever its score
     c[j] = v;
-    lo[j] = v - eps;
-    hi[j] = v + eps;
+    eps[j] = err;
   }
 
-  bool marks[kSlots];
-#pragma unroll
-  for (int j = 0; j < kSlots; ++j) marks[j] = false;
+  // next to a bias a softmax hangs on every logit, through the sum
+  const bool all = !a.sigmoid && a.select_bias;
+  uint32_t marks = 0;   // bit j: the choice hangs on slot j's logit
+  auto unsure = [&](int j) { return open[j] || (all && dmax > 0.f); };
   if (a.groups > 1) {
-    Top2<Real> vc, vlo, vhi;
+    Top2<Real> vc;
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) {
-      vc.add(c[j]);
-      vlo.add(lo[j]);
-      vhi.add(hi[j]);
-    }
+    for (int j = 0; j < kSlots; ++j) vc.add(c[j]);
     vc.join(map.lanes);
-    vlo.join(map.lanes);
-    vhi.join(map.lanes);
-    auto value = [&](const Top2<Real>& v) {
-      const Real sum = a.top2 ? v.first + v.second : v.first;
-      return sum > -INFINITY ? sum : (Real)-INFINITY;   // +inf and -inf too
-    };
-    const Real val = value(vc), val_lo = value(vlo), val_hi = value(vhi);
+    const Real val = vc.value(a.top2);
+    Real lo, hi, least;    // ends of the group's value, and what a member needs to count in it
+    if constexpr (kDouble) {
+      Top2<Real> vlo, vhi;
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        vlo.add(c[j] - eps[j]);
+        vhi.add(c[j] + eps[j]);
+      }
+      vlo.join(map.lanes);
+      vhi.join(map.lanes);
+      lo = vlo.value(a.top2);
+      hi = vhi.value(a.top2);
+      least = a.top2 ? vlo.second : vlo.first;
+    } else {
+      // wider ends that cost one exchange
+      Real e = 0;
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) e = fmaxf(e, eps[j]);
+      e = wave_max(e);
+      lo = val - (a.top2 ? 2 * e : e);
+      hi = val + (a.top2 ? 2 * e : e);
+      least = (a.top2 ? vc.second : vc.first) - e;
+    }
     int before = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const Real o = __shfl(val, g * map.lanes);
+      const Real o = lane_value(val, g * map.lanes);
       before += o > val || (o == val && g < map.group);
     }
     const bool real = map.group < a.groups, kept = real && before < a.group_topk;
-    const Real floor = -wave_max(kept ? -val_lo : (Real)-INFINITY);      // least value of a kept group
-    const Real ceil = wave_max(real && !kept ? val_hi : (Real)-INFINITY);
-    if (a.group_topk < a.groups && !(floor > ceil)) {
-      const bool near = kept ? !(val_lo > ceil) : real && !(val_hi < floor);
-      const Real least = a.top2 ? vlo.second : vlo.first;   // what a member needs to count in its group's value
+    if (a.group_topk < a.groups) {
+      const Real floor = -wave_max(kept ? -lo : kNone);      // least value of a kept group
+      const Real ceil = wave_max(real && !kept ? hi : kNone);
+      if (!(floor > ceil)) {
+        const bool near = kept ? !(lo > ceil) : real && !(hi < floor);
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) marks[j] = near && open[j] && c[j] > -INFINITY && !(hi[j] < least);
+        for (int j = 0; j < kSlots; ++j)
+          if (near && unsure(j) && c[j] > kNone && !(c[j] + eps[j] < least)) marks |= 1u << j;
+      }
     }
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
-      if (!kept) c[j] = lo[j] = hi[j] = -INFINITY;
+      if (!kept) {
+        c[j] = kNone;
+        eps[j] = 0;
+      }
   }
 
-  // K rounds; lane k keeps round k's expert and lower end
-  int rank[kSlots];
-#pragma unroll
-  for (int j = 0; j < kSlots; ++j) rank[j] = a.K;
+  // K rounds; lane k keeps round k's expert and its value's ends
+  uint32_t picked = 0;   // bit j: slot j was taken
   int my_id = -1;
-  Real my_lo = -INFINITY, my_hi = -INFINITY;
+  Real my_lo = kNone, my_hi = kNone;
   for (int k = 0; k < a.K; ++k) {
-    Real v = -INFINITY;
+    Real v = kNone;
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j)
-      if (rank[j] == a.K) v = fmax(v, c[j]);
+    for (int j = 0; j < kSlots; ++j) v = fmax(v, picked >> j & 1 ? kNone : c[j]);
     const Real top = wave_max(v);
-    if (!(top > -INFINITY)) break;
-    int e = kMaxExperts;
+    if (!(top > kNone)) break;
+    int e = kMaxExperts, slot = 0;
+    Real err = 0;
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j)
-      if (rank[j] == a.K && c[j] == top) e = min(e, e_of[j]);
-    const uint64_t equal = __ballot(e < kMaxExperts);
-    e = __popcll(equal) == 1 ? __builtin_amdgcn_readlane(e, __ffsll((unsigned long long)equal) - 1) : wave_min(e);
-    Real l = -INFINITY, h = -INFINITY;
-    bool mine = false;
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j)
-      if (e_of[j] == e) {
-        rank[j] = k;
-        l = lo[j];
-        h = hi[j];
-        mine = true;
+    for (int j = kSlots - 1; j >= 0; --j)   // a lane's experts ascend with the slot
+      if (!(picked >> j & 1) && c[j] == top) {
+        e = e_of[j];
+        slot = j;
+        err = eps[j];
       }
-    const int owner = __ffsll((unsigned long long)__ballot(mine)) - 1;
-    l = __shfl(l, owner);
-    h = __shfl(h, owner);
+    const uint64_t equal = __ballot(e < kMaxExperts);
+    int owner = __ffsll((unsigned long long)equal) - 1;
+    if (__popcll(equal) > 1) owner = __ffsll((unsigned long long)__ballot(e == wave_min(e))) - 1;
+    if (lane == owner) picked |= 1u << slot;
+    err = lane_value(err, owner);
+    e = lane_value(e, owner);
     if (lane == k) {
       my_id = e;
-      my_lo = l;
-      my_hi = h;
+      my_lo = top - err;
+      my_hi = top + err;
     }
   }
   {
     // every pick lies above all that rank after it
-    Real above = -INFINITY;
+    Real above = kNone;
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
-      if (rank[j] == a.K) above = fmax(above, hi[j]);
+      if (!(picked >> j & 1)) above = fmax(above, c[j] + eps[j]);
     above = wave_max(above);
     for (int k = a.K - 1; k >= 0; --k) {
-      const Real l = __shfl(my_lo, k), h = __shfl(my_hi, k);
-      if (__shfl(my_id, k) >= 0 && !(l > above)) {
+      const Real lo = lane_value(my_lo, k), hi = lane_value(my_hi, k);
+      const int e = lane_value(my_id, k);
+      if (e >= 0 && !(lo > above)) {
+        // it, and what may lie above its lower end (those that rank before it too: they do no harm)
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) marks[j] = marks[j] || (open[j] && (rank[j] == k || (rank[j] > k && c[j] > -INFINITY && !(hi[j] < l))));
+        for (int j = 0; j < kSlots; ++j)
+          if (unsure(j) && (e_of[j] == e || (c[j] > kNone && !(c[j] + eps[j] < lo) && !(c[j] - eps[j] > hi)))) marks |= 1u << j;
       }
-      above = fmax(above, h);
+      above = fmax(above, hi);
     }
   }
-  bool any = false;
-#pragma unroll
-  for (int j = 0; j < kSlots; ++j) any = any || marks[j];
-  if (__any(any)) {
-    // next to a bias a softmax hangs on every logit
-    const bool all = !a.sigmoid && a.select_bias;
+  if (__any(marks != 0)) {
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
-      if (all ? open[j] : marks[j]) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | e_of[j]);
+      if (open[j] && (all || marks >> j & 1)) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | e_of[j]);
     return false;
   }
 
-  // weights, in fp64 from the logits of the chosen
+  // weights, in fp64 from the logits of the chosen (lanes 0 .. 7)
   double sk = 0;
   if (my_id >= 0) sk = a.sigmoid ? 1 / (1 + exp(-logit[my_id])) : exp(logit[my_id] - m);
-  double total = wave_sum(sk);
-  if (!a.renorm) {
-    total = 1;
-    if (!a.sigmoid) {
-      total = 0;
-      for (int e = lane; e < a.E; e += kWave) total += exp(logit[e] - m);
-      total = wave_sum(total);
-    }
+  double total = 1;
+  if (a.renorm) {
+    total = sk;
+#pragma unroll
+    for (int off = 4; off >= 1; off >>= 1) total += __shfl_xor(total, off);
+  } else if (!a.sigmoid) {
+    total = 0;
+    for (int e = lane; e < a.E; e += kWave) total += exp(logit[e] - m);
+    total = wave_sum(total);
   }
   if (lane < a.K) {
     ids[lane] = my_id;
@@ -402,403 +423,276 @@ __device__ __forceinline__ void put_logit(const GateArgs& a, const TokenState& s
   if (!(fabs(v) < 0x1p120)) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | e);
 }
 
-// ------------------------------------------------------------------ up to 64 experts
-constexpr int kTok = 16;
-constexpr int kSlices = 16;
+// ------------------------------------------------------------------ logits
+// A block is 128 bytes of a row of x or router_w: 64 bf16 or 32 fp32 elements.
+// Lane l of a wave holds the 32 bytes at 32*(l/16) of row l%16, of x and of w alike.
+// Rows go through LDS: direct loads of 8 rows an instruction, whose eight lanes a
+// row read one cache line (lanes that read their MFMA rows themselves touch 64 lines an
+// instruction, and stay at 14 bytes a cycle and CU). The 16-byte pieces of a row are XOR-swizzled by its number.
+constexpr int kBlockBytes = 128;
+constexpr int kTileBytes = 16 * kBlockBytes;   // a block of 16 rows
 
-// One workgroup scores tpw <= 16 tokens against every expert (the MFMA tile keeps
-// 16 rows; rows past tpw stay zero), EB blocks of 16 experts. Slice s of the hidden
-// dimension is its 32-wide chunks s, s + 16, ...; wave w takes the slices w, w + kWaves, ..., U
-// chunks requested together, and the slices' sums meet in LDS. A token's sums
-// depend neither on tpw nor on kWaves.
-template <typename Act, int EB, int kWaves>
-__global__ __launch_bounds__(kWaves* kWave, 4) void route_gated_kernel(GateArgs a, int tpw) {
-  constexpr int EP = 16 * EB;
-  constexpr int U = sizeof(Act) == 2 ? 4 / EB : EB == 1 ? 2 : 1;   // more would spill
-  constexpr int kSlots = EB <= 2 ? 1 : 2;   // a group has more than 32 / groups lanes
-  __shared__ float part[kSlices][kTok][EP];
-  __shared__ float norm_part[kSlices][kTok + EP];
-  __shared__ double logit[kTok][EP];
-  __shared__ float x_norm[kTok], w_norm[EP];
-  __shared__ uint32_t refined[kTok][8];
-  __shared__ uint16_t work[kTok * EP];
-  __shared__ int n_work;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int li = lane & 15;
-  const int lg = lane >> 4;
-  const int tok0 = blockIdx.x * tpw;
-  const int n = min(tpw, a.T - tok0);
-  const int d = a.d;
-  const Act* x = static_cast<const Act*>(a.x) + (long)(tok0 + min(li, n - 1)) * d + 8 * lg;
-  const bool x_ok = li < n;
-  const Act* wr = static_cast<const Act*>(a.router_w) + 8 * lg;
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  const int chunks = d >> 5;
+struct Block {
+  uint4 h[2];
+};
 
-#pragma unroll 1
-  for (int slice = wave; slice < kSlices; slice += kWaves) {
-    double acc[EB][4];
+// This lane's part of a block of 16 rows in LDS.
+__device__ __forceinline__ Block lds_block(const uint8_t* tile) {
+  const int li = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
+  Block b;
 #pragma unroll
-    for (int eb = 0; eb < EB; ++eb)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[eb][r] = 0;
-    f32x4 xx = zero, ww[EB];    // bf16: tiles of x.x and w.w, whose diagonals are the norms
-    float xs = 0.f, wsum[EB];   // fp32: a lane's part of them
-#pragma unroll
-    for (int eb = 0; eb < EB; ++eb) {
-      ww[eb] = zero;
-      wsum[eb] = 0.f;
-    }
-    if constexpr (sizeof(Act) == 2) {
-      bf16x8 u[2][U], v[2][U][EB];
-      auto load = [&](int c0, bf16x8 (&un)[U], bf16x8 (&vn)[U][EB]) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int c = c0 + i * kSlices;
-          un[i] = x_ok && c < chunks ? as_bf16x8(*reinterpret_cast<const uint4*>(x + 32 * c)) : zero_bf16x8();
-#pragma unroll
-          for (int eb = 0; eb < EB; ++eb) {
-            const int e = eb * 16 + li;
-            vn[i][eb] = e < a.E && c < chunks ? as_bf16x8(*reinterpret_cast<const uint4*>(wr + (long)e * d + 32 * c)) : zero_bf16x8();
-          }
-        }
-      };
-      auto add = [&](const bf16x8 (&un)[U], const bf16x8 (&vn)[U][EB]) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          xx = mfma_bf16(un[i], un[i], xx);
-#pragma unroll
-          for (int eb = 0; eb < EB; ++eb) {
-            const f32x4 p = mfma_bf16(un[i], vn[i][eb], zero);
-            ww[eb] = mfma_bf16(vn[i][eb], vn[i][eb], ww[eb]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[eb][r] += (double)p[r];
-          }
-        }
-      };
-      load(slice, u[0], v[0]);
-      for (int c0 = slice; c0 < chunks; c0 += 2 * kSlices * U) {
-        load(c0 + kSlices * U, u[1], v[1]);
-        add(u[0], v[0]);
-        if (c0 + kSlices * U >= chunks) break;
-        load(c0 + 2 * kSlices * U, u[0], v[0]);
-        add(u[1], v[1]);
-      }
-    } else {
-      f32x4 u[2][U][2], v[2][U][EB][2];
-      auto load = [&](int c0, f32x4 (&un)[U][2], f32x4 (&vn)[U][EB][2]) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int c = c0 + i * kSlices;
-          un[i][0] = un[i][1] = zero;
-          if (x_ok && c < chunks) {
-            const f32x4* p = reinterpret_cast<const f32x4*>(x + 32 * c);
-            un[i][0] = p[0];
-            un[i][1] = p[1];
-          }
-#pragma unroll
-          for (int eb = 0; eb < EB; ++eb) {
-            const int e = eb * 16 + li;
-            vn[i][eb][0] = vn[i][eb][1] = zero;
-            if (e < a.E && c < chunks) {
-              const f32x4* p = reinterpret_cast<const f32x4*>(wr + (long)e * d + 32 * c);
-              vn[i][eb][0] = p[0];
-              vn[i][eb][1] = p[1];
-            }
-          }
-        }
-      };
-      auto add = [&](const f32x4 (&un)[U][2], const f32x4 (&vn)[U][EB][2]) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          f32x4 p[EB];
-#pragma unroll
-          for (int eb = 0; eb < EB; ++eb) p[eb] = zero;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float y = un[i][j >> 2][j & 3];
-            xs += y * y;
-#pragma unroll
-            for (int eb = 0; eb < EB; ++eb) {
-              const float z = vn[i][eb][j >> 2][j & 3];
-              p[eb] = mfma_f32(y, z, p[eb]);
-              wsum[eb] += z * z;
-            }
-          }
-#pragma unroll
-          for (int eb = 0; eb < EB; ++eb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[eb][r] += (double)p[eb][r];
-        }
-      };
-      load(slice, u[0], v[0]);
-      for (int c0 = slice; c0 < chunks; c0 += 2 * kSlices * U) {
-        load(c0 + kSlices * U, u[1], v[1]);
-        add(u[0], v[0]);
-        if (c0 + kSlices * U >= chunks) break;
-        load(c0 + 2 * kSlices * U, u[0], v[0]);
-        add(u[1], v[1]);
-      }
-    }
-
-    // lane l holds tokens 4*lg + r of expert 16*eb + li
-#pragma unroll
-    for (int eb = 0; eb < EB; ++eb)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) part[slice][4 * lg + r][eb * 16 + li] = (float)acc[eb][r];
-    if constexpr (sizeof(Act) == 2) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (4 * lg + r == li) {
-          norm_part[slice][li] = xx[r];
-#pragma unroll
-          for (int eb = 0; eb < EB; ++eb) norm_part[slice][kTok + eb * 16 + li] = ww[eb][r];
-        }
-    } else {
-      xs += __shfl_xor(xs, 16);
-      xs += __shfl_xor(xs, 32);
-      if (lg == 0) norm_part[slice][li] = xs;
-#pragma unroll
-      for (int eb = 0; eb < EB; ++eb) {
-        wsum[eb] += __shfl_xor(wsum[eb], 16);
-        wsum[eb] += __shfl_xor(wsum[eb], 32);
-        if (lg == 0) norm_part[slice][kTok + eb * 16 + li] = wsum[eb];
-      }
-    }
-  }
-  const TokenState s = {&logit[0][0], x_norm, w_norm, &refined[0][0], work, &n_work, EP};
-  if (threadIdx.x < kTok * 8) (&refined[0][0])[threadIdx.x] = 0;
-  if (threadIdx.x == 0) n_work = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n * EP; i += kWaves * kWave) {
-    const int t = i / EP, e = i % EP;
-    double v = 0;
-#pragma unroll
-    for (int k = 0; k < kSlices; ++k) v += (double)part[k][t][e];
-    if (e < a.E) put_logit(a, s, t, e, v);
-  }
-  if (threadIdx.x < kTok + EP) {
-    float v = 0.f;
-#pragma unroll
-    for (int k = 0; k < kSlices; ++k) v += norm_part[k][threadIdx.x];
-    // the sum of squares is off by less than a thousandth
-    v = sqrtf(v) * 1.01f;
-    if (threadIdx.x < kTok) x_norm[threadIdx.x] = v;
-    else w_norm[threadIdx.x - kTok] = v;
-  }
-  __syncthreads();
-  // the parts of the slices are rounded to fp32 once more
-  choose_all<Act, kWaves, kTok, kSlots>(a, s, tok0, n, kMfmaUnits + 1.f);
+  for (int h = 0; h < 2; ++h) b.h[h] = *reinterpret_cast<const uint4*>(tile + li * kBlockBytes + 16 * ((2 * lg + h) ^ (li & 7)));
+  return b;
 }
 
-// ------------------------------------------------------------------ up to 256 experts
-constexpr int kWideWaves = 16;
-constexpr int kRowBytes = 256;   // of a token's row in a step
+// The block's sums x . w of 16 rows by 16, added to acc in fp64 one (bf16) or two (fp32) MFMAs at a time.
+template <typename Act>
+__device__ __forceinline__ void add_block(const Block& x, const Block& w, double (&acc)[4]) {
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  auto add = [&](const f32x4& p) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[r] += (double)p[r];
+  };
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (sizeof(Act) == 2) {
+      add(mfma_bf16(as_bf16x8(x.h[h]), as_bf16x8(w.h[h]), zero));
+    } else {
+      const f32x4 u = __builtin_bit_cast(f32x4, x.h[h]), v = __builtin_bit_cast(f32x4, w.h[h]);
+      add(mfma_f32(u[1], v[1], mfma_f32(u[0], v[0], zero)));
+      add(mfma_f32(u[3], v[3], mfma_f32(u[2], v[2], zero)));
+    }
+  }
+}
 
-// One workgroup scores 16*TB tokens. Its 16 waves take a block of 16 experts each (KS = 1), or half of the chunks of
-// one (KS = 2, up to 128 experts), and share the tokens' rows through LDS (direct loads, double buffered; 16-byte pieces
-// XOR-swizzled by the row). The weights go to the registers of the one wave that needs them, a step ahead.
-template <typename Act, int TB, int KS>
-__global__ __launch_bounds__(kWideWaves* kWave) void route_gated_wide_kernel(GateArgs a) {
-  constexpr int EP = kMaxExperts / KS;
-  constexpr int TOK = 16 * TB;
-  constexpr int CS = kRowBytes / (32 * (int)sizeof(Act));   // 32-wide chunks of a step: 4 or 2
-  constexpr int WC = CS / KS;                               // of a wave
-  constexpr int STAGE = TOK * kRowBytes;
-  __shared__ __attribute__((aligned(1024))) uint8_t xs[2][STAGE];
-  __shared__ double logit[TOK][EP];
-  __shared__ float x_norm[TOK], w_norm[EP];
-  __shared__ uint32_t refined[TOK][8];
-  __shared__ uint16_t work[TOK * EP];
-  __shared__ int n_work;
+// A lane's part of the squares of its row's block.
+template <typename Act>
+__device__ __forceinline__ void add_squares(const Block& b, float& sum) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t u[4] = {b.h[h].x, b.h[h].y, b.h[h].z, b.h[h].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(Act) == 2) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        const bf16x2 v = __builtin_bit_cast(bf16x2, u[j]);
+        sum = __builtin_amdgcn_fdot2_f32_bf16(v, v, sum, false);
+      } else {
+        const float v = __uint_as_float(u[j]);
+        sum += v * v;
+      }
+    }
+  }
+}
+
+// The squares of row l%16 over the lanes that hold it.
+__device__ __forceinline__ float row_squares(float v) {
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+
+// A norm from its square, whose own sum is off by less than a thousandth, rounded up.
+__device__ __forceinline__ float norm_of(float square) { return sqrtf(square) * 1.01f; }
+
+// Shape of a logits tile: NEB blocks of 16 experts by TB blocks of 16 tokens by KS slices of the hidden dimension (block b
+// belongs to slice b % KS); wave (eb, ks) has expert block eb and slice ks, and all token blocks. A step is a
+// block of every slice; its rows lie in one of D stages of LDS, requested D - 1 steps ahead.
+template <int NEB, int TB, int kWaves, int D>
+struct Tile {
+  static constexpr int KS = kWaves / NEB;
+  static constexpr int EP = 16 * NEB;
+  static constexpr int TOK = 16 * TB;
+  static constexpr int kStage = (kWaves + KS * TB) * kTileBytes;
+  // the sums of the slices, then the choice's state, take the stages' place
+  static constexpr int kSums = KS * TOK * EP * 8;
+  static constexpr int kState = TOK * EP * (8 + 2);
+  static constexpr int kLds = D * kStage > kSums ? (D * kStage > kState ? D * kStage : kState) : (kSums > kState ? kSums : kState);
+};
+
+// Sums of x . w over the steps [s0, s1) of one workgroup's tokens, in fp64: sum[ks][token][expert] in LDS (lds, after a
+// barrier), the squares of the rows in x_sq [KS][TOK] and w_sq [KS][EP].
+template <typename Act, int NEB, int TB, int kWaves, int D>
+__device__ __forceinline__ void tile_logits(const GateArgs& a, int tok0, int n, int s0, int s1, uint8_t* lds, float* x_sq,
+                                            float* w_sq) {
+  using S = Tile<NEB, TB, kWaves, D>;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int li = lane & 15;
   const int lg = lane >> 4;
-  const int tok0 = blockIdx.x * TOK;
-  const int n = min(TOK, a.T - tok0);
-  const int d = a.d;
-  const int ks = wave / (16 / KS);
-  const int e = (wave % (16 / KS)) * 16 + li;
-  const bool active = (wave % (16 / KS)) * 16 < a.E;
-  const TokenState s = {&logit[0][0], x_norm, w_norm, &refined[0][0], work, &n_work, EP};
-  if (threadIdx.x < TOK * 8) (&refined[0][0])[threadIdx.x] = 0;
-  if (threadIdx.x < TOK) x_norm[threadIdx.x] = 0.f;
-  if (threadIdx.x < EP) w_norm[threadIdx.x] = 0.f;
-  if (threadIdx.x == 0) n_work = 0;
+  const int eb = wave % NEB, ks = wave / NEB;
+  const long row_bytes = (long)a.d * sizeof(Act);
+  const int blocks = (int)(row_bytes / kBlockBytes);
 
-  const uint8_t* x = static_cast<const uint8_t*>(a.x) + (long)tok0 * d * sizeof(Act);
-  const Act* wr = static_cast<const Act*>(a.router_w) + (long)min(e, a.E - 1) * d + 8 * lg;
-  const int chunks = d >> 5;
-  const int nsteps = (chunks + CS - 1) / CS;
-  // waves 0 .. 4*TB - 1 copy four rows each; the last step of bf16 rows may be half a step: its other half re-reads the first
-  const int row = wave * 4 + (lane >> 4);
-  const int piece = li ^ (row & 15);
-  const uint32_t x_off = (uint32_t)min(row, n - 1) * (uint32_t)(d * (int)sizeof(Act)) + 16u * piece;
-  auto issue_x = [&](int step, int buf) {
-    if (wave >= 4 * TB || step >= nsteps) return;
-    uint32_t off = x_off + (uint32_t)step * kRowBytes;
-    if (step * CS + CS > chunks && piece >= 8) off -= 128;
-    dma16(x, off, lds_addr(&xs[buf][0]) + wave * 1024);
-  };
-  constexpr int V = sizeof(Act) == 2 ? 1 : 2;   // 16-byte loads of a lane's 8 elements
-  auto load_w = [&](int step, uint4 (&b)[WC][V]) {
+  // sources: lane l of a load reads 16 bytes of row l/8 of eight rows, at the place that its LDS slot must hold
+  const int r8 = lane >> 3;
+  const uint32_t piece = 16u * (uint32_t)((lane & 7) ^ r8);
+  const uint8_t* xb = static_cast<const uint8_t*>(a.x) + tok0 * row_bytes;      // offsets below 32 rows: 32 bits
+  const uint8_t* wb = static_cast<const uint8_t*>(a.router_w);                  // 256 rows of 65536 at most
+  uint32_t w_off[2];
 #pragma unroll
-    for (int i = 0; i < WC; ++i) {
-      const int c = min(step * CS + i * KS + ks, chunks - 1);
+  for (int h = 0; h < 2; ++h) w_off[h] = (uint32_t)(min(eb * 16 + h * 8 + r8, a.E - 1) * row_bytes) + piece;
+  constexpr int XN = 2 * TB;                          // loads of a slice's token rows, dealt to its NEB waves
+  constexpr int XI = (XN + NEB - 1) / NEB;
+  uint32_t x_off[XI];
 #pragma unroll
-      for (int h = 0; h < V; ++h) b[i][h] = reinterpret_cast<const uint4*>(wr + 32 * (long)c)[h];
-    }
+  for (int i = 0; i < XI; ++i) x_off[i] = (uint32_t)(min((eb + NEB * i) * 8 + r8, n - 1) * row_bytes) + piece;
+  const int x_loads = eb < XN ? (XN - eb + NEB - 1) / NEB : 0;
+
+  const uint32_t base = lds_addr(lds);
+  auto issue = [&](int st) {
+    // past the end the last block again, so that a wave's loads stay countable
+    const uint32_t off = (uint32_t)min(min(st, s1 - 1) * S::KS + ks, blocks - 1) * kBlockBytes;
+    const uint32_t stage = base + (uint32_t)(st % D) * S::kStage;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) dma16(wb, w_off[h] + off, stage + wave * kTileBytes + h * 1024);
+#pragma unroll
+    for (int i = 0; i < XI; ++i)
+      if (i < x_loads) dma16(xb, x_off[i] + off, stage + (kWaves + ks * TB) * kTileBytes + (eb + NEB * i) * 1024);
   };
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  // all but the loads of the last `steps` steps have landed
+  auto wait = [&](auto steps) {
+    constexpr int K = decltype(steps)::value;
+    if constexpr (K == 0) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+    else if (x_loads == XI) __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(K * (2 + XI)));
+    else __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(K * (2 + XI - 1)));
+  };
+
   double acc[TB][4];
 #pragma unroll
   for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc[tb][r] = 0;
-  f32x4 xx = zero, ww = zero;
-  float xsum = 0.f, wsum = 0.f;
-  // a lane's 8 elements of chunk c of a step, token block tb
-  auto x_piece = [&](int buf, int tb, int c, int h) {
-    const int r = tb * 16 + li;
-    const int p = V == 1 ? 4 * c + lg : 8 * c + 2 * lg + h;
-    return *reinterpret_cast<const uint4*>(&xs[buf][r * kRowBytes + 16 * (p ^ li)]);
-  };
-  auto step_of = [&](int st, int buf, const uint4 (&b)[WC][V], uint4 (&bn)[WC][V]) {
-    // this step's rows have landed, and every wave is past the buffer that the next ones overwrite
+  float xs[TB], ws = 0.f;
+#pragma unroll
+  for (int tb = 0; tb < TB; ++tb) xs[tb] = 0.f;
+#pragma unroll
+  for (int i = 0; i < D - 1; ++i) issue(s0 + i);
+  for (int st = s0; st < s1; ++st) {
+    // this step's rows have landed, and every wave is past the stage that the next ones overwrite
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
+    wait(int_constant<D - 2>{});
     __builtin_amdgcn_s_barrier();
-    issue_x(st + 1, 1 - buf);
-    if (active && st + 1 < nsteps) load_w(st + 1, bn);
-    if (active) {
-      f32x4 p[TB];
+    issue(st + D - 1);
+    if (st * S::KS + ks < blocks) {
+      const uint8_t* stage = lds + (st % D) * S::kStage;
+      const Block w = lds_block(stage + wave * kTileBytes);
+      add_squares<Act>(w, ws);
 #pragma unroll
-      for (int i = 0; i < WC; ++i) {
-        const int c = i * KS + ks;
-        if (st * CS + c >= chunks) break;
-        // sums of two chunks with bf16, of one (a chain of eight) with fp32
-        if (V == 2 || i % 2 == 0)
-#pragma unroll
-          for (int tb = 0; tb < TB; ++tb) p[tb] = zero;
-        if constexpr (V == 1) {
-          const bf16x8 w = as_bf16x8(b[i][0]);
-          ww = mfma_bf16(w, w, ww);
-#pragma unroll
-          for (int tb = 0; tb < TB; ++tb) p[tb] = mfma_bf16(as_bf16x8(x_piece(buf, tb, c, 0)), w, p[tb]);
-        } else {
-          const f32x4 w[2] = {__builtin_bit_cast(f32x4, b[i][0]), __builtin_bit_cast(f32x4, b[i][V - 1])};
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            f32x4 u[TB];
-#pragma unroll
-            for (int tb = 0; tb < TB; ++tb) u[tb] = __builtin_bit_cast(f32x4, x_piece(buf, tb, c, h));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              wsum += w[h][j] * w[h][j];
-#pragma unroll
-              for (int tb = 0; tb < TB; ++tb) p[tb] = mfma_f32(u[tb][j], w[h][j], p[tb]);
-            }
-          }
-        }
-        if (V == 2 || i % 2 == 1 || i == WC - 1 || st * CS + c + KS >= chunks)
-#pragma unroll
-          for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[tb][r] += (double)p[tb][r];
+      for (int tb = 0; tb < TB; ++tb) {
+        const Block x = lds_block(stage + (kWaves + ks * TB + tb) * kTileBytes);
+        if (eb == 0) add_squares<Act>(x, xs[tb]);
+        add_block<Act>(x, w, acc[tb]);
       }
     }
-    // the tokens' norms: wave tb takes token block tb
-    if (wave < TB) {
-#pragma unroll
-      for (int c = 0; c < CS; ++c) {
-        if (st * CS + c >= chunks) break;
-#pragma unroll
-        for (int h = 0; h < V; ++h) {
-          const uint4 q = x_piece(buf, wave, c, h);
-          if constexpr (V == 1) {
-            xx = mfma_bf16(as_bf16x8(q), as_bf16x8(q), xx);
-          } else {
-            const f32x4 u = __builtin_bit_cast(f32x4, q);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) xsum += u[j] * u[j];
-          }
-        }
-      }
-    }
-  };
-  uint4 b[2][WC][V];
-  issue_x(0, 0);
-  if (active) load_w(0, b[0]);
-  for (int st = 0; st < nsteps; st += 2) {
-    step_of(st, 0, b[0], b[1]);
-    if (st + 1 < nsteps) step_of(st + 1, 1, b[1], b[0]);
   }
-
-  // norms (1.01: the sum of squares is off by less than a thousandth), and the slices' sums
-  if constexpr (V == 2) {
-    xsum += __shfl_xor(xsum, 16);
-    xsum += __shfl_xor(xsum, 32);
-    wsum += __shfl_xor(wsum, 16);
-    wsum += __shfl_xor(wsum, 32);
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    if (V == 1 ? 4 * lg + r != li : lg > 0 || r > 0) continue;
-    if (wave < TB) x_norm[wave * 16 + li] = sqrtf(V == 1 ? xx[r] : xsum) * 1.01f;
-    if (active && KS == 1) w_norm[e] = sqrtf(V == 1 ? ww[r] : wsum) * 1.01f;
-    if (active && KS == 2) atomicAdd(&w_norm[e], V == 1 ? ww[r] : wsum);   // squares; two addends
-  }
-  if (KS == 2 && active && ks == 1) {
-#pragma unroll
-    for (int tb = 0; tb < TB; ++tb)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) logit[tb * 16 + 4 * lg + r][e] = acc[tb][r];
-  }
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));   // the loads past the end too
   __syncthreads();
-  if (KS == 2 && threadIdx.x < EP) w_norm[threadIdx.x] = sqrtf(w_norm[threadIdx.x]) * 1.01f;
-  if (active && ks == 0) {
+  // lane l holds tokens 16*tb + 4*lg + r of expert 16*eb + li
+  double* sum = reinterpret_cast<double*>(lds) + ks * S::TOK * S::EP;
 #pragma unroll
-    for (int tb = 0; tb < TB; ++tb)
+  for (int tb = 0; tb < TB; ++tb) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = tb * 16 + 4 * lg + r;
-        if (t < n && e < a.E) put_logit(a, s, t, e, KS == 2 ? acc[tb][r] + logit[t][e] : acc[tb][r]);
-      }
+    for (int r = 0; r < 4; ++r) sum[(tb * 16 + 4 * lg + r) * S::EP + eb * 16 + li] = acc[tb][r];
+    xs[tb] = row_squares(xs[tb]);
+    if (eb == 0 && lg == 0) x_sq[ks * S::TOK + tb * 16 + li] = xs[tb];
   }
+  ws = row_squares(ws);
+  if (lg == 0) w_sq[ks * S::EP + eb * 16 + li] = ws;
   __syncthreads();
-  const float units = V == 1 ? 2 * kMfmaUnits : kMfmaUnits;
-  // slots of a lane: experts of a group over its lanes, 8 at most; 4 if the groups are a power of two, as they mostly are
-  const ChoiceMap map(a, lane);
-  if (map.size <= 4 * map.lanes) choose_all<Act, kWideWaves, TOK, 4>(a, s, tok0, n, units);
-  else choose_all<Act, kWideWaves, TOK, 8>(a, s, tok0, n, units);
 }
 
-template <typename Act, int EB>
-void launch_narrow(const GateArgs& a, hipStream_t stream) {
-  // as few tokens a workgroup as leave no CU without one, so that a small batch's reads of router_w are spread
-  const int tpw = min(kTok, (a.T + 255) / 256);
-  const dim3 grid((a.T + tpw - 1) / tpw);
-  // few workgroups: the most waves each; many: two workgroups a CU, one of which loads while the other chooses
-  if (grid.x <= 256) hipLaunchKernelGGL((route_gated_kernel<Act, EB, 16>), grid, dim3(16 * kWave), 0, stream, a, tpw);
-  else hipLaunchKernelGGL((route_gated_kernel<Act, EB, 8>), grid, dim3(8 * kWave), 0, stream, a, tpw);
+// What a workgroup's choice needs besides the logits.
+template <int TOK, int EP>
+struct ChoiceLds {
+  float x_norm[TOK], w_norm[EP];
+  uint32_t refined[TOK][8];
+  int n_work;
+};
+
+template <typename Act, int kWaves, int TOK, int EP>
+__device__ __forceinline__ void choose_tokens(const GateArgs& a, const TokenState& s, int tok0, int n) {
+  // Slots of a lane: a group's experts over its lanes, of which there are more than 32 / groups. With up to 256 experts 8;
+  // 4 if the groups are a power of two, as they mostly are.
+  if constexpr (EP <= 32) {
+    choose_all<Act, kWaves, TOK, 1>(a, s, tok0, n, kMfmaUnits);
+  } else if constexpr (EP <= 64) {
+    choose_all<Act, kWaves, TOK, 2>(a, s, tok0, n, kMfmaUnits);
+  } else {
+    const ChoiceMap map(a, threadIdx.x & 63);
+    if (map.size <= 4 * map.lanes) choose_all<Act, kWaves, TOK, 4>(a, s, tok0, n, kMfmaUnits);
+    else choose_all<Act, kWaves, TOK, 8>(a, s, tok0, n, kMfmaUnits);
+  }
 }
 
-template <typename Act, int TB>
-void launch_wide(const GateArgs& a, hipStream_t stream) {
-  const dim3 grid((a.T + 16 * TB - 1) / (16 * TB)), block(kWideWaves * kWave);
-  if (a.E <= 128) hipLaunchKernelGGL((route_gated_wide_kernel<Act, TB, 2>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((route_gated_wide_kernel<Act, TB, 1>), grid, block, 0, stream, a);
+// Logits and choice of 16*TB tokens in one workgroup.
+template <typename Act, int NEB, int TB, int kWaves, int D>
+__global__ __launch_bounds__(kWaves* kWave, 4) void route_gated_kernel(GateArgs a, int tpw) {
+  using S = Tile<NEB, TB, kWaves, D>;
+  constexpr int EP = S::EP, TOK = S::TOK, KS = S::KS;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
+  __shared__ float x_sq[KS * TOK], w_sq[KS * EP];
+  __shared__ ChoiceLds<TOK, EP> c;
+  const int tok0 = blockIdx.x * tpw;
+  const int n = min(tpw, a.T - tok0);
+  const int blocks = (int)((long)a.d * sizeof(Act) / kBlockBytes);
+  if (threadIdx.x < TOK * 8) (&c.refined[0][0])[threadIdx.x] = 0;
+  if (threadIdx.x == 0) c.n_work = 0;
+  tile_logits<Act, NEB, TB, kWaves, D>(a, tok0, n, 0, (blocks + KS - 1) / KS, lds, x_sq, w_sq);
+
+  // the slices' sums, each thread's before any is overwritten
+  constexpr int kPer = (TOK * EP + kWaves * kWave - 1) / (kWaves * kWave);
+  double v[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = threadIdx.x + i * kWaves * kWave;
+    v[i] = 0;
+    if (at < TOK * EP)
+#pragma unroll
+      for (int k = 0; k < KS; ++k) v[i] += reinterpret_cast<const double*>(lds)[k * TOK * EP + at];
+  }
+  for (int i = threadIdx.x; i < TOK + EP; i += kWaves * kWave) {
+    float q = 0.f;
+#pragma unroll
+    for (int k = 0; k < KS; ++k) q += i < TOK ? x_sq[k * TOK + i] : w_sq[k * EP + i - TOK];
+    if (i < TOK) c.x_norm[i] = norm_of(q);
+    else c.w_norm[i - TOK] = norm_of(q);
+  }
+  __syncthreads();
+  const TokenState s = {reinterpret_cast<double*>(lds), c.x_norm, c.w_norm, &c.refined[0][0],
+                        reinterpret_cast<uint16_t*>(lds + TOK * EP * 8), &c.n_work, EP};
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int at = threadIdx.x + i * kWaves * kWave, t = at / EP, e = at % EP;
+    if (t < n && e < a.E) put_logit(a, s, t, e, v[i]);
+  }
+  __syncthreads();
+  choose_tokens<Act, kWaves, TOK, EP>(a, s, tok0, n);
+}
+
+template <typename Act, int NEB>
+void launch_experts(const GateArgs& a, hipStream_t stream) {
+  constexpr int D = NEB == 1 ? 2 : 3;
+  if constexpr (NEB <= 4) {
+    // as few tokens a workgroup as leave no CU without one, so that a small batch's reads of router_w are spread
+    const int tpw = min(16, (a.T + 255) / 256);
+    const dim3 grid((a.T + tpw - 1) / tpw);
+    // few workgroups: the most waves each; many: two workgroups a CU, one of which loads while the other chooses
+    if (grid.x <= 256) hipLaunchKernelGGL((route_gated_kernel<Act, NEB, 1, 16, D>), grid, dim3(16 * kWave), 0, stream, a, tpw);
+    else hipLaunchKernelGGL((route_gated_kernel<Act, NEB, 1, 8, D>), grid, dim3(8 * kWave), 0, stream, a, tpw);
+  } else if (a.T <= 16 * 256) {
+    hipLaunchKernelGGL((route_gated_kernel<Act, NEB, 1, 16, D>), dim3((a.T + 15) / 16), dim3(16 * kWave), 0, stream, a, 16);
+  } else {
+    hipLaunchKernelGGL((route_gated_kernel<Act, NEB, 2, 16, D>), dim3((a.T + 31) / 32), dim3(16 * kWave), 0, stream, a, 32);
+  }
 }
 
 template <typename Act>
 void launch(const GateArgs& a, hipStream_t stream) {
-  if (a.E <= 16) launch_narrow<Act, 1>(a, stream);
-  else if (a.E <= 32) launch_narrow<Act, 2>(a, stream);
-  else if (a.E <= 64) launch_narrow<Act, 4>(a, stream);
-  else if (a.T <= 256 * 16) launch_wide<Act, 1>(a, stream);
-  else launch_wide<Act, 2>(a, stream);
+  if (a.E <= 16) launch_experts<Act, 1>(a, stream);
+  else if (a.E <= 32) launch_experts<Act, 2>(a, stream);
+  else if (a.E <= 64) launch_experts<Act, 4>(a, stream);
+  else if (a.E <= 128) launch_experts<Act, 8>(a, stream);
+  else launch_experts<Act, 16>(a, stream);
 }
 
 }  // namespace
