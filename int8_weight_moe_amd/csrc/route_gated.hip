@@ -12,7 +12,7 @@
 // waves of a workgroup, in blocks of 128 bytes of a row (whole cache lines). A
 // block's sums are added in fp64, so a logit is off by at most
 //     delta = units * 2^-23 * |x| |w_e|
-// (units: what the MFMAs' own sums round, see kMfmaUnits; sum |x_i w_i| <= |x| |w_e|).
+// (units: what the MFMAs' own sums round, see kSumUnits; sum |x_i w_i| <= |x| |w_e|).
 // |x|^2 and |w_e|^2 are taken on the way.
 // Choice: one wave a token, first in fp32 with an error bound eps_e on every c_e
 // (delta through the score's derivative, the evaluation, the bias's rounding). A
@@ -29,12 +29,14 @@ namespace {
 
 constexpr int kMaxExperts = 256;
 
-// What an MFMA sum is taken to be off by, in 2^-23 of the sum of its terms'
-// magnitudes: the 16x16x32 bf16 MFMA adds four groups of eight products, each
-// sum rounded (2 units; measured over one-sided and mixed sums with up to 24
-// bits between the terms: 2.5); a chain of two 16x16x4 fp32 MFMAs rounds eight sums
-// (4 units; measured for a chain of eight: 9.9).
-constexpr float kMfmaUnits = 4.f;
+// What the fp32 sums of a block are taken to be off by, in 2^-23 of the sum of their
+// terms' magnitudes. A 16x16x32 bf16 MFMA adds four groups of eight products, each
+// sum rounded to nearest (2 units; measured over one-sided and mixed sums with up
+// to 24 bits between the terms: 2.5), and two of them make a sum: 6 with the slack
+// of one. A chain of four 16x16x4 fp32 MFMAs rounds 16 sums: 8 (a chain of eight
+// measured: 9.9 of 16).
+template <typename Act>
+constexpr float kSumUnits = sizeof(Act) == 2 ? 6.f : 8.f;
 constexpr float kUnit = 0x1p-23f;
 
 __device__ __forceinline__ void load8d(const __bf16* p, double (&v)[8]) {
@@ -445,51 +447,59 @@ __device__ __forceinline__ Block lds_block(const uint8_t* tile) {
   return b;
 }
 
-// The block's sums x . w of 16 rows by 16, added to acc in fp64 one (bf16) or two (fp32) MFMAs at a time.
+// The block's sums x . w of 16 rows by 16, added to acc in fp64: one sum of two MFMAs (bf16), two of four (fp32). The
+// conversions and additions are what the sums cost: one a MFMA took 1.6 times as long with 256 experts.
 template <typename Act>
 __device__ __forceinline__ void add_block(const Block& x, const Block& w, double (&acc)[4]) {
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-  auto add = [&](const f32x4& p) {
-#pragma unroll
-    for (int r = 0; r < 4; ++r) acc[r] += (double)p[r];
-  };
+  f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if constexpr (sizeof(Act) == 2) {
-      add(mfma_bf16(as_bf16x8(x.h[h]), as_bf16x8(w.h[h]), zero));
+      p = mfma_bf16(as_bf16x8(x.h[h]), as_bf16x8(w.h[h]), p);
+      if (h == 0) continue;
     } else {
       const f32x4 u = __builtin_bit_cast(f32x4, x.h[h]), v = __builtin_bit_cast(f32x4, w.h[h]);
-      add(mfma_f32(u[1], v[1], mfma_f32(u[0], v[0], zero)));
-      add(mfma_f32(u[3], v[3], mfma_f32(u[2], v[2], zero)));
+      p = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p = mfma_f32(u[j], v[j], p);
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[r] += (double)p[r];
   }
 }
 
-// A lane's part of the squares of its row's block.
+// The squares of 16 rows, block by block: with bf16 the diagonal of a tile rows . rows (an MFMA costs its wave
+// nothing next to the sums' additions), with fp32 a lane's share of its row.
 template <typename Act>
-__device__ __forceinline__ void add_squares(const Block& b, float& sum) {
+struct Squares {
+  f32x4 tile = {0.f, 0.f, 0.f, 0.f};
+  float mine = 0.f;
+  __device__ void add(const Block& b) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t u[4] = {b.h[h].x, b.h[h].y, b.h[h].z, b.h[h].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int h = 0; h < 2; ++h) {
       if constexpr (sizeof(Act) == 2) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        const bf16x2 v = __builtin_bit_cast(bf16x2, u[j]);
-        sum = __builtin_amdgcn_fdot2_f32_bf16(v, v, sum, false);
+        tile = mfma_bf16(as_bf16x8(b.h[h]), as_bf16x8(b.h[h]), tile);
       } else {
-        const float v = __uint_as_float(u[j]);
-        sum += v * v;
+        const f32x4 u = __builtin_bit_cast(f32x4, b.h[h]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mine += u[j] * u[j];
       }
     }
   }
-}
-
-// The squares of row l%16 over the lanes that hold it.
-__device__ __forceinline__ float row_squares(float v) {
-  v += __shfl_xor(v, 16);
-  return v + __shfl_xor(v, 32);
-}
+  // out[row], by the lanes that hold a row's sum
+  __device__ void store(float* out) {
+    const int li = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
+    if constexpr (sizeof(Act) == 2) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (4 * lg + r == li) out[li] = tile[r];
+    } else {
+      mine += __shfl_xor(mine, 16);
+      mine += __shfl_xor(mine, 32);
+      if (lg == 0) out[li] = mine;
+    }
+  }
+};
 
 // A norm from its square, whose own sum is off by less than a thousandth, rounded up.
 __device__ __forceinline__ float norm_of(float square) { return sqrtf(square) * 1.01f; }
@@ -538,10 +548,15 @@ __device__ __forceinline__ void tile_logits(const GateArgs& a, int tok0, int n, 
   for (int i = 0; i < XI; ++i) x_off[i] = (uint32_t)(min((eb + NEB * i) * 8 + r8, n - 1) * row_bytes) + piece;
   const int x_loads = eb < XN ? (XN - eb + NEB - 1) / NEB : 0;
 
+  // Workgroups start at different steps: rows a power of two apart lie in the same memory channels, which workgroups in
+  // step would ask for all at once (16384 tokens, 16 experts: 64 -> 52 us without the choice). The sums of fp32 sums
+  // lose nothing in fp64 unless one is 2^-27 of the others, so their order does not show.
+  const int turn = (blockIdx.x >> 3) % (s1 - s0);
+  auto turned = [&](int st) { return st + turn >= s1 ? st + turn - (s1 - s0) : st + turn; };
   const uint32_t base = lds_addr(lds);
   auto issue = [&](int st) {
-    // past the end the last block again, so that a wave's loads stay countable
-    const uint32_t off = (uint32_t)min(min(st, s1 - 1) * S::KS + ks, blocks - 1) * kBlockBytes;
+    // past the end the last step again, so that a wave's loads stay countable
+    const uint32_t off = (uint32_t)min(turned(min(st, s1 - 1)) * S::KS + ks, blocks - 1) * kBlockBytes;
     const uint32_t stage = base + (uint32_t)(st % D) * S::kStage;
 #pragma unroll
     for (int h = 0; h < 2; ++h) dma16(wb, w_off[h] + off, stage + wave * kTileBytes + h * 1024);
@@ -562,9 +577,7 @@ __device__ __forceinline__ void tile_logits(const GateArgs& a, int tok0, int n, 
   for (int tb = 0; tb < TB; ++tb)
 #pragma unroll
     for (int r = 0; r < 4; ++r) acc[tb][r] = 0;
-  float xs[TB], ws = 0.f;
-#pragma unroll
-  for (int tb = 0; tb < TB; ++tb) xs[tb] = 0.f;
+  Squares<Act> xs[TB], ws;
 #pragma unroll
   for (int i = 0; i < D - 1; ++i) issue(s0 + i);
   for (int st = s0; st < s1; ++st) {
@@ -573,14 +586,14 @@ __device__ __forceinline__ void tile_logits(const GateArgs& a, int tok0, int n, 
     wait(int_constant<D - 2>{});
     __builtin_amdgcn_s_barrier();
     issue(st + D - 1);
-    if (st * S::KS + ks < blocks) {
+    if (turned(st) * S::KS + ks < blocks) {
       const uint8_t* stage = lds + (st % D) * S::kStage;
       const Block w = lds_block(stage + wave * kTileBytes);
-      add_squares<Act>(w, ws);
+      ws.add(w);
 #pragma unroll
       for (int tb = 0; tb < TB; ++tb) {
         const Block x = lds_block(stage + (kWaves + ks * TB + tb) * kTileBytes);
-        if (eb == 0) add_squares<Act>(x, xs[tb]);
+        if (eb == 0) xs[tb].add(x);
         add_block<Act>(x, w, acc[tb]);
       }
     }
@@ -593,11 +606,9 @@ __device__ __forceinline__ void tile_logits(const GateArgs& a, int tok0, int n, 
   for (int tb = 0; tb < TB; ++tb) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) sum[(tb * 16 + 4 * lg + r) * S::EP + eb * 16 + li] = acc[tb][r];
-    xs[tb] = row_squares(xs[tb]);
-    if (eb == 0 && lg == 0) x_sq[ks * S::TOK + tb * 16 + li] = xs[tb];
+    if (eb == 0) xs[tb].store(x_sq + ks * S::TOK + tb * 16);
   }
-  ws = row_squares(ws);
-  if (lg == 0) w_sq[ks * S::EP + eb * 16 + li] = ws;
+  ws.store(w_sq + ks * S::EP + eb * 16);
   __syncthreads();
 }
 
@@ -614,13 +625,13 @@ __device__ __forceinline__ void choose_tokens(const GateArgs& a, const TokenStat
   // Slots of a lane: a group's experts over its lanes, of which there are more than 32 / groups. With up to 256 experts 8;
   // 4 if the groups are a power of two, as they mostly are.
   if constexpr (EP <= 32) {
-    choose_all<Act, kWaves, TOK, 1>(a, s, tok0, n, kMfmaUnits);
+    choose_all<Act, kWaves, TOK, 1>(a, s, tok0, n, kSumUnits<Act>);
   } else if constexpr (EP <= 64) {
-    choose_all<Act, kWaves, TOK, 2>(a, s, tok0, n, kMfmaUnits);
+    choose_all<Act, kWaves, TOK, 2>(a, s, tok0, n, kSumUnits<Act>);
   } else {
     const ChoiceMap map(a, threadIdx.x & 63);
-    if (map.size <= 4 * map.lanes) choose_all<Act, kWaves, TOK, 4>(a, s, tok0, n, kMfmaUnits);
-    else choose_all<Act, kWaves, TOK, 8>(a, s, tok0, n, kMfmaUnits);
+    if (map.size <= 4 * map.lanes) choose_all<Act, kWaves, TOK, 4>(a, s, tok0, n, kSumUnits<Act>);
+    else choose_all<Act, kWaves, TOK, 8>(a, s, tok0, n, kSumUnits<Act>);
   }
 }
 
