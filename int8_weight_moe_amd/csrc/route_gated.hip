@@ -161,39 +161,53 @@ struct ChoiceMap {
   }
 };
 
+// Compare and exchange: the larger value first, of equal ones the lower id.
+template <typename Real>
+__device__ __forceinline__ void order(Real& v0, Real& e0, int& i0, Real& v1, Real& e1, int& i1) {
+  const bool swap = v1 > v0 || (v1 == v0 && (i1 & 0xffff) < (i0 & 0xffff));
+  const Real v = v0, e = e0;
+  const int i = i0;
+  v0 = swap ? v1 : v0;
+  e0 = swap ? e1 : e0;
+  i0 = swap ? i1 : i0;
+  v1 = swap ? v : v1;
+  e1 = swap ? e : e1;
+  i1 = swap ? i : i1;
+}
+
 // One token's choice by one wave, in fp32 or fp64. Returns whether it is taken (and written); else the experts that it
 // hangs on are appended to the work.
 template <typename Real, int kSlots>
 __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, int t, int32_t* ids, float* w, float units) {
   constexpr bool kDouble = sizeof(Real) == 8;
   constexpr Real kNone = -INFINITY;
+  constexpr int kOpen = 1 << 16, kMark = 1 << 17;   // beside an expert's id: not refined; the choice hangs on its logit
   const int lane = threadIdx.x & 63;
   const ChoiceMap map(a, lane);
   const double* logit = s.logit + t * s.stride;
   const float xn = s.x_norm[t];
   Real arg[kSlots], c[kSlots], eps[kSlots];   // arg: the exponential's argument; c +- eps: the value that decides
   float delta[kSlots];
-  int e_of[kSlots];
-  bool open[kSlots];                          // not refined
+  int id[kSlots];                             // -1: no expert
   Real m = kNone;
   float dmax = 0.f;
 #pragma unroll
   for (int j = 0; j < kSlots; ++j) {
     const int i = map.i0 + j * map.lanes;
-    const bool valid = map.group < a.groups && i < map.size;
-    const int e = valid ? map.group * map.size + i : -1;
-    e_of[j] = e;
-    open[j] = false;
+    const int e = map.group * map.size + i;
+    id[j] = -1;
     delta[j] = 0.f;
     arg[j] = 0;
-    if (valid) {
-      arg[j] = (Real)logit[e];
-      open[j] = !((s.refined[t * 8 + (e >> 5)] >> (e & 31)) & 1u);
-      if (open[j]) {
+    if (map.group < a.groups && i < map.size) {
+      const double l = logit[e];
+      arg[j] = (Real)l;
+      id[j] = e;
+      if (!((s.refined[t * 8 + (e >> 5)] >> (e & 31)) & 1u)) {
+        id[j] = e | kOpen;
         const float wn = s.w_norm[e];
         delta[j] = units * kUnit * xn * wn;
         // norms that say nothing: past the fp32 range, or lost below it
-        if (!(delta[j] < INFINITY) || ((xn < 0x1p-45f || wn < 0x1p-45f) && logit[e] != 0)) delta[j] = INFINITY;
+        if (!(delta[j] < INFINITY) || ((xn < 0x1p-45f || wn < 0x1p-45f) && l != 0)) delta[j] = INFINITY;
       }
       m = fmax(m, arg[j]);
       dmax = fmaxf(dmax, delta[j]);
@@ -207,7 +221,7 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
     z = 0;
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
-      if (e_of[j] >= 0) {
+      if (id[j] >= 0) {
         arg[j] -= m;
         c[j] = exp_of(arg[j]);
         z += c[j];
@@ -217,9 +231,9 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
 #pragma unroll
   for (int j = 0; j < kSlots; ++j) {
     Real v = kNone, err = 0;
-    if (e_of[j] >= 0) {
+    if (id[j] >= 0) {
       const Real score = a.sigmoid ? 1 / (1 + exp_of(-arg[j])) : c[j] / z;
-      const Real b = a.select_bias ? (Real)a.select_bias[e_of[j]] : (Real)0;
+      const Real b = a.select_bias ? (Real)a.select_bias[id[j] & 0xffff] : (Real)0;
       v = score + b;
       // the score's change with its logit: s (1 - s), or s; exp(x) - 1 <= 1.3 x up to 0.5
       const float from = a.sigmoid ? delta[j] : delta[j] + dmax;
@@ -239,8 +253,7 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
 
   // next to a bias a softmax hangs on every logit, through the sum
   const bool all = !a.sigmoid && a.select_bias;
-  uint32_t marks = 0;   // bit j: the choice hangs on slot j's logit
-  auto unsure = [&](int j) { return open[j] || (all && dmax > 0.f); };
+  auto unsure = [&](int i) { return i >= 0 && ((i & kOpen) || (all && dmax > 0.f)); };
   if (a.groups > 1) {
     Top2<Real> vc;
 #pragma unroll
@@ -283,7 +296,7 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
         const bool near = kept ? !(lo > ceil) : real && !(hi < floor);
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
-          if (near && unsure(j) && c[j] > kNone && !(c[j] + eps[j] < least)) marks |= 1u << j;
+          if (near && unsure(id[j]) && c[j] > kNone && !(c[j] + eps[j] < least)) id[j] |= kMark;
       }
     }
 #pragma unroll
@@ -294,64 +307,94 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
       }
   }
 
-  // K rounds; lane k keeps round k's expert and its value's ends
-  uint32_t picked = 0;   // bit j: slot j was taken
+  // a lane's experts in descending order (an odd-even merge sort's exchanges)
+  auto exchange = [&](int i, int j) { order(c[i], eps[i], id[i], c[j], eps[j], id[j]); };
+  if constexpr (kSlots == 2) exchange(0, 1);
+  if constexpr (kSlots >= 4) {
+#pragma unroll
+    for (int h = 0; h < kSlots; h += 4) {
+      exchange(h, h + 1);
+      exchange(h + 2, h + 3);
+      exchange(h, h + 2);
+      exchange(h + 1, h + 3);
+      exchange(h + 1, h + 2);
+    }
+  }
+  if constexpr (kSlots == 8) {
+    exchange(0, 4);
+    exchange(1, 5);
+    exchange(2, 6);
+    exchange(3, 7);
+    exchange(2, 4);
+    exchange(3, 5);
+    exchange(1, 2);
+    exchange(3, 4);
+    exchange(5, 6);
+  }
+  // K rounds: the largest of the lanes' first ones, which its lane then drops; lane k keeps round k's
   int my_id = -1;
   Real my_lo = kNone, my_hi = kNone;
   for (int k = 0; k < a.K; ++k) {
-    Real v = kNone;
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j) v = fmax(v, picked >> j & 1 ? kNone : c[j]);
-    const Real top = wave_max(v);
+    const Real top = wave_max(c[0]);
     if (!(top > kNone)) break;
-    int e = kMaxExperts, slot = 0;
-    Real err = 0;
-#pragma unroll
-    for (int j = kSlots - 1; j >= 0; --j)   // a lane's experts ascend with the slot
-      if (!(picked >> j & 1) && c[j] == top) {
-        e = e_of[j];
-        slot = j;
-        err = eps[j];
-      }
-    const uint64_t equal = __ballot(e < kMaxExperts);
+    const uint64_t equal = __ballot(c[0] == top);
     int owner = __ffsll((unsigned long long)equal) - 1;
-    if (__popcll(equal) > 1) owner = __ffsll((unsigned long long)__ballot(e == wave_min(e))) - 1;
-    if (lane == owner) picked |= 1u << slot;
-    err = lane_value(err, owner);
-    e = lane_value(e, owner);
+    if (__popcll(equal) > 1) {
+      const int e = c[0] == top ? id[0] & 0xffff : kMaxExperts;
+      owner = __ffsll((unsigned long long)__ballot(e == wave_min(e))) - 1;
+    }
+    const Real err = lane_value(eps[0], owner);
+    const int i = lane_value(id[0], owner);
     if (lane == k) {
-      my_id = e;
+      my_id = i;
       my_lo = top - err;
       my_hi = top + err;
+    }
+    if (lane == owner) {
+#pragma unroll
+      for (int j = 0; j + 1 < kSlots; ++j) {
+        c[j] = c[j + 1];
+        eps[j] = eps[j + 1];
+        id[j] = id[j + 1];
+      }
+      c[kSlots - 1] = kNone;
+      eps[kSlots - 1] = 0;
+      id[kSlots - 1] = -1;
     }
   }
   {
     // every pick lies above all that rank after it
     Real above = kNone;
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j)
-      if (!(picked >> j & 1)) above = fmax(above, c[j] + eps[j]);
+    for (int j = 0; j < kSlots; ++j) above = fmax(above, c[j] + eps[j]);
     above = wave_max(above);
     for (int k = a.K - 1; k >= 0; --k) {
       const Real lo = lane_value(my_lo, k), hi = lane_value(my_hi, k);
-      const int e = lane_value(my_id, k);
-      if (e >= 0 && !(lo > above)) {
-        // it, and what may lie above its lower end (those that rank before it too: they do no harm)
+      if (lo > kNone && !(lo > above)) {
+        // it, and what may lie above its lower end
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
-          if (unsure(j) && (e_of[j] == e || (c[j] > kNone && !(c[j] + eps[j] < lo) && !(c[j] - eps[j] > hi)))) marks |= 1u << j;
+          if (unsure(id[j]) && c[j] > kNone && !(c[j] + eps[j] < lo)) id[j] |= kMark;
+        if (lane >= k && unsure(my_id) && (lane == k || !(my_hi < lo))) my_id |= kMark;
       }
       above = fmax(above, hi);
     }
   }
-  if (__any(marks != 0)) {
+  bool hangs = my_id >= 0 && (my_id & kMark);
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j)
-      if (open[j] && (all || marks >> j & 1)) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | e_of[j]);
+  for (int j = 0; j < kSlots; ++j) hangs = hangs || (id[j] >= 0 && (id[j] & kMark));
+  if (__any(hangs)) {
+    auto append = [&](int i) {
+      if (i >= 0 && (i & kOpen) && (all || (i & kMark))) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | (i & 0xff));
+    };
+    append(my_id);
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) append(id[j]);
     return false;
   }
 
   // weights, in fp64 from the logits of the chosen (lanes 0 .. 7)
+  if (my_id >= 0) my_id &= 0xffff;
   double sk = 0;
   if (my_id >= 0) sk = a.sigmoid ? 1 / (1 + exp(-logit[my_id])) : exp(logit[my_id] - m);
   double total = 1;
