@@ -14,12 +14,12 @@
 //     delta = units * 2^-23 * |x| |w_e|
 // (units: what the MFMAs' own sums round, see kSumUnits; sum |x_i w_i| <= |x| |w_e|).
 // |x|^2 and |w_e|^2 are taken on the way.
-// Choice: one wave a token, first in fp32 with an error bound eps_e on every c_e
-// (delta through the score's derivative, the evaluation, the bias's rounding). A
-// decision between two values whose intervals overlap is not taken: the experts it
-// hangs on are marked, the workgroup's waves compute their logits again in fp64, and the
-// choice is repeated in fp64, until no decision hangs on an unrefined logit. So
-// the ids are those of 64-bit values, at the price of fp32 ones.
+// Choice: one wave a token, in fp32 with an error bound eps_e on every c_e (delta
+// through the score's derivative, the evaluation, the bias's rounding). A decision
+// between two values whose intervals overlap is not taken: the experts it hangs on
+// are marked, the workgroup's waves compute their logits again in fp64, and the choice is
+// repeated, in fp64 if it then hangs on the fp32 evaluation alone. So the ids are
+// those of 64-bit values, at the price of fp32 ones.
 #include "device_common.h"
 #include "kernels.h"
 
@@ -38,23 +38,6 @@ constexpr int kMaxExperts = 256;
 template <typename Act>
 constexpr float kSumUnits = sizeof(Act) == 2 ? 6.f : 8.f;
 constexpr float kUnit = 0x1p-23f;
-
-__device__ __forceinline__ void load8d(const __bf16* p, double (&v)[8]) {
-  const u32x4 u = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void load8d(const float* p, double (&v)[8]) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[i] = a[i];
-    v[4 + i] = b[i];
-  }
-}
 
 // ---- reductions over a wave; the same value in every lane
 template <int kCtrl, int kRows>
@@ -88,16 +71,36 @@ __device__ __forceinline__ int wave_min(int v) {
   return v;
 }
 
-// a . b over d elements by one wave, in fp64; the same value in every lane.
+// a . b over d elements by one wave, in fp64; the same value in every lane. Sixteen bytes a lane and load, U of them
+// requested together: the rows come from afar, one load at a time took 12 us for 4096 elements.
 template <typename Act>
 __device__ __forceinline__ double dot64(const Act* __restrict__ a, const Act* __restrict__ b, int d) {
+  constexpr int U = 4, V = 16 / sizeof(Act);
   double s = 0;
-  for (int c = 8 * (threadIdx.x & 63); c < d; c += 8 * kWave) {
-    double u[8], v[8];
-    load8d(a + c, u);
-    load8d(b + c, v);
+  for (int c0 = V * (threadIdx.x & 63); c0 < d; c0 += U * V * kWave) {
+    uint4 u[U], v[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s = fma(u[i], v[i], s);
+    for (int i = 0; i < U; ++i) {
+      const int c = c0 + i * V * kWave;
+      u[i] = v[i] = make_uint4(0, 0, 0, 0);
+      if (c < d) {
+        u[i] = *reinterpret_cast<const uint4*>(a + c);
+        v[i] = *reinterpret_cast<const uint4*>(b + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const uint32_t p[4] = {u[i].x, u[i].y, u[i].z, u[i].w}, q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(Act) == 2) {
+          s = fma((double)__uint_as_float(p[j] << 16), (double)__uint_as_float(q[j] << 16), s);
+          s = fma((double)__uint_as_float(p[j] & 0xffff0000u), (double)__uint_as_float(q[j] & 0xffff0000u), s);
+        } else {
+          s = fma((double)__uint_as_float(p[j]), (double)__uint_as_float(q[j]), s);
+        }
+      }
+    }
   }
   return wave_sum(s);
 }
@@ -175,10 +178,12 @@ __device__ __forceinline__ void order(Real& v0, Real& e0, int& i0, Real& v1, Rea
   i1 = swap ? i : i1;
 }
 
-// One token's choice by one wave, in fp32 or fp64. Returns whether it is taken (and written); else the experts that it
-// hangs on are appended to the work.
+enum Choice { kTaken, kRefine, kInDouble };
+
+// One token's choice by one wave, in fp32 or fp64: taken (and written); or the experts whose logits it hangs on are
+// appended to the work; or (fp32) it hangs on the rounding of refined ones, or on values past the range.
 template <typename Real, int kSlots>
-__device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, int t, int32_t* ids, float* w, float units) {
+__device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s, int t, int32_t* ids, float* w, float units) {
   constexpr bool kDouble = sizeof(Real) == 8;
   constexpr Real kNone = -INFINITY;
   constexpr int kOpen = 1 << 16, kMark = 1 << 17;   // beside an expert's id: not refined; the choice hangs on its logit
@@ -191,6 +196,7 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
   int id[kSlots];                             // -1: no expert
   Real m = kNone;
   float dmax = 0.f;
+  bool far = false;
 #pragma unroll
   for (int j = 0; j < kSlots; ++j) {
     const int i = map.i0 + j * map.lanes;
@@ -201,6 +207,7 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
     if (map.group < a.groups && i < map.size) {
       const double l = logit[e];
       arg[j] = (Real)l;
+      far = far || l >= 0x1p120 || (l <= -0x1p120 && l > -INFINITY);
       id[j] = e;
       if (!((s.refined[t * 8 + (e >> 5)] >> (e & 31)) & 1u)) {
         id[j] = e | kOpen;
@@ -213,11 +220,15 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
       dmax = fmaxf(dmax, delta[j]);
     }
   }
+  if constexpr (!kDouble)
+    if (__any(far)) return kInDouble;
+  // A softmax's sum z of all exponentials is off by up to dmax of itself. It scales every score alike, so the order
+  // of the c is that of z c = exponential + z b: what it moves there, |b| dmax of the sum, is the error that counts.
+  const bool all = !a.sigmoid && a.select_bias;
   Real z = 1;
   if (!a.sigmoid) {
     m = wave_max(m);
-    // the sum of all exponentials matters next to a bias only: it scales every score alike
-    dmax = a.select_bias ? wave_max(dmax) : 0.f;
+    dmax = all ? wave_max(dmax) : 0.f;
     z = 0;
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
@@ -236,12 +247,15 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
       const Real b = a.select_bias ? (Real)a.select_bias[id[j] & 0xffff] : (Real)0;
       v = score + b;
       // the score's change with its logit: s (1 - s), or s; exp(x) - 1 <= 1.3 x up to 0.5
-      const float from = a.sigmoid ? delta[j] : delta[j] + dmax;
       const Real part = a.sigmoid ? score * (1 - score) : score;
-      err = from <= 0.5f ? part * (Real)(1.3f * from) : (Real)INFINITY;
+      err = part * (Real)(1.3f * delta[j]);
+      if (all) err += fabs(b) * (Real)(1.3f * dmax);
+      if (!(delta[j] <= 0.5f) || (all && !(dmax <= 0.5f))) err = INFINITY;
       if constexpr (!kDouble) {
-        // the exponential and its argument's rounding, the sum of exponentials, the division; then the sum with b
-        err += score * ((16 + fabsf(arg[j])) * kUnit) + (score + fabsf(b)) * kUnit;
+        // The exponential (one unit; OCML), its argument's rounding, 1 + it and the division, the sum with b; a
+        // softmax's sum of up to eight and six additions matters next to a bias, as above.
+        const float own = 2 + fabsf(arg[j]);
+        err += kUnit * (score * (a.sigmoid ? (1 - score) * own + 3 : own + 2) + fabsf(b) * (all ? 17 : 1));
         err = fmaxf(err, 0x1p-120f);           // scores lost below the fp32 range
       }
       if (!(v > kNone)) v = kNone;
@@ -251,9 +265,8 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
     eps[j] = err;
   }
 
-  // next to a bias a softmax hangs on every logit, through the sum
-  const bool all = !a.sigmoid && a.select_bias;
-  auto unsure = [&](int i) { return i >= 0 && ((i & kOpen) || (all && dmax > 0.f)); };
+  // what a refined logit leaves open: in fp32 the evaluation, in fp64 a softmax's sum next to a bias
+  auto unsure = [&](int i) { return i >= 0 && (!kDouble || (i & kOpen) || (all && dmax > 0.f)); };
   if (a.groups > 1) {
     Top2<Real> vc;
 #pragma unroll
@@ -380,17 +393,24 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
       above = fmax(above, hi);
     }
   }
-  bool hangs = my_id >= 0 && (my_id & kMark);
+  bool hangs = my_id >= 0 && (my_id & kMark), on_open = hangs && (my_id & kOpen);
 #pragma unroll
-  for (int j = 0; j < kSlots; ++j) hangs = hangs || (id[j] >= 0 && (id[j] & kMark));
+  for (int j = 0; j < kSlots; ++j) {
+    const bool mark = id[j] >= 0 && (id[j] & kMark);
+    hangs = hangs || mark;
+    on_open = on_open || (mark && (id[j] & kOpen));
+  }
   if (__any(hangs)) {
+    const bool some = __any(on_open);
+    if (!kDouble && !some) return kInDouble;
+    // the marked ones; if these are refined, every logit of the sum
     auto append = [&](int i) {
-      if (i >= 0 && (i & kOpen) && (all || (i & kMark))) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | (i & 0xff));
+      if (i >= 0 && (i & kOpen) && (!some || (i & kMark))) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | (i & 0xff));
     };
     append(my_id);
 #pragma unroll
     for (int j = 0; j < kSlots; ++j) append(id[j]);
-    return false;
+    return kRefine;
   }
 
   // weights, in fp64 from the logits of the chosen (lanes 0 .. 7)
@@ -411,7 +431,7 @@ __device__ __forceinline__ bool choose(const GateArgs& a, const TokenState& s, i
     ids[lane] = my_id;
     w[lane] = total > 0 ? (float)(sk / total * a.scale) : 0.f;
   }
-  return true;
+  return kTaken;
 }
 
 // The choice of the workgroup's tokens (kTok of them at most, n present) once their logits lie in LDS. All waves call
@@ -425,40 +445,35 @@ __device__ __forceinline__ void choose_all(const GateArgs& a, const TokenState& 
 #pragma unroll
   for (int i = 0; i < kMine; ++i)
     if (wave + kWaves * i < n) pending |= 1u << i;
-  bool first = *s.n_work == 0;   // logits that are no numbers in fp32 are refined before any choice
-  __syncthreads();               // every wave has read it before one adds to it
   for (;;) {
-    if (first) {
-#pragma unroll
-      for (int i = 0; i < kMine; ++i) {
-        const int t = wave + kWaves * i;
-        const long o = (long)(tok0 + t) * a.K;
-        if ((pending >> i & 1) && choose<float, kSlots>(a, s, t, a.topk_ids + o, a.topk_w + o, units)) pending &= ~(1u << i);
-      }
-      first = false;
-      __syncthreads();
-    }
+    // logits that are no numbers in fp32 are in the work before any choice
     const int work = *s.n_work;
-    if (work == 0) break;
-    for (int i = wave; i < work; i += kWaves) {
-      const int t = s.work[i] >> 8, e = s.work[i] & 255;
-      const double v = dot64(static_cast<const Act*>(a.x) + (long)(tok0 + t) * a.d,
-                             static_cast<const Act*>(a.router_w) + (long)e * a.d, a.d);
-      if (lane == 0) {
-        s.logit[t * s.stride + e] = a.router_bias ? v + a.router_bias[e] : v;
-        atomicOr(&s.refined[t * 8 + (e >> 5)], 1u << (e & 31));
+    if (work > 0) {
+      for (int i = wave; i < work; i += kWaves) {
+        const int t = s.work[i] >> 8, e = s.work[i] & 255;
+        const double v = dot64(static_cast<const Act*>(a.x) + (long)(tok0 + t) * a.d,
+                               static_cast<const Act*>(a.router_w) + (long)e * a.d, a.d);
+        if (lane == 0) {
+          s.logit[t * s.stride + e] = a.router_bias ? v + a.router_bias[e] : v;
+          atomicOr(&s.refined[t * 8 + (e >> 5)], 1u << (e & 31));
+        }
       }
+      __syncthreads();
+      if (threadIdx.x == 0) *s.n_work = 0;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) *s.n_work = 0;
-    __syncthreads();
-#pragma unroll
+    __syncthreads();   // every wave has read the number before one adds to it
+#pragma unroll 1
     for (int i = 0; i < kMine; ++i) {
+      if (!(pending >> i & 1)) continue;
       const int t = wave + kWaves * i;
-      const long o = (long)(tok0 + t) * a.K;
-      if ((pending >> i & 1) && choose<double, kSlots>(a, s, t, a.topk_ids + o, a.topk_w + o, units)) pending &= ~(1u << i);
+      int32_t* ids = a.topk_ids + (long)(tok0 + t) * a.K;
+      float* w = a.topk_w + (long)(tok0 + t) * a.K;
+      Choice c = choose<float, kSlots>(a, s, t, ids, w, units);
+      if (c == kInDouble) c = choose<double, kSlots>(a, s, t, ids, w, units);
+      if (c == kTaken) pending &= ~(1u << i);
     }
     __syncthreads();
+    if (*s.n_work == 0) break;   // a token that is not taken has added to it
   }
 }
 
@@ -663,23 +678,8 @@ struct ChoiceLds {
   int n_work;
 };
 
-template <typename Act, int kWaves, int TOK, int EP>
-__device__ __forceinline__ void choose_tokens(const GateArgs& a, const TokenState& s, int tok0, int n) {
-  // Slots of a lane: a group's experts over its lanes, of which there are more than 32 / groups. With up to 256 experts 8;
-  // 4 if the groups are a power of two, as they mostly are.
-  if constexpr (EP <= 32) {
-    choose_all<Act, kWaves, TOK, 1>(a, s, tok0, n, kSumUnits<Act>);
-  } else if constexpr (EP <= 64) {
-    choose_all<Act, kWaves, TOK, 2>(a, s, tok0, n, kSumUnits<Act>);
-  } else {
-    const ChoiceMap map(a, threadIdx.x & 63);
-    if (map.size <= 4 * map.lanes) choose_all<Act, kWaves, TOK, 4>(a, s, tok0, n, kSumUnits<Act>);
-    else choose_all<Act, kWaves, TOK, 8>(a, s, tok0, n, kSumUnits<Act>);
-  }
-}
-
 // Logits and choice of 16*TB tokens in one workgroup.
-template <typename Act, int NEB, int TB, int kWaves, int D>
+template <typename Act, int NEB, int TB, int kWaves, int D, int kSlots>
 __global__ __launch_bounds__(kWaves* kWave, 4) void route_gated_kernel(GateArgs a, int tpw) {
   using S = Tile<NEB, TB, kWaves, D>;
   constexpr int EP = S::EP, TOK = S::TOK, KS = S::KS;
@@ -720,33 +720,48 @@ __global__ __launch_bounds__(kWaves* kWave, 4) void route_gated_kernel(GateArgs 
     if (t < n && e < a.E) put_logit(a, s, t, e, v[i]);
   }
   __syncthreads();
-  choose_tokens<Act, kWaves, TOK, EP>(a, s, tok0, n);
+  choose_all<Act, kWaves, TOK, kSlots>(a, s, tok0, n, kSumUnits<Act>);
 }
 
-template <typename Act, int NEB>
-void launch_experts(const GateArgs& a, hipStream_t stream) {
+template <typename Act, int NEB, int TB, int kWaves, int kSlots>
+void launch_tile(const GateArgs& a, int tpw, hipStream_t stream) {
   constexpr int D = NEB == 1 ? 2 : 3;
+  hipLaunchKernelGGL((route_gated_kernel<Act, NEB, TB, kWaves, D, kSlots>), dim3((a.T + tpw - 1) / tpw), dim3(kWaves * kWave), 0,
+                     stream, a, tpw);
+}
+
+template <typename Act, int NEB, int kSlots>
+void launch_experts(const GateArgs& a, hipStream_t stream) {
   if constexpr (NEB <= 4) {
-    // as few tokens a workgroup as leave no CU without one, so that a small batch's reads of router_w are spread
+    // As few tokens a workgroup as leave no CU without one, so that a small batch's reads of router_w are spread. Few
+    // workgroups: the most waves each; many: two workgroups a CU, one of which loads while the other chooses.
     const int tpw = min(16, (a.T + 255) / 256);
-    const dim3 grid((a.T + tpw - 1) / tpw);
-    // few workgroups: the most waves each; many: two workgroups a CU, one of which loads while the other chooses
-    if (grid.x <= 256) hipLaunchKernelGGL((route_gated_kernel<Act, NEB, 1, 16, D>), grid, dim3(16 * kWave), 0, stream, a, tpw);
-    else hipLaunchKernelGGL((route_gated_kernel<Act, NEB, 1, 8, D>), grid, dim3(8 * kWave), 0, stream, a, tpw);
+    if ((a.T + tpw - 1) / tpw <= 256) launch_tile<Act, NEB, 1, 16, kSlots>(a, tpw, stream);
+    else launch_tile<Act, NEB, 1, 8, kSlots>(a, tpw, stream);
   } else if (a.T <= 16 * 256) {
-    hipLaunchKernelGGL((route_gated_kernel<Act, NEB, 1, 16, D>), dim3((a.T + 15) / 16), dim3(16 * kWave), 0, stream, a, 16);
+    launch_tile<Act, NEB, 1, 16, kSlots>(a, 16, stream);
   } else {
-    hipLaunchKernelGGL((route_gated_kernel<Act, NEB, 2, 16, D>), dim3((a.T + 31) / 32), dim3(16 * kWave), 0, stream, a, 32);
+    launch_tile<Act, NEB, 2, 16, kSlots>(a, 32, stream);
   }
+}
+
+// Slots of a lane: a group's experts over its lanes, of which there are more than 32 / groups; 8 at most, 4 if the groups
+// are a power of two, as they mostly are.
+template <typename Act, int NEB>
+void launch_slots(const GateArgs& a, hipStream_t stream) {
+  int lanes = kWave;
+  while (lanes * a.groups > kWave) lanes >>= 1;
+  if (a.E / a.groups <= 4 * lanes) launch_experts<Act, NEB, 4>(a, stream);
+  else launch_experts<Act, NEB, 8>(a, stream);
 }
 
 template <typename Act>
 void launch(const GateArgs& a, hipStream_t stream) {
-  if (a.E <= 16) launch_experts<Act, 1>(a, stream);
-  else if (a.E <= 32) launch_experts<Act, 2>(a, stream);
-  else if (a.E <= 64) launch_experts<Act, 4>(a, stream);
-  else if (a.E <= 128) launch_experts<Act, 8>(a, stream);
-  else launch_experts<Act, 16>(a, stream);
+  if (a.E <= 16) launch_experts<Act, 1, 1>(a, stream);
+  else if (a.E <= 32) launch_experts<Act, 2, 1>(a, stream);
+  else if (a.E <= 64) launch_experts<Act, 4, 2>(a, stream);
+  else if (a.E <= 128) launch_slots<Act, 8>(a, stream);
+  else launch_slots<Act, 16>(a, stream);
 }
 
 }  // namespace
