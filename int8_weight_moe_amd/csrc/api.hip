@@ -115,8 +115,13 @@ constexpr long kMxFewTilesRowsPerExpert = 32;
 constexpr long kMxFewTilesWideRowsPerExpert = 20;
 constexpr long kMxFewTilesChannels = 16384;
 
-// Rows an expert on average up to which a product of int8 rows streams its weights.
-constexpr long kI8StreamRowsPerExpert = 32;
+// Rows an expert on average up to which a product of int8 rows streams its weights,
+// and the same where tiles are fewer than one a CU. Measured, us, stream / tiled: gate/up, d
+// 4096, f 14336, E 16: 8 rows 312 / 330, 16 334 / 350, 32 434 / 348; down, d 24576, f 8192: 8 595 / 626, 16
+// 597 / 609. Beyond 8 rows the tiles are within 5% and do not read the weights of a crowded expert again (999 slots, E 40,
+// unevenly: 93 / 60). One expert, 64 rows, d 24576, f 8192 (64 tiles): 69 / 150.
+constexpr long kI8StreamRowsPerExpert = 8;
+constexpr long kI8FewTilesRowsPerExpert = 64;
 
 // routes: the call's K experts of a token are distinct ones of the E.
 moe_status check_shape(const moe_shape* s, bool routes = true, int max_experts = 64) {
@@ -420,12 +425,16 @@ moe_status check_i8_shape(const moe_shape* s, bool routes) {
 
 // One product of int8 rows and weights; `call` and `what` name it in the log and in an error.
 moe_status run_i8(const char* call, const char* what, const moe_shape* s, const moe::I8Args& m, hipStream_t stream) {
-  bool by_stream = s->ffn_path == MOE_PATH_STREAM || (s->ffn_path == MOE_PATH_AUTO && m.S <= kI8StreamRowsPerExpert * m.E);
+  bool by_stream = s->ffn_path == MOE_PATH_STREAM;
+  if (s->ffn_path == MOE_PATH_AUTO)
+    by_stream = m.S <= (moe::i8_few_tiles(m) ? kI8FewTilesRowsPerExpert : kI8StreamRowsPerExpert) * m.E;
   // rows past the tiled kernel's 32-bit offsets
   if (!moe::i8_tiled_offsets_fit(m.a_rows, m.Kd)) by_stream = true;
   if (log_on()) {
-    char how[128] = "tiled schedule";
-    if (by_stream) {
+    char how[128];
+    if (!by_stream) {
+      snprintf(how, sizeof(how), "tiled schedule, 128x%d tiles", moe::i8_tile_columns(m));
+    } else {
       const moe::I8StreamPlan p = moe::i8_stream_plan(m);
       snprintf(how, sizeof(how), "stream schedule, %d-channel items, %d-row passes, reduction in %d slices", p.channels,
                p.rows, p.slices);

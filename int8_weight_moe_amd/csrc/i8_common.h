@@ -34,11 +34,12 @@ __device__ __forceinline__ float4 i8_scale4(const void* s, bool bf16, long idx) 
 
 // Four consecutive channels of one row from their sums, as out's type: the
 // scaled sums (NMAT = 1), or silu(first) * second. A sum becomes fp32 (one
-// rounding past 2^24) and takes its two scales, the channel's first; SwiGLU with
-// the full-precision exponential and division, since out may be fp32.
-template <int NMAT>
-__device__ __forceinline__ void i8_store4(void* out, bool bf16, long o, const i32x4 (&acc)[NMAT],
-                                          const float4 (&ws)[NMAT], float as) {
+// rounding past 2^24) and takes its two scales, the channel's first. SwiGLU for an
+// fp32 out takes the full-precision exponential and division; for a bf16 one the
+// hardware's, whose errors are far below its rounding (the epilogue of a 128x256
+// tile of 4096 columns: 2030 -> 1950 us with its four-fragment steps).
+template <int NMAT, bool kOutBf16>
+__device__ __forceinline__ void i8_store4(void* out, long o, const i32x4 (&acc)[NMAT], const float4 (&ws)[NMAT], float as) {
   f32x4 v;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -47,9 +48,9 @@ __device__ __forceinline__ void i8_store4(void* out, bool bf16, long o, const i3
       return (float)acc[m][q] * s * as;
     };
     v[q] = scaled(0);
-    if constexpr (NMAT == 2) v[q] = v[q] / (1.0f + expf(-v[q])) * scaled(NMAT - 1);
+    if constexpr (NMAT == 2) v[q] = (kOutBf16 ? silu(v[q]) : v[q] / (1.0f + expf(-v[q]))) * scaled(NMAT - 1);
   }
-  if (bf16) {
+  if constexpr (kOutBf16) {
     bf16x4 b;
 #pragma unroll
     for (int q = 0; q < 4; ++q) b[q] = (__bf16)v[q];

@@ -13,6 +13,8 @@
 // Items are numbered over the experts that have rows. With few items the
 // reduction is cut into KS slices, streamed by the KS waves of a workgroup and
 // added through LDS (integers: exact in any order).
+// Bound by HBM: gate/up of one token (d 4096, f 14336, two experts) 39 us, 6.0
+// TB/s; down of 64 tokens (d 24576, f 8192, E 16) 506 us, 6.4 TB/s.
 #include "i8_common.h"
 #include "kernels.h"
 
@@ -23,7 +25,7 @@ namespace {
 constexpr int kStreamWaves = 4;
 constexpr int block_waves(int KS) { return KS > 1 ? KS : kStreamWaves; }
 
-template <int NMAT, int NG, int RB, int KS, int U>
+template <int NMAT, bool kOutBf16, int NG, int RB, int KS, int U>
 __global__ __launch_bounds__(block_waves(KS) * kWave) void i8_stream_kernel(I8Args a) {
   constexpr int IPW = block_waves(KS) / KS;   // items per workgroup
   __shared__ i32x4 red[KS > 1 ? KS - 1 : 1][NG][NMAT][kWave];
@@ -155,7 +157,7 @@ __global__ __launch_bounds__(block_waves(KS) * kWave) void i8_stream_kernel(I8Ar
         float4 ws[NMAT];
         ws[0] = i8_scale4(a.s0, a.scale_bf16, (long)e * N + ch);
         if constexpr (NMAT == 2) ws[1] = i8_scale4(a.s1, a.scale_bf16, (long)e * N + ch);
-        i8_store4<NMAT>(a.out, a.out_bf16, (long)(row0 + r) * N + ch, acc[rb][ng], ws, as);
+        i8_store4<NMAT, kOutBf16>(a.out, (long)(row0 + r) * N + ch, acc[rb][ng], ws, as);
       }
     }
   }
@@ -165,29 +167,42 @@ __global__ __launch_bounds__(block_waves(KS) * kWave) void i8_stream_kernel(I8Ar
 // the S at least).
 long stream_items(const I8Args& a, int NG) { return (long)min(a.E, a.S) * (a.N / (16 * NG)); }
 
-template <int NMAT, int NG, int RB, int KS, int U>
+template <int NMAT, bool kOutBf16, int NG, int RB, int KS, int U>
 hipError_t launch(const I8Args& a, hipStream_t stream) {
   const long items = stream_items(a, NG);
-  hipLaunchKernelGGL((i8_stream_kernel<NMAT, NG, RB, KS, U>),
+  hipLaunchKernelGGL((i8_stream_kernel<NMAT, kOutBf16, NG, RB, KS, U>),
                      dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves)),
                      dim3(block_waves(KS) * kWave), 0, stream, a);
   return hipGetLastError();
 }
 
+template <int NMAT, bool kOutBf16>
+hipError_t launch_rows(const I8Args& a, hipStream_t stream) {
+  switch (i8_stream_plan(a).rows) {
+    case 16: return launch<NMAT, kOutBf16, 1, 1, 4, 4>(a, stream);
+    case 32: return launch<NMAT, kOutBf16, 2, 2, 2, 4>(a, stream);
+    default: return launch<NMAT, kOutBf16, 2, 4, 4, 2>(a, stream);
+  }
+}
+
 }  // namespace
 
+// Rows a pass, channels of an item, slices. Measured, us, weights that no cache
+// holds (16r: 16 rows, 16 channels, 4 slices of 4 steps at a time; 32r: 32, 32, 2 of 4; 64r: 64, 32, 4 of 2):
+//   gate/up, d 4096, f 14336, E 16: 2 slots 39 / 43 / 51, 32 slots 255 / 261 / 292, 128 slots
+//     323 / 312 / 343; down, d 24576, f 8192, E 16, 128 slots 573 / 595 / 582;
+//   one expert: 4 rows, d 24576, f 8192 39 / 55 / 49; 16 rows, gate/up, d 8192, f 24576 78 / 88 / 90; 64 rows, d 24576, f 8192
+//     173 / 124 / 69 (128-row tiles: 150).
+// More rows a pass cost registers, hence waves; an expert with more rows than a pass streams its weights again.
 I8StreamPlan i8_stream_plan(const I8Args& a) {
-  I8StreamPlan p;
-  p.channels = 16;
-  p.rows = a.S <= 8L * a.E ? 16 : 32;
-  p.slices = 1;
-  return p;
+  const long few = (long)min(a.E, a.S) * a.N / 32 < 2048;   // fewer 32-channel items than two waves a SIMD
+  if (a.S <= (few ? 8L : 4L) * a.E) return {16, 16, 4};
+  return a.S <= 8L * a.E ? I8StreamPlan{32, 32, 2} : I8StreamPlan{32, 64, 4};
 }
 
 hipError_t launch_i8_stream(const I8Args& a, hipStream_t stream) {
-  const I8StreamPlan p = i8_stream_plan(a);
-  if (a.w1) return p.rows == 16 ? launch<2, 1, 1, 1, 2>(a, stream) : launch<2, 1, 2, 1, 2>(a, stream);
-  return p.rows == 16 ? launch<1, 1, 1, 1, 2>(a, stream) : launch<1, 1, 2, 1, 2>(a, stream);
+  if (a.w1) return a.out_bf16 ? launch_rows<2, true>(a, stream) : launch_rows<2, false>(a, stream);
+  return a.out_bf16 ? launch_rows<1, true>(a, stream) : launch_rows<1, false>(a, stream);
 }
 
 }  // namespace moe

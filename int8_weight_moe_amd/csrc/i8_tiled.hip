@@ -31,7 +31,7 @@ constexpr int ROWB = KB * kI8Step;  // bytes of a row per step
 constexpr int CPR = ROWB / 16;      // its 16-byte chunks
 constexpr int RPI = 1024 / ROWB;    // rows per 1 KiB load
 
-template <int NMAT, int GM, int kBM, int kBN, int kWpe>
+template <int NMAT, bool kOutBf16, int GM, int kBM, int kBN, int kWpe>
 __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(kWpe, kWpe))) void i8_tiled_kernel(
     I8Args a, int n_tiles) {
   constexpr int A_STAGE = kBM * ROWB;
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(k
 #pragma unroll
       for (int k = 0; k < KB; ++k) {
         if (k > 0 && 2 * st + k >= n) break;
-        constexpr int HB = 2;
+        constexpr int HB = MBV % 4 == 0 ? 4 : 2;   // row blocks whose fragments are read together (two: 3% slower)
 #pragma unroll
         for (int h = 0; h < MBV; h += HB) {
           uint4 xf[HB];
@@ -176,29 +176,51 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(k
       i32x4 v[NMAT];
       v[0] = acc[i][j];
       if constexpr (NMAT == 2) v[1] = acc[i][j + HALF];
-      i8_store4<NMAT>(a.out, a.out_bf16, (long)rr * N + ch_of[j] + 4 * lg, v, ws[j], as);
+      i8_store4<NMAT, kOutBf16>(a.out, (long)rr * N + ch_of[j] + 4 * lg, v, ws[j], as);
     }
   }
 }
 
-template <int NMAT, int kBM, int kBN, int kWpe>
+// Channel tiles of a row of tiles, and the most tiles that any segments make.
+int tile_columns(const I8Args& a, int channels) {
+  const int ch = a.w1 ? channels / 2 : channels;
+  return (a.N + ch - 1) / ch;
+}
+long tile_bound(const I8Args& a, int rows, int channels) {
+  return ((long)(a.S + rows - 1) / rows + a.E) * tile_columns(a, channels);
+}
+
+template <int NMAT, bool kOutBf16, int kBM, int kBN, int kWpe>
 hipError_t launch_tile(const I8Args& a, hipStream_t stream) {
-  constexpr int GM = 8;
-  constexpr int CH = kBN / NMAT;
-  const int n_tiles = (a.N + CH - 1) / CH;
-  const long tiles = ((long)(a.S + kBM - 1) / kBM + a.E) * n_tiles;
-  const long per_xcd = (tiles + kXcds - 1) / kXcds;
-  hipLaunchKernelGGL((i8_tiled_kernel<NMAT, GM, kBM, kBN, kWpe>), dim3((unsigned)(kXcds * per_xcd)),
-                     dim3(kWaves * kWave), 0, stream, a, n_tiles);
+  constexpr int GM = 8;   // row tiles of an expert that take a channel tile together (4: 2 to 5% slower, 12: within 1%)
+  const long per_xcd = (tile_bound(a, kBM, kBN) + kXcds - 1) / kXcds;
+  hipLaunchKernelGGL((i8_tiled_kernel<NMAT, kOutBf16, GM, kBM, kBN, kWpe>), dim3((unsigned)(kXcds * per_xcd)),
+                     dim3(kWaves * kWave), 0, stream, a, tile_columns(a, kBN));
   return hipGetLastError();
+}
+
+template <int NMAT, bool kOutBf16>
+hipError_t launch_columns(const I8Args& a, hipStream_t stream) {
+  return i8_tile_columns(a) == 128 ? launch_tile<NMAT, kOutBf16, 128, 128, 3>(a, stream)
+                                   : launch_tile<NMAT, kOutBf16, 128, 256, 2>(a, stream);
 }
 
 }  // namespace
 
 bool i8_tiled_offsets_fit(long rows, int cols) { return (uint64_t)rows * (uint64_t)cols < (1ull << 32); }
 
+bool i8_few_tiles(const I8Args& a) { return tile_bound(a, 128, 128) - (long)a.E * tile_columns(a, 128) < 256; }
+
+// Channels of a tile. Measured, us, 128 / 256: gate/up, d 4096, f 14336, E 16: 16 rows an expert 350 / 368, 32 348 / 378, 64
+// 354 / 357, 128 499 / 486, 1024 2149 / 2034; d 4160, f 1472, E 40, 25 rows 60 / 64; one expert, 64 rows, d 8192, f 24576 95 / 106;
+// down, d 24576, f 8192, E 16: 16 rows 690 / 609, 375 1419 / 1267, 2048 6998 / 5853; few tiles: d 14336, f 4096, 32 rows 180 / 199.
+int i8_tile_columns(const I8Args& a) {
+  return (a.w1 && a.S <= 64L * a.E) || tile_bound(a, 128, 256) < 512 ? 128 : 256;
+}
+
 hipError_t launch_i8_tiled(const I8Args& a, hipStream_t stream) {
-  return a.w1 ? launch_tile<2, 128, 256, 2>(a, stream) : launch_tile<1, 128, 256, 2>(a, stream);
+  if (a.w1) return a.out_bf16 ? launch_columns<2, true>(a, stream) : launch_columns<2, false>(a, stream);
+  return a.out_bf16 ? launch_columns<1, true>(a, stream) : launch_columns<1, false>(a, stream);
 }
 
 }  // namespace moe

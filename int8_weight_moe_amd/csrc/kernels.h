@@ -150,6 +150,9 @@ I8StreamPlan i8_stream_plan(const I8Args& a);
 hipError_t launch_i8_stream(const I8Args& a, hipStream_t stream);
 // Whether rows of `cols` codes lie within 32-bit byte offsets, as launch_i8_tiled needs the rows of a to.
 bool i8_tiled_offsets_fit(long rows, int cols);
+// Channels of a tile (both matrices'), and whether tiles are fewer than one a CU.
+int i8_tile_columns(const I8Args& a);
+bool i8_few_tiles(const I8Args& a);
 hipError_t launch_i8_tiled(const I8Args& a, hipStream_t stream);
 
 // Gated routing (route_gated.hip).

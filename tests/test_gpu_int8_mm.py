@@ -5,7 +5,9 @@ a plain result is off by at most 3 u of its magnitude (u = 2^-24). SwiGLU: p0 an
 p1 are each off by 3 u; |silu'| <= 1.1; the exponential is good to 2 units in the
 last place (4 u), 1 + it, the division and the two products add one rounding each
 (some of them halves): at most 12 u of the result besides the two terms of p0 and
-p1. A bf16 result adds half a step, 2^-8 of the value.
+p1. For a bf16 result the exponential is the hardware's: its argument, scaled, is off
+by 2^-23 |p0|, it and the reciprocal by some 2^-22 each, at most (8 + |p0|) * 2^-22 of
+the result in all; and half a step, 2^-8 of the value.
 """
 import sys
 
@@ -55,6 +57,8 @@ def _bound(a_q, a_s, ws, off, rows, swiglu, out):
         p1 = oint8.grouped_product(a_q, a_s, ws[1][0], n64[1], off, rows)
         bound = 1.1 * 3.01 * U * np.abs(p0 * p1) + 15 * U * np.abs(ref)
     if out == "bf16":
+        if swiglu:
+            bound = bound + (8 + np.abs(p0)) * 2.0 ** -22 * np.abs(ref)
         bound = bound + 2.0 ** -8 * (np.abs(ref) + bound)
     return ref, bound + 1e-37
 
