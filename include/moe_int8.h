@@ -46,13 +46,15 @@
  *     value other than "0"), the calls that take or produce a permutation
  *     also check it, on the host:
  *       moe_expert_ffn, moe_expert_gate_up, moe_expert_down,
- *       moe_expert_ffn_mxfp4, moe_grouped_mm_mxfp4: expert_offsets starts at
+ *       moe_expert_ffn_mxfp4, moe_grouped_mm_mxfp4,
+ *       moe_expert_ffn_int8, moe_grouped_mm_int8: expert_offsets starts at
  *         0, never decreases and ends at most at T*K; where sorted_slots is
  *         given, its rows below off[E] hold distinct slots in [0, T*K);
  *       moe_combine, moe_combine_post: every slot_to_row entry is -1 or in [0, T*K);
  *       these run BEFORE anything is launched, so bad caller arrays are
  *       reported instead of being read out of bounds by a kernel;
- *       moe_permute, moe_forward, moe_forward_noalloc, moe_block_forward: after the permutation
+ *       moe_permute, moe_forward, moe_forward_noalloc, moe_block_forward,
+ *       moe_forward_gated, moe_block_forward_gated: after the permutation
  *         is computed, also that every id is in [0, E) (all slots placed),
  *         that each expert's rows hold its own slots in ascending order and
  *         that slot_to_row inverts sorted_slots.
@@ -487,6 +489,33 @@ moe_status moe_grouped_mm_int8(const moe_shape* shape, const int8_t* a_q, const 
                                const int32_t* expert_offsets, const int32_t* sorted_slots, const int8_t* w_q,
                                const void* w_s, const int8_t* w2_q, const void* w2_s, void* out, hipStream_t stream);
 
+/* The expert FFN with int8 weights AND activations, on the permuted rows: x is
+ * quantized per token, gate/up with SwiGLU gives h (bf16), h is quantized per row
+ * (moe_quantize_rows, fp32 scales), down gives y_rows. As moe_expert_ffn with int8
+ * products (half as long at prefill) and the rounding of int8 activations.
+ *   weight_fmt MOE_W_INT8; act_dtype is x's type;
+ *   workspace >= moe_expert_ffn_int8_workspace_size bytes. */
+moe_status moe_expert_ffn_int8_workspace_size(const moe_shape* shape, size_t* bytes);
+moe_status moe_expert_ffn_int8(const moe_shape* shape, const void* x, const int32_t* expert_offsets,
+                               const int32_t* sorted_slots, const int8_t* w_gate, const int8_t* w_up,
+                               const int8_t* w_down, const void* s_gate, const void* s_up, const void* s_down,
+                               float* y_rows, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The layer with a gate and a choice of activations: moe_route_gated, moe_permute, the
+ * expert FFN (expert_act MOE_ACT_AS_IS: moe_expert_ffn, any weight encoding;
+ * MOE_ACT_INT8: moe_expert_ffn_int8, weight_fmt MOE_W_INT8), moe_combine. Bit-identical to these
+ * staged calls. shape->E up to 64, as for the other calls with weights. Slots
+ * whose id is -1 are not placed and add nothing.
+ *   workspace >= moe_gated_workspace_size bytes; the other arguments as in moe_forward.
+ * Under MOE_DEBUG ids of -1 pass the check of the permutation. */
+enum { MOE_ACT_AS_IS = 0, MOE_ACT_INT8 = 1 };
+moe_status moe_gated_workspace_size(const moe_shape* shape, int32_t expert_act, size_t* bytes);
+moe_status moe_forward_gated(const moe_shape* shape, const moe_gate* gate, int32_t expert_act, const void* x,
+                             const void* router_w, const float* router_bias, const void* w_gate, const void* w_up,
+                             const void* w_down, const void* s_gate, const void* s_up, const void* s_down, void* y,
+                             int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
 /* ---------------------------------------------------------------- norms around the layer
  * rms(v) = v / sqrt(mean(v^2) + eps) over the d elements of a token, in fp32 (a
  * sum of squares past the fp32 range is infinite, as from an infinite element:
@@ -539,6 +568,16 @@ moe_status moe_block_forward(const moe_shape* shape, const void* residual, const
                              const void* w_gate, const void* w_up, const void* w_down, const void* s_gate,
                              const void* s_up, const void* s_down, void* out, void* next, int32_t* topk_ids_out,
                              float* topk_w_out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The block with moe_forward_gated's steps in place of moe_forward's.
+ *   workspace >= moe_block_gated_workspace_size bytes; the other arguments as in moe_block_forward. */
+moe_status moe_block_gated_workspace_size(const moe_shape* shape, int32_t expert_act, size_t* bytes);
+moe_status moe_block_forward_gated(const moe_shape* shape, const moe_gate* gate, int32_t expert_act,
+                                   const void* residual, const void* pre_weight, float pre_eps, const void* x,
+                                   const moe_post* post, const void* router_w, const float* router_bias,
+                                   const void* w_gate, const void* w_up, const void* w_down, const void* s_gate,
+                                   const void* s_up, const void* s_down, void* out, void* next, int32_t* topk_ids_out,
+                                   float* topk_w_out, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

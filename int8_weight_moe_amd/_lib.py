@@ -24,6 +24,7 @@ MOE_W_INT8, MOE_W_BF16, MOE_W_FP8, MOE_W_MXFP4 = 0, 1, 2, 4
 MOE_MX_ROWS, MOE_MX_TILED = 0, 1
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_ACT_AS_IS, MOE_ACT_INT8 = 0, 1
 
 # every symbol the header declares
 EXPORTS = (
@@ -34,7 +35,8 @@ EXPORTS = (
     "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_pack_mxfp4", "moe_grouped_mm_mxfp4",
     "moe_expert_ffn_mxfp4_workspace_size", "moe_expert_ffn_mxfp4", "moe_norm_pre", "moe_norm_post",
     "moe_combine_post", "moe_block_workspace_size", "moe_block_forward",
-    "moe_route_gated", "moe_grouped_mm_int8",
+    "moe_route_gated", "moe_grouped_mm_int8", "moe_expert_ffn_int8_workspace_size", "moe_expert_ffn_int8",
+    "moe_gated_workspace_size", "moe_forward_gated", "moe_block_gated_workspace_size", "moe_block_forward_gated",
 )
 
 
@@ -98,6 +100,12 @@ _SIGS = {
     "moe_expert_ffn_mxfp4": (_I32, [_SHAPE] + [_P] * 11 + [_SIZE, _P]),
     "moe_route_gated": (_I32, [_SHAPE, _GATE] + [_P] * 6),
     "moe_grouped_mm_int8": (_I32, [_SHAPE] + [_P] * 10),
+    "moe_expert_ffn_int8_workspace_size": (_I32, [_SHAPE, ctypes.POINTER(_SIZE)]),
+    "moe_expert_ffn_int8": (_I32, [_SHAPE] + [_P] * 11 + [_SIZE, _P]),
+    "moe_gated_workspace_size": (_I32, [_SHAPE, _I32, ctypes.POINTER(_SIZE)]),
+    "moe_forward_gated": (_I32, [_SHAPE, _GATE, _I32] + [_P] * 13 + [_SIZE, _P]),
+    "moe_block_gated_workspace_size": (_I32, [_SHAPE, _I32, ctypes.POINTER(_SIZE)]),
+    "moe_block_forward_gated": (_I32, [_SHAPE, _GATE, _I32, _P, _P, _F32, _P, _POST] + [_P] * 13 + [_SIZE, _P]),
     "moe_norm_pre": (_I32, [_SHAPE, _P, _P, _F32, _P, _P]),
     "moe_norm_post": (_I32, [_SHAPE, _POST, _P, _P, _P, _P, _P]),
     "moe_combine_post": (_I32, [_SHAPE, _POST, _P, _P, _P, _P, _P, _P, _P]),

@@ -79,7 +79,7 @@ moe_status debug_rows(const moe_shape* s, const int32_t* s2r, hipStream_t stream
 
 // The permutation the library produced from the expert ids.
 moe_status debug_permutation(const moe_shape* s, const int32_t* ids, const int32_t* offsets, const int32_t* sorted,
-                             const int32_t* s2r, hipStream_t stream) {
+                             const int32_t* s2r, hipStream_t stream, bool gaps = false) {
   const long S = (long)s->T * s->K;
   std::vector<int32_t> i, off, srt, rows;
   moe_status st;
@@ -87,7 +87,7 @@ moe_status debug_permutation(const moe_shape* s, const int32_t* ids, const int32
   if ((st = fetch_ints(offsets, s->E + 1, off, stream)) != MOE_OK) return st;
   if ((st = fetch_ints(sorted, S, srt, stream)) != MOE_OK) return st;
   if ((st = fetch_ints(s2r, S, rows, stream)) != MOE_OK) return st;
-  return debug_verdict(moe_debug::check_permutation(i.data(), off.data(), srt.data(), rows.data(), s->E, S),
+  return debug_verdict(moe_debug::check_permutation(i.data(), off.data(), srt.data(), rows.data(), s->E, S, gaps),
                        "permutation");
 }
 
@@ -447,6 +447,79 @@ moe_status run_i8(const char* call, const char* what, const moe_shape* s, const 
   return MOE_OK;
 }
 
+// Workspace of moe_expert_ffn_int8: x in int8, h in int8, h (not in the layer, whose workspace has it).
+struct I8FfnLayout {
+  size_t xq, xs, hq, hs, h, total;
+};
+
+I8FfnLayout i8_ffn_layout(const moe_shape* s, bool with_h) {
+  const size_t T = (size_t)s->T, S = T * s->K, d = (size_t)s->d, f = (size_t)s->f;
+  I8FfnLayout L;
+  size_t o = 0;
+  L.xq = o; o += round_up(T * d);
+  L.xs = o; o += round_up(T * 4);
+  L.hq = o; o += round_up(S * f);
+  L.hs = o; o += round_up(S * 4);
+  L.h = o;  o += with_h ? round_up(S * f * 2) : 0;
+  L.total = o;
+  return L;
+}
+
+// The expert FFN with int8 activations (arguments checked by the caller); h null: in the workspace.
+moe_status run_i8_ffn(const char* call, const moe_shape* s, const void* x, const int32_t* offsets,
+                      const int32_t* sorted_slots, const void* w_gate, const void* w_up, const void* w_down,
+                      const void* s_gate, const void* s_up, const void* s_down, float* y_rows, void* h,
+                      void* workspace, hipStream_t stream) {
+  const I8FfnLayout L = i8_ffn_layout(s, !h);
+  char* ws = static_cast<char*>(workspace);
+  if (!h) h = ws + L.h;
+  const long S = (long)s->T * s->K;
+  int8_t* q = reinterpret_cast<int8_t*>(ws + L.xq);
+  float* qs = reinterpret_cast<float*>(ws + L.xs);
+  hipError_t e = moe::launch_quantize_rows(s->T, s->d, s->act_dtype == MOE_BF16, x, false, q, qs, false, false, stream);
+  if (e != hipSuccess) return hip_fail(e, "quantize launch");
+  moe::I8Args m;
+  m.a = q;
+  m.a_s = qs;
+  m.offsets = offsets;
+  m.sorted_slots = sorted_slots;
+  m.topk = s->K;
+  m.a_rows = s->T;
+  m.w0 = static_cast<const int8_t*>(w_gate);
+  m.w1 = static_cast<const int8_t*>(w_up);
+  m.s0 = s_gate;
+  m.s1 = s_up;
+  m.scale_bf16 = s->scale_dtype == MOE_BF16;
+  m.out = h;
+  m.out_bf16 = true;
+  m.E = s->E;
+  m.N = s->f;
+  m.Kd = s->d;
+  m.S = (int)S;
+  moe_status st = run_i8(call, "gate/up", s, m, stream);
+  if (st != MOE_OK) return st;
+
+  // rows past off[E] hold whatever was there: their codes are never read
+  q = reinterpret_cast<int8_t*>(ws + L.hq);
+  qs = reinterpret_cast<float*>(ws + L.hs);
+  e = moe::launch_quantize_rows(S, s->f, true, h, false, q, qs, false, false, stream);
+  if (e != hipSuccess) return hip_fail(e, "quantize launch");
+  m.a = q;
+  m.a_s = qs;
+  m.sorted_slots = nullptr;
+  m.topk = 1;
+  m.a_rows = S;
+  m.w0 = static_cast<const int8_t*>(w_down);
+  m.w1 = nullptr;
+  m.s0 = s_down;
+  m.s1 = nullptr;
+  m.out = y_rows;
+  m.out_bf16 = false;
+  m.N = s->d;
+  m.Kd = s->f;
+  return run_i8(call, "down", s, m, stream);
+}
+
 // What a gate may be for this shape; select_bias is checked where it is read.
 moe_status check_gate(const moe_shape* s, const moe_gate* g) {
   if (!g) return fail(MOE_ERR_NULL, "gate is NULL");
@@ -633,16 +706,33 @@ moe_status scratch_on_current_device(void** out) {
   return MOE_OK;
 }
 
+// moe_forward_gated's workspace: moe_forward's, then with int8 activations moe_expert_ffn_int8's but h.
+size_t gated_ws_bytes(const moe_shape* s, int32_t expert_act) {
+  const size_t fwd = round_up(forward_layout(s).total);
+  return expert_act == MOE_ACT_INT8 ? fwd + i8_ffn_layout(s, false).total : fwd;
+}
+
+moe_status check_expert_act(const moe_shape* s, int32_t expert_act) {
+  if (expert_act == MOE_ACT_AS_IS) return MOE_OK;
+  if (expert_act != MOE_ACT_INT8) return fail(MOE_ERR_DTYPE, "expert_act=%d", expert_act);
+  if (s->weight_fmt != MOE_W_INT8) return fail(MOE_ERR_DTYPE, "weight_fmt=%d: int8 activations take int8 weights", s->weight_fmt);
+  return MOE_OK;
+}
+
 // post: null, or the norm and residual sum that take the combine's place (y is then unused).
+// gate, expert_act: null and as they are, or moe_forward_gated's.
 moe_status forward_impl(const char* call, const moe_shape* s, const void* x, const void* router_w,
                        const float* router_bias, const void* w_gate, const void* w_up, const void* w_down,
                        const void* s_gate, const void* s_up, const void* s_down, void* y, int32_t* topk_ids_out,
                        float* topk_w_out, void* workspace, size_t workspace_bytes, hipStream_t stream,
-                       moe::NormArgs* post = nullptr) {
+                       moe::NormArgs* post = nullptr, const moe_gate* gate = nullptr,
+                       int32_t expert_act = MOE_ACT_AS_IS) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
   st = check_ffn(s, kBothPasses);
   if (st != MOE_OK) return st;
+  if (gate && (st = check_gate(s, gate)) != MOE_OK) return st;
+  if ((st = check_expert_act(s, expert_act)) != MOE_OK) return st;
   if (s->T == 0) return MOE_OK;   // nothing is read or written
   REQUIRE_PTR(x);
   REQUIRE_PTR(router_w);
@@ -658,8 +748,9 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
   if (topk_ids_out && !aligned16(topk_ids_out)) return fail(MOE_ERR_ALIGN, "topk_ids_out is not 16-byte aligned");
   if (topk_w_out && !aligned16(topk_w_out)) return fail(MOE_ERR_ALIGN, "topk_w_out is not 16-byte aligned");
   const WsLayout L = forward_layout(s);
-  if (workspace_bytes < L.total)
-    return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, L.total);
+  const size_t need = expert_act == MOE_ACT_INT8 ? gated_ws_bytes(s, expert_act) : L.total;
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
 
   char* ws = static_cast<char*>(workspace);
   int32_t* ids = topk_ids_out ? topk_ids_out : reinterpret_cast<int32_t*>(ws + L.ids);
@@ -670,8 +761,9 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
   __bf16* h = reinterpret_cast<__bf16*>(ws + L.h);
   float* y_rows = reinterpret_cast<float*>(ws + L.y_rows);
 
-  hipError_t e = moe::launch_router(x, router_w, router_bias, s->T, s->d, s->E, s->K, s->act_dtype == MOE_BF16,
-                                    ids, wts, stream);
+  hipError_t e = gate ? moe::launch_route_gated(gate_args(s, gate, x, router_w, router_bias, ids, wts), stream)
+                      : moe::launch_router(x, router_w, router_bias, s->T, s->d, s->E, s->K,
+                                           s->act_dtype == MOE_BF16, ids, wts, stream);
   if (e != hipSuccess) return hip_fail(e, "router launch");
   moe::FfnArgs a = ffn_args(s, x, offsets, sorted, w_gate, w_up, w_down, s_gate, s_up, s_down, y_rows, h);
   if (L.part_bytes) a.part = reinterpret_cast<float*>(ws + L.part);
@@ -679,7 +771,13 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
     a.claims_gate_up = reinterpret_cast<unsigned long long*>(ws + L.claims);
     a.claims_down = reinterpret_cast<unsigned long long*>(ws + L.claims + moe::kTileClaimBytes);
   }
-  if (use_stream(s) && s->weight_fmt != MOE_W_MXFP4 && moe::stream_gate_up_takes_ids((long)s->T * s->K, s->E)) {
+  if (expert_act == MOE_ACT_INT8) {
+    e = moe::launch_permute(ids, s->T * s->K, s->E, offsets, sorted, s2r, stream);
+    if (e != hipSuccess) return hip_fail(e, "permute launch");
+    if (debug_on() && (st = debug_permutation(s, ids, offsets, sorted, s2r, stream, gate != nullptr)) != MOE_OK) return st;
+    st = run_i8_ffn(call, s, x, offsets, sorted, w_gate, w_up, w_down, s_gate, s_up, s_down, y_rows,
+                    h, ws + round_up(L.total), stream);
+  } else if (use_stream(s) && s->weight_fmt != MOE_W_MXFP4 && moe::stream_gate_up_takes_ids((long)s->T * s->K, s->E)) {
     // at most 256 slots: the gate/up pass derives the permutation from the ids
     // and writes it for the down pass and the combine (one launch fewer)
     a.ids = ids;
@@ -688,18 +786,18 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
     a.perm_s2r = s2r;
     st = run_gate_up(call, s, a, stream);
     a.ids = nullptr;
-    if (st == MOE_OK && debug_on()) st = debug_permutation(s, ids, offsets, sorted, s2r, stream);
+    if (st == MOE_OK && debug_on()) st = debug_permutation(s, ids, offsets, sorted, s2r, stream, gate != nullptr);
+    if (st == MOE_OK) st = run_down(call, s, a, stream);
   } else {
     e = moe::launch_permute(ids, s->T * s->K, s->E, offsets, sorted, s2r, stream);
     if (e != hipSuccess) return hip_fail(e, "permute launch");
     if (debug_on()) {
-      st = debug_permutation(s, ids, offsets, sorted, s2r, stream);
+      st = debug_permutation(s, ids, offsets, sorted, s2r, stream, gate != nullptr);
       if (st != MOE_OK) return st;
     }
     st = run_gate_up(call, s, a, stream);
+    if (st == MOE_OK) st = run_down(call, s, a, stream);
   }
-  if (st != MOE_OK) return st;
-  st = run_down(call, s, a, stream);
   if (st != MOE_OK) return st;
   if (post) {
     post->y_rows = y_rows;
@@ -712,6 +810,59 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
   e = moe::launch_combine(y_rows, s2r, wts, s->T, s->d, s->K, s->act_dtype == MOE_BF16, y, stream);
   if (e != hipSuccess) return hip_fail(e, "combine launch");
   return MOE_OK;
+}
+
+// gate null: moe_block_forward.
+moe_status block_impl(const char* call, const moe_shape* s, const moe_gate* gate, int32_t expert_act,
+                      const void* residual, const void* pre_weight, float pre_eps, const void* x, const moe_post* post,
+                      const void* router_w, const float* router_bias, const void* w_gate, const void* w_up,
+                      const void* w_down, const void* s_gate, const void* s_up, const void* s_down, void* out,
+                      void* next, int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes,
+                      hipStream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (gate && (st = check_gate(s, gate)) != MOE_OK) return st;
+  if ((st = check_expert_act(s, expert_act)) != MOE_OK) return st;
+  if ((st = check_ffn(s, kBothPasses)) != MOE_OK) return st;
+  if ((st = check_post(s, post, residual, out, next)) != MOE_OK) return st;
+  if (pre_weight && (st = check_eps("pre_eps", pre_eps)) != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  if (!x == !pre_weight)
+    return fail(x ? MOE_ERR_UNSUPPORTED : MOE_ERR_NULL, "exactly one of x and pre_weight is given");
+  if (!aligned16(pre_weight)) return fail(MOE_ERR_ALIGN, "pre_weight is not 16-byte aligned");
+  REQUIRE_PTR(workspace);
+  const size_t fwd = round_up(gated_ws_bytes(s, expert_act)), need = fwd + block_x_bytes(s);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
+  // everything forward_impl checks, before the first launch
+  REQUIRE_PTR(router_w);
+  REQUIRE_PTR(w_gate);
+  REQUIRE_PTR(w_up);
+  REQUIRE_PTR(w_down);
+  REQUIRE_SCALE(s, s_gate);
+  REQUIRE_SCALE(s, s_up);
+  REQUIRE_SCALE(s, s_down);
+  if (!aligned16(router_bias)) return fail(MOE_ERR_ALIGN, "router_bias is not 16-byte aligned");
+  if (!aligned16(topk_ids_out)) return fail(MOE_ERR_ALIGN, "topk_ids_out is not 16-byte aligned");
+  if (!aligned16(topk_w_out)) return fail(MOE_ERR_ALIGN, "topk_w_out is not 16-byte aligned");
+  if (!aligned16(x)) return fail(MOE_ERR_ALIGN, "x is not 16-byte aligned");
+  if ((st = check_post_reads(s, post, nullptr, out, next)) != MOE_OK) return st;
+  moe::NormArgs pa = post_args(s, post, residual, out, next);
+  if (pre_weight) {
+    moe::NormArgs a = {};
+    a.act_bf16 = s->act_dtype == MOE_BF16;
+    a.x = residual;
+    a.weight = pre_weight;
+    a.out = static_cast<char*>(workspace) + fwd;
+    a.eps = pre_eps;
+    a.T = s->T;
+    a.d = s->d;
+    const hipError_t e = moe::launch_block_norm(a, stream);
+    if (e != hipSuccess) return hip_fail(e, "norm launch");
+    x = a.out;
+  }
+  return forward_impl(call, s, x, router_w, router_bias, w_gate, w_up, w_down, s_gate, s_up, s_down, nullptr,
+                      topk_ids_out, topk_w_out, workspace, fwd, stream, &pa, gate, expert_act);
 }
 
 }  // namespace
@@ -1258,6 +1409,59 @@ moe_status moe_grouped_mm_int8(const moe_shape* s, const int8_t* a_q, const floa
   return run_i8("moe_grouped_mm_int8", "product", s, m, stream);
 }
 
+moe_status moe_expert_ffn_int8_workspace_size(const moe_shape* shape, size_t* bytes) {
+  const moe_status st = check_i8_shape(shape, true);
+  if (st != MOE_OK) return st;
+  if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+  *bytes = i8_ffn_layout(shape, true).total;
+  return MOE_OK;
+}
+
+moe_status moe_expert_ffn_int8(const moe_shape* s, const void* x, const int32_t* expert_offsets,
+                               const int32_t* sorted_slots, const int8_t* w_gate, const int8_t* w_up,
+                               const int8_t* w_down, const void* s_gate, const void* s_up, const void* s_down,
+                               float* y_rows, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  moe_status st = check_i8_shape(s, true);
+  if (st != MOE_OK) return st;
+  if (s->T == 0) return MOE_OK;   // nothing is read or written
+  REQUIRE_PTR(x);
+  REQUIRE_PTR(expert_offsets);
+  REQUIRE_PTR(sorted_slots);
+  REQUIRE_PTR(w_gate);
+  REQUIRE_PTR(w_up);
+  REQUIRE_PTR(w_down);
+  REQUIRE_PTR(s_gate);
+  REQUIRE_PTR(s_up);
+  REQUIRE_PTR(s_down);
+  REQUIRE_PTR(y_rows);
+  REQUIRE_PTR(workspace);
+  const size_t need = i8_ffn_layout(s, true).total;
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
+  if (debug_on() && (st = debug_inputs(s, expert_offsets, sorted_slots, stream)) != MOE_OK) return st;
+  return run_i8_ffn("moe_expert_ffn_int8", s, x, expert_offsets, sorted_slots, w_gate, w_up, w_down, s_gate, s_up, s_down,
+                    y_rows, nullptr, workspace, stream);
+}
+
+moe_status moe_gated_workspace_size(const moe_shape* shape, int32_t expert_act, size_t* bytes) {
+  moe_status st = check_shape(shape);
+  if (st != MOE_OK) return st;
+  if ((st = check_expert_act(shape, expert_act)) != MOE_OK) return st;
+  if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+  *bytes = gated_ws_bytes(shape, expert_act);
+  return MOE_OK;
+}
+
+moe_status moe_forward_gated(const moe_shape* s, const moe_gate* gate, int32_t expert_act, const void* x,
+                             const void* router_w, const float* router_bias, const void* w_gate, const void* w_up,
+                             const void* w_down, const void* s_gate, const void* s_up, const void* s_down, void* y,
+                             int32_t* topk_ids_out, float* topk_w_out, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+  if (!gate) return fail(MOE_ERR_NULL, "gate is NULL");
+  return forward_impl("moe_forward_gated", s, x, router_w, router_bias, w_gate, w_up, w_down, s_gate, s_up, s_down, y,
+                      topk_ids_out, topk_w_out, workspace, workspace_bytes, stream, nullptr, gate, expert_act);
+}
+
 moe_status moe_norm_pre(const moe_shape* s, const void* x, const void* weight, float eps, void* n, hipStream_t stream) {
   moe_status st = check_shape(s);
   if (st != MOE_OK) return st;
@@ -1330,48 +1534,30 @@ moe_status moe_block_forward(const moe_shape* s, const void* residual, const voi
                              const void* w_gate, const void* w_up, const void* w_down, const void* s_gate,
                              const void* s_up, const void* s_down, void* out, void* next, int32_t* topk_ids_out,
                              float* topk_w_out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  moe_status st = check_shape(s);
+  return block_impl("moe_block_forward", s, nullptr, MOE_ACT_AS_IS, residual, pre_weight, pre_eps, x, post, router_w,
+                    router_bias, w_gate, w_up, w_down, s_gate, s_up, s_down, out, next, topk_ids_out, topk_w_out,
+                    workspace, workspace_bytes, stream);
+}
+
+moe_status moe_block_gated_workspace_size(const moe_shape* shape, int32_t expert_act, size_t* bytes) {
+  moe_status st = check_shape(shape);
   if (st != MOE_OK) return st;
-  if ((st = check_ffn(s, kBothPasses)) != MOE_OK) return st;
-  if ((st = check_post(s, post, residual, out, next)) != MOE_OK) return st;
-  if (pre_weight && (st = check_eps("pre_eps", pre_eps)) != MOE_OK) return st;
-  if (s->T == 0) return MOE_OK;   // nothing is read or written
-  if (!x == !pre_weight)
-    return fail(x ? MOE_ERR_UNSUPPORTED : MOE_ERR_NULL, "exactly one of x and pre_weight is given");
-  if (!aligned16(pre_weight)) return fail(MOE_ERR_ALIGN, "pre_weight is not 16-byte aligned");
-  REQUIRE_PTR(workspace);
-  const size_t fwd = round_up(forward_layout(s).total), need = fwd + block_x_bytes(s);
-  if (workspace_bytes < need)
-    return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
-  // everything forward_impl checks, before the first launch
-  REQUIRE_PTR(router_w);
-  REQUIRE_PTR(w_gate);
-  REQUIRE_PTR(w_up);
-  REQUIRE_PTR(w_down);
-  REQUIRE_SCALE(s, s_gate);
-  REQUIRE_SCALE(s, s_up);
-  REQUIRE_SCALE(s, s_down);
-  if (!aligned16(router_bias)) return fail(MOE_ERR_ALIGN, "router_bias is not 16-byte aligned");
-  if (!aligned16(topk_ids_out)) return fail(MOE_ERR_ALIGN, "topk_ids_out is not 16-byte aligned");
-  if (!aligned16(topk_w_out)) return fail(MOE_ERR_ALIGN, "topk_w_out is not 16-byte aligned");
-  if (!aligned16(x)) return fail(MOE_ERR_ALIGN, "x is not 16-byte aligned");
-  if ((st = check_post_reads(s, post, nullptr, out, next)) != MOE_OK) return st;
-  moe::NormArgs pa = post_args(s, post, residual, out, next);
-  if (pre_weight) {
-    moe::NormArgs a = {};
-    a.act_bf16 = s->act_dtype == MOE_BF16;
-    a.x = residual;
-    a.weight = pre_weight;
-    a.out = static_cast<char*>(workspace) + fwd;
-    a.eps = pre_eps;
-    a.T = s->T;
-    a.d = s->d;
-    const hipError_t e = moe::launch_block_norm(a, stream);
-    if (e != hipSuccess) return hip_fail(e, "norm launch");
-    x = a.out;
-  }
-  return forward_impl("moe_block_forward", s, x, router_w, router_bias, w_gate, w_up, w_down, s_gate, s_up, s_down,
-                      nullptr, topk_ids_out, topk_w_out, workspace, fwd, stream, &pa);
+  if ((st = check_expert_act(shape, expert_act)) != MOE_OK) return st;
+  if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+  *bytes = round_up(gated_ws_bytes(shape, expert_act)) + block_x_bytes(shape);
+  return MOE_OK;
+}
+
+moe_status moe_block_forward_gated(const moe_shape* s, const moe_gate* gate, int32_t expert_act, const void* residual,
+                                   const void* pre_weight, float pre_eps, const void* x, const moe_post* post,
+                                   const void* router_w, const float* router_bias, const void* w_gate,
+                                   const void* w_up, const void* w_down, const void* s_gate, const void* s_up,
+                                   const void* s_down, void* out, void* next, int32_t* topk_ids_out, float* topk_w_out,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!gate) return fail(MOE_ERR_NULL, "gate is NULL");
+  return block_impl("moe_block_forward_gated", s, gate, expert_act, residual, pre_weight, pre_eps, x, post, router_w,
+                    router_bias, w_gate, w_up, w_down, s_gate, s_up, s_down, out, next, topk_ids_out, topk_w_out,
+                    workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -59,12 +59,15 @@ inline std::string check_rows(const int32_t* s2r, long S) {
 // A permutation of the expert ids `ids` [S] as the library produces it: the
 // checks above, every slot placed, each sorted row's slot routed to its
 // segment's expert in ascending slot order, and slot_to_row the inverse of
-// sorted_slots.
+// sorted_slots. gaps: ids of -1 are slots that are not placed (their row is -1).
 inline std::string check_permutation(const int32_t* ids, const int32_t* off, const int32_t* sorted,
-                                     const int32_t* s2r, int E, long S) {
-  long outside = 0, first = -1;
+                                     const int32_t* s2r, int E, long S, bool gaps = false) {
+  long outside = 0, first = -1, placed = S;
   for (long s = 0; s < S; ++s)
-    if (ids[s] < 0 || ids[s] >= E) {
+    if (gaps && ids[s] == -1) {
+      --placed;
+      if (s2r[s] != -1) return msg("slot_to_row[%ld] = %ld, but the slot has no expert", s, s2r[s]);
+    } else if (ids[s] < 0 || ids[s] >= E) {
       if (first < 0) first = s;
       ++outside;
     }
@@ -72,8 +75,8 @@ inline std::string check_permutation(const int32_t* ids, const int32_t* off, con
     return msg("%ld slots have an expert id outside [0, %ld) (first: slot %ld, id %ld)", outside, E, first,
                ids[first]);
   std::string m = check_offsets(off, E, S);
-  if (m.empty() && off[E] != S) m = msg("expert_offsets[E] = %ld, expected all %ld slots", off[E], S);
-  if (m.empty()) m = check_sorted(sorted, S, S);
+  if (m.empty() && off[E] != placed) m = msg("expert_offsets[E] = %ld, expected all %ld slots", off[E], placed);
+  if (m.empty()) m = check_sorted(sorted, placed, S);
   if (m.empty()) m = check_rows(s2r, S);
   if (!m.empty()) return m;
   for (int e = 0; e < E; ++e)
@@ -85,7 +88,7 @@ inline std::string check_permutation(const int32_t* ids, const int32_t* off, con
         return msg("sorted rows %ld and %ld of expert %ld hold slots %ld out of ascending order", r - 1, r, e,
                    sorted[r]);
     }
-  for (long r = 0; r < S; ++r)
+  for (long r = 0; r < placed; ++r)
     if (s2r[sorted[r]] != r) return msg("slot_to_row[%ld] = %ld, but the slot is held by sorted row %ld",
                                         sorted[r], s2r[sorted[r]], r);
   return "";

@@ -209,7 +209,9 @@ hipError_t launch_columns(const I8Args& a, hipStream_t stream) {
 
 bool i8_tiled_offsets_fit(long rows, int cols) { return (uint64_t)rows * (uint64_t)cols < (1ull << 32); }
 
-bool i8_few_tiles(const I8Args& a) { return tile_bound(a, 128, 128) - (long)a.E * tile_columns(a, 128) < 256; }
+bool i8_few_tiles(const I8Args& a) {
+  return (long)max(min(a.E, a.S), (a.S + 127) / 128) * tile_columns(a, 128) < 256;
+}
 
 // Channels of a tile. Measured, us, 128 / 256: gate/up, d 4096, f 14336, E 16: 16 rows an expert 350 / 368, 32 348 / 378, 64
 // 354 / 357, 128 499 / 486, 1024 2149 / 2034; d 4160, f 1472, E 40, 25 rows 60 / 64; one expert, 64 rows, d 8192, f 24576 95 / 106;

@@ -14,7 +14,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import (MOE_BF16, MOE_F32, MOE_GROUP_MAX, MOE_GROUP_TOP2, MOE_MX_ROWS, MOE_MX_TILED,  # noqa: F401
+from ._lib import (MOE_ACT_AS_IS, MOE_ACT_INT8, MOE_BF16, MOE_F32, MOE_GROUP_MAX, MOE_GROUP_TOP2, MOE_MX_ROWS, MOE_MX_TILED,  # noqa: F401
                    MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_TILED, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MOE_W_BF16,
                    MOE_W_FP8, MOE_W_INT8, MOE_W_MXFP4, MoeError, MoeGate, MoePost, MoeShape)
 
@@ -278,24 +278,56 @@ def moe_combine(y_rows: torch.Tensor, slot_to_row: torch.Tensor, topk_w: torch.T
     return y
 
 
-class MoeLayer:
-    """A resident MoE layer: router weights, int8 experts and a reusable workspace."""
+@dataclasses.dataclass
+class Gate:
+    """How a router's scores become the choice of experts and their weights (moe_route_gated).
 
-    def __init__(self, router_w: torch.Tensor, bias: Optional[torch.Tensor], experts: Int8Experts, K: int):
+    score MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID; select_bias [E] fp32 is added to
+    the scores for the choice only (-inf takes an expert out of service); groups of
+    E / groups consecutive experts, of which the group_topk of the largest value stay
+    (group_by MOE_GROUP_MAX: the largest choice value of the group, MOE_GROUP_TOP2:
+    the sum of its two largest); renorm: the weights are divided by their sum; scale
+    multiplies them.
+    """
+    score: int = MOE_SCORE_SOFTMAX
+    select_bias: Optional[torch.Tensor] = None
+    groups: int = 1
+    group_topk: int = 1
+    group_by: int = MOE_GROUP_MAX
+    renorm: bool = True
+    scale: float = 1.0
+
+    def struct(self, E: int) -> MoeGate:
+        _check_sizes(self.groups, self.group_topk)
+        return MoeGate(_arg("select_bias", self.select_bias, torch.float32, (E,)), self.score, self.groups,
+                       self.group_topk, self.group_by, 1 if self.renorm else 0, self.scale)
+
+
+class MoeLayer:
+    """A resident MoE layer: router weights, int8 experts and a reusable workspace. With a gate the tokens are
+    routed by it, and with act_int8 the experts' products take int8 activations (moe_forward_gated)."""
+
+    def __init__(self, router_w: torch.Tensor, bias: Optional[torch.Tensor], experts: Int8Experts, K: int,
+                 gate: Optional[Gate] = None, act_int8: bool = False):
         self.router_w = router_w
         self.bias = bias
         self.experts = experts
         self.K = K
+        self.gate = Gate() if gate is None and act_int8 else gate
+        self.act_int8 = act_int8
         self._ws = None
 
     def workspace(self, shape: MoeShape) -> torch.Tensor:
-        need = max(workspace_size(shape), 256)
+        need = max(workspace_size(shape) if self.gate is None else gated_workspace_size(shape, self.act_int8), 256)
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(need, dtype=torch.uint8, device=self.router_w.device)
         return self._ws
 
     def forward(self, x: torch.Tensor, path: int = MOE_PATH_AUTO, y: Optional[torch.Tensor] = None,
                 ids: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None):
+        if self.gate is not None:
+            return moe_forward_gated(x, self.router_w, self.bias, self.experts, self.K, self.gate, self.act_int8,
+                                     path=path, y=y, ids=ids, w=w, workspace=self.workspace(self.shape(x, path)))
         return moe_forward(x, self.router_w, self.bias, self.experts, self.K, path=path, y=y, ids=ids, w=w,
                            workspace=self.workspace(self.shape(x, path)))
 
@@ -599,31 +631,6 @@ def moe_expert_ffn_mxfp4(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_s
 
 # ---------------------------------------------------------------- gated routing, int8 activations
 
-@dataclasses.dataclass
-class Gate:
-    """How a router's scores become the choice of experts and their weights (moe_route_gated).
-
-    score MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID; select_bias [E] fp32 is added to
-    the scores for the choice only (-inf takes an expert out of service); groups of
-    E / groups consecutive experts, of which the group_topk of the largest value stay
-    (group_by MOE_GROUP_MAX: the largest choice value of the group, MOE_GROUP_TOP2:
-    the sum of its two largest); renorm: the weights are divided by their sum; scale
-    multiplies them.
-    """
-    score: int = MOE_SCORE_SOFTMAX
-    select_bias: Optional[torch.Tensor] = None
-    groups: int = 1
-    group_topk: int = 1
-    group_by: int = MOE_GROUP_MAX
-    renorm: bool = True
-    scale: float = 1.0
-
-    def struct(self, E: int) -> MoeGate:
-        _check_sizes(self.groups, self.group_topk)
-        return MoeGate(_arg("select_bias", self.select_bias, torch.float32, (E,)), self.score, self.groups,
-                       self.group_topk, self.group_by, 1 if self.renorm else 0, self.scale)
-
-
 def moe_route_gated(x: torch.Tensor, router_w: torch.Tensor, bias: Optional[torch.Tensor], K: int, gate: Gate,
                     ids: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None):
     """Router with a Gate: x [T, d], router_w [E, d] (E up to 256), bias [E] fp32 added to the logits or None.
@@ -676,6 +683,67 @@ def moe_grouped_mm_int8(a_q: torch.Tensor, a_s: torch.Tensor, expert_offsets: to
         _arg("w_q", w_q, i8, w_shape), _arg("w_s", w_s, w_s.dtype, s_shape), _arg("w2_q", w2_q, i8, w_shape),
         _arg("w2_s", w2_s, w_s.dtype, s_shape), _arg("out", out, out_dtype, (rows * K, f)), _stream()))
     return out
+
+
+def moe_expert_ffn_int8(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_slots: torch.Tensor,
+                        experts: Int8Experts, K: int, path: int = MOE_PATH_AUTO,
+                        workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Expert SwiGLU FFNs with weights and activations in int8. Returns y_rows fp32 [T*K, d]."""
+    lib = _lib_handle()
+    if experts.fmt != MOE_W_INT8:
+        raise ValueError("the experts are not in int8")
+    T, d = x.shape
+    _check_width("x", d, experts.d)
+    weights = _weights(experts, "gate", "up", "down")
+    shape = make_shape(T, d, experts.f, experts.E, K, x.dtype, experts.scale_dtype, path, experts.fmt)
+    n = ctypes.c_size_t(0)
+    _lib.check(lib.moe_expert_ffn_int8_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    y_rows = torch.empty((T * K, d), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(max(n.value, 256), dtype=torch.uint8, device=x.device)
+    _lib.check(lib.moe_expert_ffn_int8(
+        ctypes.byref(shape), _arg("x", x, None),
+        _arg("expert_offsets", expert_offsets, torch.int32, (experts.E + 1,)),
+        _arg("sorted_slots", sorted_slots, torch.int32, (T * K,)), *weights, _ptr(y_rows),
+        _arg("workspace", workspace, torch.uint8), ctypes.c_size_t(workspace.numel()), _stream()))
+    return y_rows
+
+
+def gated_workspace_size(shape: MoeShape, act_int8: bool = False) -> int:
+    lib = _lib_handle()
+    n = ctypes.c_size_t(0)
+    _lib.check(lib.moe_gated_workspace_size(ctypes.byref(shape), MOE_ACT_INT8 if act_int8 else MOE_ACT_AS_IS,
+                                            ctypes.byref(n)))
+    return n.value
+
+
+def moe_forward_gated(x: torch.Tensor, router_w: torch.Tensor, bias: Optional[torch.Tensor], experts: Int8Experts,
+                      K: int, gate: Gate, act_int8: bool = False, path: int = MOE_PATH_AUTO,
+                      y: Optional[torch.Tensor] = None, ids: Optional[torch.Tensor] = None,
+                      w: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The whole layer with a Gate, and with act_int8 the experts' products in int8 by int8 (int8 weights).
+    Returns (y [T, d] in x.dtype, topk_ids [T, K], topk_w [T, K])."""
+    lib = _lib_handle()
+    T, d = x.shape
+    _check_width("x", d, experts.d)
+    weights = _weights(experts, "gate", "up", "down")
+    shape = make_shape(T, d, experts.f, experts.E, K, x.dtype, experts.scale_dtype, path, experts.fmt)
+    g = gate.struct(experts.E)
+    need = gated_workspace_size(shape, act_int8)
+    if y is None:
+        y = torch.empty((T, d), dtype=x.dtype, device=x.device)
+    if ids is None:
+        ids = torch.empty((T, K), dtype=torch.int32, device=x.device)
+    if w is None:
+        w = torch.empty((T, K), dtype=torch.float32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    _lib.check(lib.moe_forward_gated(
+        ctypes.byref(shape), ctypes.byref(g), MOE_ACT_INT8 if act_int8 else MOE_ACT_AS_IS, _arg("x", x, None),
+        _arg("router_w", router_w, x.dtype, (experts.E, d)), _arg("bias", bias, torch.float32, (experts.E,)), *weights,
+        _arg("y", y, x.dtype, (T, d)), _arg("ids", ids, torch.int32, (T, K)), _arg("w", w, torch.float32, (T, K)),
+        _arg("workspace", workspace, torch.uint8), ctypes.c_size_t(workspace.numel()), _stream()))
+    return y, ids, w
 
 
 def moe_norm_pre(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -790,5 +858,48 @@ def moe_block_forward(residual: torch.Tensor, router_w: torch.Tensor, bias: Opti
         ctypes.byref(p), _arg("router_w", router_w, dt, (experts.E, d)),
         _arg("bias", bias, torch.float32, (experts.E,)), *weights, _arg("out", out, dt, (T, d)),
         _arg("next_out", nxt, dt, (T, d)), _ptr(ids), _ptr(w),
+        _arg("workspace", workspace, torch.uint8), ctypes.c_size_t(workspace.numel()), _stream()))
+    return out, nxt, ids, w
+
+
+def block_gated_workspace_size(shape: MoeShape, act_int8: bool = False) -> int:
+    lib = _lib_handle()
+    n = ctypes.c_size_t(0)
+    _lib.check(lib.moe_block_gated_workspace_size(ctypes.byref(shape), MOE_ACT_INT8 if act_int8 else MOE_ACT_AS_IS,
+                                                  ctypes.byref(n)))
+    return n.value
+
+
+def moe_block_forward_gated(residual: torch.Tensor, router_w: torch.Tensor, bias: Optional[torch.Tensor],
+                            experts: Int8Experts, K: int, route: Gate, act_int8: bool = False,
+                            pre_weight: Optional[torch.Tensor] = None, pre_eps: float = 1e-6,
+                            x: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                            gate: Optional[torch.Tensor] = None, gate_tokens: int = 1, residual_scale: float = 1.0,
+                            block_scale: float = 1.0, eps: float = 1e-6, next_weight: Optional[torch.Tensor] = None,
+                            next_eps: Optional[float] = None, path: int = MOE_PATH_AUTO,
+                            out: Optional[torch.Tensor] = None, next_out: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None):
+    """moe_block_forward with the layer of moe_forward_gated; `route` is its Gate, `gate` the factor of the
+    layer's output as there. Returns (out, next or None, topk_ids [T, K], topk_w [T, K])."""
+    lib = _lib_handle()
+    T, d = residual.shape
+    dt = residual.dtype
+    _check_width("residual", d, experts.d)
+    weights = _weights(experts, "gate", "up", "down")
+    shape = make_shape(T, d, experts.f, experts.E, K, dt, experts.scale_dtype, path, experts.fmt)
+    g = route.struct(experts.E)
+    p = _post(T, d, dt, weight, gate, gate_tokens, residual_scale, block_scale, eps, next_weight, next_eps)
+    res = _arg("residual", residual, dt)
+    out, nxt = _post_outputs(residual, out, next_weight, next_out)
+    ids = torch.empty((T, K), dtype=torch.int32, device=residual.device)
+    w = torch.empty((T, K), dtype=torch.float32, device=residual.device)
+    need = block_gated_workspace_size(shape, act_int8)
+    if workspace is None:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=residual.device)
+    _lib.check(lib.moe_block_forward_gated(
+        ctypes.byref(shape), ctypes.byref(g), MOE_ACT_INT8 if act_int8 else MOE_ACT_AS_IS, res,
+        _arg("pre_weight", pre_weight, dt, (d,)), pre_eps, _arg("x", x, dt, (T, d)), ctypes.byref(p),
+        _arg("router_w", router_w, dt, (experts.E, d)), _arg("bias", bias, torch.float32, (experts.E,)), *weights,
+        _arg("out", out, dt, (T, d)), _arg("next_out", nxt, dt, (T, d)), _ptr(ids), _ptr(w),
         _arg("workspace", workspace, torch.uint8), ctypes.c_size_t(workspace.numel()), _stream()))
     return out, nxt, ids, w

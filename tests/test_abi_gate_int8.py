@@ -103,3 +103,95 @@ def test_binding_checks():
         m.moe_grouped_mm_int8(aq, a_s, off, wq, w_s.half(), torch.float32)
     with pytest.raises(ValueError, match="a_q is on cpu"):
         m.moe_grouped_mm_int8(aq, a_s, off, wq, w_s, torch.float32)
+
+
+BIG = ctypes.c_size_t(1 << 40)
+
+
+def _r(v):
+    return (v + 255) // 256 * 256
+
+
+def test_expert_ffn_int8(lib):
+    n = ctypes.c_size_t(0)
+    size = lib.moe_expert_ffn_int8_workspace_size
+    assert size(_shape(weight_fmt=2), ctypes.byref(n)) == DTYPE and size(_shape(), None) == NULL
+    assert size(_shape(K=17), ctypes.byref(n)) == SHAPE and size(_shape(E=1), ctypes.byref(n)) == SHAPE
+    assert size(_shape(), ctypes.byref(n)) == OK
+    assert n.value == _r(32 * 256) + _r(32 * 4) + _r(64 * 512) + _r(64 * 4) + _r(64 * 1024)
+    call = lambda ws, b: lib.moe_expert_ffn_int8(_shape(), *([A] * 10), ws, ctypes.c_size_t(b), None)
+    assert call(A, n.value - 1) == WORKSPACE and call(None, n.value) == NULL and call(MIS, n.value) == ALIGN
+    for i in range(10):
+        args = [A] * 10
+        args[i] = None
+        assert lib.moe_expert_ffn_int8(_shape(), *args, A, n, None) == NULL, i
+    assert lib.moe_expert_ffn_int8(_shape(T=0), *([None] * 11), ctypes.c_size_t(0), None) == OK
+
+
+def test_forward_gated(lib):
+    n, fwd, ffn = (ctypes.c_size_t(0) for _ in range(3))
+    size = lib.moe_gated_workspace_size
+    assert size(_shape(), 2, ctypes.byref(n)) == DTYPE and size(_shape(), 0, None) == NULL
+    assert size(_shape(E=65), 0, ctypes.byref(n)) == SHAPE
+    for fmt in (1, 2, 4):
+        assert size(_shape(weight_fmt=fmt), 1, ctypes.byref(n)) == DTYPE
+    assert lib.moe_workspace_size(_shape(), ctypes.byref(fwd)) == OK
+    assert lib.moe_expert_ffn_int8_workspace_size(_shape(), ctypes.byref(ffn)) == OK
+    assert size(_shape(), 0, ctypes.byref(n)) == OK and n.value == _r(fwd.value)
+    assert size(_shape(), 1, ctypes.byref(n)) == OK and n.value == _r(fwd.value) + ffn.value - _r(64 * 1024)
+
+    def call(s=None, g=None, act=1, ptrs=None, ws=A, b=1 << 40, ids=None):
+        ptrs = ptrs or [A, A, None, A, A, A, A, A, A, B]
+        return lib.moe_forward_gated(s or _shape(), g or _gate(), act, *ptrs, ids, None, ws, ctypes.c_size_t(b), None)
+    assert lib.moe_forward_gated(_shape(), None, 0, *([A] * 13), BIG, None) == NULL
+    assert call(act=-1) == DTYPE and call(_shape(weight_fmt=2), act=1) == DTYPE
+    assert call(_shape(E=128)) == SHAPE and call(g=_gate(groups=5)) == SHAPE and call(g=_gate(select_bias=MIS)) == ALIGN
+    assert call(b=n.value - 1) == WORKSPACE and call(ws=None) == NULL and call(ids=MIS) == ALIGN
+    assert call(act=0, b=fwd.value - 1) == WORKSPACE
+    for i in (0, 1, 3, 4, 5, 6, 7, 8, 9):
+        ptrs = [A, A, None, A, A, A, A, A, A, B]
+        ptrs[i] = None
+        assert call(ptrs=ptrs) == NULL, i
+        ptrs[i] = MIS
+        assert call(ptrs=ptrs) == ALIGN, i
+    assert call(ptrs=[A, A, MIS, A, A, A, A, A, A, B]) == ALIGN
+    assert lib.moe_forward_gated(_shape(T=0), _gate(), 1, *([None] * 13), ctypes.c_size_t(0), None) == OK
+
+
+def test_block_forward_gated(lib):
+    n, g = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    assert lib.moe_gated_workspace_size(_shape(), 1, ctypes.byref(g)) == OK
+    assert lib.moe_block_gated_workspace_size(_shape(), 1, ctypes.byref(n)) == OK
+    assert n.value == _r(g.value) + _r(32 * 256 * 2)
+    assert lib.moe_block_gated_workspace_size(_shape(), 3, ctypes.byref(n)) == DTYPE
+    post = ctypes.byref(_lib.MoePost(weight=A, gate=None, next_weight=None, gate_tokens=1, residual_scale=1.0,
+                                     block_scale=1.0, eps=1e-6, next_eps=1e-6))
+
+    def call(s=None, gate=_gate(), act=1, b=1 << 40, x=None, pre=A):
+        return lib.moe_block_forward_gated(s or _shape(), gate, act, A, pre, 1e-6, x, post, A, None, A, A, A, A, A, A, B,
+                                           None, None, None, A, ctypes.c_size_t(b), None)
+    assert call(gate=None) == NULL and call(gate=_gate(score=7)) == SHAPE and call(act=5) == DTYPE
+    assert call(_shape(weight_fmt=1)) == DTYPE
+    assert call(b=_r(g.value) + _r(32 * 256 * 2) - 1) == WORKSPACE
+    assert call(x=A) == UNSUPPORTED and call(pre=None) == NULL
+    assert call(_shape(T=0)) == OK
+
+
+def test_binding_of_the_layer():
+    from tests.test_binding_mxfp4 import D, E, _experts
+    x, wr = torch.zeros(4, D, dtype=torch.bfloat16), torch.zeros(E, D, dtype=torch.bfloat16)
+    off, srt = torch.zeros(E + 1, dtype=torch.int32), torch.zeros(8, dtype=torch.int32)
+    ex = _experts(m.MOE_W_INT8)
+    for bad in (m.MOE_W_FP8, m.MOE_W_MXFP4):
+        with pytest.raises(ValueError, match="not in int8"):
+            m.moe_expert_ffn_int8(x, off, srt, _experts(bad), 2)
+    for call in (lambda: m.moe_expert_ffn_int8(x, off, srt, ex, 2),
+                 lambda: m.moe_forward_gated(x, wr, None, ex, 2, m.Gate()),
+                 lambda: m.moe_block_forward_gated(x, wr, None, ex, 2, m.Gate(), pre_weight=x[0])):
+        with pytest.raises(ValueError, match="not on the current HIP device"):
+            call()
+    with pytest.raises(ValueError, match="columns"):
+        m.moe_forward_gated(x[:, :64].contiguous(), wr, None, ex, 2, m.Gate())
+    ex.s_up = ex.s_up[:, :-1].contiguous()
+    with pytest.raises(ValueError, match="the experts' s_up"):
+        m.moe_forward_gated(x, wr, None, ex, 2, m.Gate())

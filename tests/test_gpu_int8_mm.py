@@ -109,6 +109,31 @@ def test_long_and_wide(counts, d, f, path):
     _run(counts, sum(counts), 1, d, f, True, "bf16", "bf16", path, False, d + f)
 
 
+# what is taken: (mean rows an expert, E, f, path, the log's words); f / 32 * E items of 32 channels: 2048 is the border
+INSTANCES = [(4, 16, 4160, MOE_PATH_AUTO, "16-channel items, 16-row passes, reduction in 4 slices"),
+             (5, 16, 4160, MOE_PATH_AUTO, "32-channel items, 32-row passes, reduction in 2 slices"),
+             (8, 16, 4160, MOE_PATH_AUTO, "32-channel items, 32-row passes, reduction in 2 slices"),
+             (8, 16, 4032, MOE_PATH_AUTO, "16-channel items, 16-row passes, reduction in 4 slices"),
+             (9, 16, 4160, MOE_PATH_STREAM, "32-channel items, 64-row passes, reduction in 4 slices"),
+             (9, 16, 4160, MOE_PATH_AUTO, "tiled schedule, 128x"),
+             (64, 1, 1024, MOE_PATH_AUTO, "32-channel items, 64-row passes, reduction in 4 slices"),
+             (65, 1, 1024, MOE_PATH_AUTO, "tiled schedule, 128x128 tiles"),
+             (64, 16, 8320, MOE_PATH_AUTO, "tiled schedule, 128x"), (65, 16, 8320, MOE_PATH_AUTO, "tiled schedule, 128x256 tiles"),
+             (40, 4, 512, MOE_PATH_TILED, "tiled schedule, 128x128 tiles")]
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,E,f,path,words", INSTANCES)
+def test_every_instance_and_border(rows, E, f, path, words, out, swiglu, monkeypatch, capfd):
+    rng = np.random.default_rng(rows * 31 + E)
+    counts = rng.multinomial(rows * E, np.ones(E) / E).tolist()
+    monkeypatch.setenv("MOE_LOG", "1")
+    _run(counts, rows * E, 1, 192, f, swiglu, out, "bf16", path, True, rows + f)
+    line = [l for l in capfd.readouterr().err.splitlines() if "moe_grouped_mm_int8" in l]
+    assert len(line) == 1 and words in line[0], line
+
+
 @pytest.mark.parametrize("path", PATHS)
 def test_largest_sums(path):
     """Codes of -128, -127 and 127 only, over the longest reduction: sums up to 2^30."""
