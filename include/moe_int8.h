@@ -463,9 +463,14 @@ typedef struct moe_gate {
 } moe_gate;
 
 /* As moe_route; here shape->E may be up to 256 (a GPU that holds some of them
- * permutes ids less its first expert's: ids outside [0, its experts) are not placed). */
+ * permutes ids less its first expert's: ids outside [0, its experts) are not placed).
+ *   workspace: NULL, or 16-byte aligned and at least moe_route_gated_workspace_size
+ *     bytes (0 for shapes that have no use for it). With it the rows of few tokens
+ *     are split over workgroups (half as long for 63 tokens and 64 experts). */
+moe_status moe_route_gated_workspace_size(const moe_shape* shape, size_t* bytes);
 moe_status moe_route_gated(const moe_shape* shape, const moe_gate* gate, const void* x, const void* router_w,
-                           const float* router_bias, int32_t* topk_ids, float* topk_w, hipStream_t stream);
+                           const float* router_bias, int32_t* topk_ids, float* topk_w, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------- int8 activations
  * Products of int8 rows, a scale each (moe_quantize_rows with fp32 scales), and the

@@ -35,7 +35,7 @@ EXPORTS = (
     "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_pack_mxfp4", "moe_grouped_mm_mxfp4",
     "moe_expert_ffn_mxfp4_workspace_size", "moe_expert_ffn_mxfp4", "moe_norm_pre", "moe_norm_post",
     "moe_combine_post", "moe_block_workspace_size", "moe_block_forward",
-    "moe_route_gated", "moe_grouped_mm_int8", "moe_expert_ffn_int8_workspace_size", "moe_expert_ffn_int8",
+    "moe_route_gated_workspace_size", "moe_route_gated", "moe_grouped_mm_int8", "moe_expert_ffn_int8_workspace_size", "moe_expert_ffn_int8",
     "moe_gated_workspace_size", "moe_forward_gated", "moe_block_gated_workspace_size", "moe_block_forward_gated",
 )
 
@@ -98,7 +98,8 @@ _SIGS = {
     "moe_grouped_mm_mxfp4": (_I32, [_SHAPE] + [_P] * 10),
     "moe_expert_ffn_mxfp4_workspace_size": (_I32, [_SHAPE, ctypes.POINTER(_SIZE)]),
     "moe_expert_ffn_mxfp4": (_I32, [_SHAPE] + [_P] * 11 + [_SIZE, _P]),
-    "moe_route_gated": (_I32, [_SHAPE, _GATE] + [_P] * 6),
+    "moe_route_gated_workspace_size": (_I32, [_SHAPE, ctypes.POINTER(_SIZE)]),
+    "moe_route_gated": (_I32, [_SHAPE, _GATE] + [_P] * 6 + [_SIZE, _P]),
     "moe_grouped_mm_int8": (_I32, [_SHAPE] + [_P] * 10),
     "moe_expert_ffn_int8_workspace_size": (_I32, [_SHAPE, ctypes.POINTER(_SIZE)]),
     "moe_expert_ffn_int8": (_I32, [_SHAPE] + [_P] * 11 + [_SIZE, _P]),

@@ -559,7 +559,12 @@ moe::GateArgs gate_args(const moe_shape* s, const moe_gate* g, const void* x, co
   a.groups = g->groups;
   a.group_topk = g->group_topk;
   a.scale = g->scale;
+  a.workspace = nullptr;
   return a;
+}
+
+size_t route_gated_ws_bytes(const moe_shape* s) {
+  return moe::route_gated_workspace(s->T, s->d, s->E, s->act_dtype == MOE_BF16);
 }
 
 // moe_block_forward's workspace: moe_forward's, then the normalised input.
@@ -706,10 +711,11 @@ moe_status scratch_on_current_device(void** out) {
   return MOE_OK;
 }
 
-// moe_forward_gated's workspace: moe_forward's, then with int8 activations moe_expert_ffn_int8's but h.
+// moe_forward_gated's workspace: moe_forward's, then moe_route_gated's, then with int8 activations
+// moe_expert_ffn_int8's but h.
+size_t gated_ffn_at(const moe_shape* s) { return round_up(forward_layout(s).total) + round_up(route_gated_ws_bytes(s)); }
 size_t gated_ws_bytes(const moe_shape* s, int32_t expert_act) {
-  const size_t fwd = round_up(forward_layout(s).total);
-  return expert_act == MOE_ACT_INT8 ? fwd + i8_ffn_layout(s, false).total : fwd;
+  return gated_ffn_at(s) + (expert_act == MOE_ACT_INT8 ? i8_ffn_layout(s, false).total : 0);
 }
 
 moe_status check_expert_act(const moe_shape* s, int32_t expert_act) {
@@ -748,7 +754,7 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
   if (topk_ids_out && !aligned16(topk_ids_out)) return fail(MOE_ERR_ALIGN, "topk_ids_out is not 16-byte aligned");
   if (topk_w_out && !aligned16(topk_w_out)) return fail(MOE_ERR_ALIGN, "topk_w_out is not 16-byte aligned");
   const WsLayout L = forward_layout(s);
-  const size_t need = expert_act == MOE_ACT_INT8 ? gated_ws_bytes(s, expert_act) : L.total;
+  const size_t need = gate ? gated_ws_bytes(s, expert_act) : L.total;
   if (workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
 
@@ -761,9 +767,14 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
   __bf16* h = reinterpret_cast<__bf16*>(ws + L.h);
   float* y_rows = reinterpret_cast<float*>(ws + L.y_rows);
 
-  hipError_t e = gate ? moe::launch_route_gated(gate_args(s, gate, x, router_w, router_bias, ids, wts), stream)
-                      : moe::launch_router(x, router_w, router_bias, s->T, s->d, s->E, s->K,
-                                           s->act_dtype == MOE_BF16, ids, wts, stream);
+  hipError_t e;
+  if (gate) {
+    moe::GateArgs g = gate_args(s, gate, x, router_w, router_bias, ids, wts);
+    g.workspace = ws + round_up(L.total);
+    e = moe::launch_route_gated(g, stream);
+  } else {
+    e = moe::launch_router(x, router_w, router_bias, s->T, s->d, s->E, s->K, s->act_dtype == MOE_BF16, ids, wts, stream);
+  }
   if (e != hipSuccess) return hip_fail(e, "router launch");
   moe::FfnArgs a = ffn_args(s, x, offsets, sorted, w_gate, w_up, w_down, s_gate, s_up, s_down, y_rows, h);
   if (L.part_bytes) a.part = reinterpret_cast<float*>(ws + L.part);
@@ -776,7 +787,7 @@ moe_status forward_impl(const char* call, const moe_shape* s, const void* x, con
     if (e != hipSuccess) return hip_fail(e, "permute launch");
     if (debug_on() && (st = debug_permutation(s, ids, offsets, sorted, s2r, stream, gate != nullptr)) != MOE_OK) return st;
     st = run_i8_ffn(call, s, x, offsets, sorted, w_gate, w_up, w_down, s_gate, s_up, s_down, y_rows,
-                    h, ws + round_up(L.total), stream);
+                    h, ws + gated_ffn_at(s), stream);
   } else if (use_stream(s) && s->weight_fmt != MOE_W_MXFP4 && moe::stream_gate_up_takes_ids((long)s->T * s->K, s->E)) {
     // at most 256 slots: the gate/up pass derives the permutation from the ids
     // and writes it for the down pass and the combine (one launch fewer)
@@ -1354,8 +1365,17 @@ moe_status moe_expert_ffn_mxfp4(const moe_shape* s, const void* x, const int32_t
   return run_mx("moe_expert_ffn_mxfp4", "down", s, m, stream);
 }
 
+moe_status moe_route_gated_workspace_size(const moe_shape* shape, size_t* bytes) {
+  const moe_status st = check_shape(shape, true, 256);
+  if (st != MOE_OK) return st;
+  if (!bytes) return fail(MOE_ERR_NULL, "bytes is NULL");
+  *bytes = route_gated_ws_bytes(shape);
+  return MOE_OK;
+}
+
 moe_status moe_route_gated(const moe_shape* s, const moe_gate* gate, const void* x, const void* router_w,
-                           const float* router_bias, int32_t* topk_ids, float* topk_w, hipStream_t stream) {
+                           const float* router_bias, int32_t* topk_ids, float* topk_w, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream) {
   moe_status st = check_shape(s, true, 256);
   if (st != MOE_OK) return st;
   if ((st = check_gate(s, gate)) != MOE_OK) return st;
@@ -1365,7 +1385,15 @@ moe_status moe_route_gated(const moe_shape* s, const moe_gate* gate, const void*
   REQUIRE_PTR(topk_ids);
   REQUIRE_PTR(topk_w);
   if (!aligned16(router_bias)) return fail(MOE_ERR_ALIGN, "router_bias is not 16-byte aligned");
-  const hipError_t e = moe::launch_route_gated(gate_args(s, gate, x, router_w, router_bias, topk_ids, topk_w), stream);
+  moe::GateArgs a = gate_args(s, gate, x, router_w, router_bias, topk_ids, topk_w);
+  if (workspace) {
+    const size_t need = route_gated_ws_bytes(s);
+    if (!aligned16(workspace)) return fail(MOE_ERR_ALIGN, "workspace is not 16-byte aligned");
+    if (workspace_bytes < need)
+      return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
+    a.workspace = workspace;
+  }
+  const hipError_t e = moe::launch_route_gated(a, stream);
   if (e != hipSuccess) return hip_fail(e, "router launch");
   return MOE_OK;
 }

@@ -166,7 +166,10 @@ struct GateArgs {
   bool act_bf16, sigmoid, top2, renorm;
   int T, d, E, K, groups, group_topk;
   float scale;
+  void* workspace;           // route_gated_workspace bytes, or null
 };
+// Workspace with which few tokens' rows are split over workgroups; 0: they are not.
+size_t route_gated_workspace(int T, int d, int E, bool act_bf16);
 hipError_t launch_route_gated(const GateArgs& a, hipStream_t stream);
 
 // Norms around the layer (block_norm.hip).

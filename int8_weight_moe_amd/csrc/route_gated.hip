@@ -28,6 +28,11 @@ namespace moe {
 namespace {
 
 constexpr int kMaxExperts = 256;
+// Up to so many tokens split rows of at least so many steps over workgroups, given a
+// workspace. Measured, us, split / fused kernel: 1 token, d 8192, E 16 (8 steps) 7.8 / 9.9, d 4096 (4 steps) 8.0 / 7.8;
+// d 8192, E 64 (32 steps): 63 tokens 13.2 / 26.0, 256 19.0 / 32.4, 1024 27.6 / 37.0, 2048 40.0 / 38.4; d 4096, E 256
+// (64 steps): 16 tokens 21.6 / 44.7, 1024 39.8 / 56.8, 2048 58.2 / 57.9; d 8192, E 16: 1024 13.4 / 15.2, 2048 19.8 / 15.5.
+constexpr int kSplitTokens = 1024, kSplitSteps = 8;
 
 // What the fp32 sums of a block are taken to be off by, in 2^-23 of the sum of their
 // terms' magnitudes. A 16x16x32 bf16 MFMA adds four groups of eight products, each
@@ -723,6 +728,96 @@ __global__ __launch_bounds__(kWaves* kWave, 4) void route_gated_kernel(GateArgs 
   choose_all<Act, kWaves, TOK, kSlots>(a, s, tok0, n, kSumUnits<Act>);
 }
 
+// ------------------------------------------------------------------ few tokens
+// One workgroup of the fused kernel walks the whole of a long row step by step, each a trip to memory. Few tokens split
+// the row over workgroups instead: one kernel writes the splits' sums and squares to the workspace, the next adds them
+// and chooses.
+struct SplitSums {
+  double* sum;          // [splits][T][E]
+  float *x_sq, *w_sq;   // [splits][T], [splits][E]
+  int splits, steps;    // steps of a split
+};
+
+template <typename Act, int NEB>
+__global__ __launch_bounds__(16 * kWave, 4) void route_logits_kernel(GateArgs a, SplitSums p) {
+  constexpr int kWaves = 16, D = 2;
+  using S = Tile<NEB, 1, kWaves, D>;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::kLds];
+  __shared__ float x_sq[S::KS * S::TOK], w_sq[S::KS * S::EP];
+  const int tok0 = blockIdx.x * 16, split = blockIdx.y;
+  const int n = min(16, a.T - tok0);
+  const int blocks = (int)((long)a.d * sizeof(Act) / kBlockBytes);
+  const int nsteps = (blocks + S::KS - 1) / S::KS;
+  // every split has a step: splits = ceil(nsteps / steps)
+  tile_logits<Act, NEB, 1, kWaves, D>(a, tok0, n, split * p.steps, min((split + 1) * p.steps, nsteps), lds, x_sq, w_sq);
+  for (int i = threadIdx.x; i < n * S::EP; i += kWaves * kWave) {
+    const int t = i / S::EP, e = i % S::EP;
+    if (e >= a.E) continue;
+    double v = 0;
+#pragma unroll
+    for (int k = 0; k < S::KS; ++k) v += reinterpret_cast<const double*>(lds)[k * S::TOK * S::EP + i];
+    p.sum[((long)split * a.T + tok0 + t) * a.E + e] = v;
+  }
+  for (int i = threadIdx.x; i < n + a.E; i += kWaves * kWave) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < S::KS; ++k) v += i < n ? x_sq[k * S::TOK + i] : w_sq[k * S::EP + i - n];
+    if (i < n) p.x_sq[(long)split * a.T + tok0 + i] = v;
+    else if (blockIdx.x == 0) p.w_sq[(long)split * a.E + i - n] = v;
+  }
+}
+
+template <typename Act, int EP, int kSlots>
+__global__ __launch_bounds__(4 * kWave) void route_choose_kernel(GateArgs a, SplitSums p) {
+  constexpr int kWaves = 4;
+  __shared__ double logit[EP];
+  __shared__ uint16_t work[EP];
+  __shared__ ChoiceLds<1, EP> c;
+  const int t = blockIdx.x;
+  if (threadIdx.x < 8) c.refined[0][threadIdx.x] = 0;
+  if (threadIdx.x == 0) c.n_work = 0;
+  __syncthreads();
+  const TokenState s = {logit, c.x_norm, c.w_norm, &c.refined[0][0], work, &c.n_work, EP};
+  for (int e = threadIdx.x; e < a.E; e += kWaves * kWave) {
+    double v = 0;
+    float q = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < p.splits; ++k) {
+      v += p.sum[((long)k * a.T + t) * a.E + e];
+      q += p.w_sq[(long)k * a.E + e];
+    }
+    c.w_norm[e] = norm_of(q);
+    put_logit(a, s, 0, e, v);
+  }
+  if (threadIdx.x >= (kWaves - 1) * kWave) {
+    float q = 0.f;
+    for (int k = threadIdx.x & 63; k < p.splits; k += kWave) q += p.x_sq[(long)k * a.T + t];
+    q = wave_sum(q);
+    if ((threadIdx.x & 63) == 0) c.x_norm[0] = norm_of(q);
+  }
+  __syncthreads();
+  choose_all<Act, kWaves, 1, kSlots>(a, s, t, 1, kSumUnits<Act>);
+}
+
+// Blocks of 16 experts of a tile, and the splits of few tokens' rows; splits 0: the fused kernel.
+int expert_blocks(int E) { return E <= 16 ? 1 : E <= 32 ? 2 : E <= 64 ? 4 : E <= 128 ? 8 : 16; }
+SplitSums split_of(int T, int d, int E, bool act_bf16) {
+  SplitSums p = {};
+  const int blocks = (int)((long)d * (act_bf16 ? 2 : 4) / kBlockBytes), slices = 16 / expert_blocks(E);
+  const int nsteps = (blocks + slices - 1) / slices, tiles = (T + 15) / 16;
+  if (T == 0 || T > kSplitTokens || nsteps < kSplitSteps) return p;
+  const int most = 256 / tiles;                      // a workgroup a CU
+  p.steps = (nsteps + most - 1) / most;
+  p.splits = (nsteps + p.steps - 1) / p.steps;
+  return p;
+}
+
+template <typename Act, int NEB, int kSlots>
+void launch_split(const GateArgs& a, const SplitSums& p, hipStream_t stream) {
+  hipLaunchKernelGGL((route_logits_kernel<Act, NEB>), dim3((a.T + 15) / 16, p.splits), dim3(16 * kWave), 0, stream, a, p);
+  hipLaunchKernelGGL((route_choose_kernel<Act, 16 * NEB, kSlots>), dim3(a.T), dim3(4 * kWave), 0, stream, a, p);
+}
+
 template <typename Act, int NEB, int TB, int kWaves, int kSlots>
 void launch_tile(const GateArgs& a, int tpw, hipStream_t stream) {
   constexpr int D = NEB == 1 ? 2 : 3;
@@ -732,6 +827,13 @@ void launch_tile(const GateArgs& a, int tpw, hipStream_t stream) {
 
 template <typename Act, int NEB, int kSlots>
 void launch_experts(const GateArgs& a, hipStream_t stream) {
+  SplitSums p = split_of(a.T, a.d, a.E, a.act_bf16);
+  if (p.splits && a.workspace) {
+    p.sum = static_cast<double*>(a.workspace);
+    p.x_sq = reinterpret_cast<float*>(p.sum + (long)p.splits * a.T * a.E);
+    p.w_sq = p.x_sq + (long)p.splits * a.T;
+    return launch_split<Act, NEB, kSlots>(a, p, stream);
+  }
   if constexpr (NEB <= 4) {
     // As few tokens a workgroup as leave no CU without one, so that a small batch's reads of router_w are spread. Few
     // workgroups: the most waves each; many: two workgroups a CU, one of which loads while the other chooses.
@@ -765,6 +867,11 @@ void launch(const GateArgs& a, hipStream_t stream) {
 }
 
 }  // namespace
+
+size_t route_gated_workspace(int T, int d, int E, bool act_bf16) {
+  const SplitSums p = split_of(T, d, E, act_bf16);
+  return (size_t)p.splits * ((size_t)T * E * 8 + (size_t)(T + E) * 4);
+}
 
 hipError_t launch_route_gated(const GateArgs& a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;

@@ -632,23 +632,32 @@ def moe_expert_ffn_mxfp4(x: torch.Tensor, expert_offsets: torch.Tensor, sorted_s
 # ---------------------------------------------------------------- gated routing, int8 activations
 
 def moe_route_gated(x: torch.Tensor, router_w: torch.Tensor, bias: Optional[torch.Tensor], K: int, gate: Gate,
-                    ids: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None):
+                    ids: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None, use_workspace: bool = True,
+                    workspace: Optional[torch.Tensor] = None):
     """Router with a Gate: x [T, d], router_w [E, d] (E up to 256), bias [E] fp32 added to the logits or None.
     Returns (topk_ids int32 [T, K], topk_w fp32 [T, K]); ids of -1 (weight 0) where fewer than K experts can
-    be taken."""
+    be taken. With use_workspace the call gets the workspace it can use (`workspace` if given, else a new one:
+    few tokens' rows are split over workgroups)."""
     lib = _lib_handle()
     T, d = x.shape
     E = router_w.shape[0]
     shape = make_shape(T, d, 64, E, K, x.dtype, torch.float32)
     g = gate.struct(E)
+    dev = x.device
     if ids is None:
-        ids = torch.empty((T, K), dtype=torch.int32, device=x.device)
+        ids = torch.empty((T, K), dtype=torch.int32, device=dev)
     if w is None:
-        w = torch.empty((T, K), dtype=torch.float32, device=x.device)
+        w = torch.empty((T, K), dtype=torch.float32, device=dev)
+    if use_workspace and workspace is None:
+        n = ctypes.c_size_t(0)
+        _lib.check(lib.moe_route_gated_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+        if n.value:
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+    ws = workspace if use_workspace else None
     _lib.check(lib.moe_route_gated(ctypes.byref(shape), ctypes.byref(g), _arg("x", x, None),
                                    _arg("router_w", router_w, x.dtype, (E, d)), _arg("bias", bias, torch.float32, (E,)),
                                    _arg("ids", ids, torch.int32, (T, K)), _arg("w", w, torch.float32, (T, K)),
-                                   _stream()))
+                                   _arg("workspace", ws, torch.uint8), 0 if ws is None else ws.numel(), _stream()))
     return ids, w
 
 

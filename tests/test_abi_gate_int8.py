@@ -49,19 +49,29 @@ def test_header_constants():
     (dict(T=0, E=1, K=1), dict(group_by=1), OK), (dict(T=0), dict(groups=16, group_topk=2, scale=-2.5), OK),
 ])
 def test_gate_refusals(lib, shape, gate, status):
-    assert lib.moe_route_gated(_shape(**shape), _gate(**gate), A, A, None, A, A, None) == status
+    assert lib.moe_route_gated(_shape(**shape), _gate(**gate), A, A, None, A, A, None, 0, None) == status
     if status != OK:
         assert lib.moe_last_error()
 
 
 def test_route_gated_pointers(lib):
-    call = lambda x=A, wr=A, b=None, ids=A, w=A, g=_gate(): lib.moe_route_gated(_shape(), g, x, wr, b, ids, w, None)
+    call = lambda x=A, wr=A, b=None, ids=A, w=A, g=_gate(): lib.moe_route_gated(_shape(), g, x, wr, b, ids, w, None, 0, None)
     assert call(g=None) == NULL
     for kw in (dict(x=None), dict(wr=None), dict(ids=None), dict(w=None)):
         assert call(**kw) == NULL, kw
     for kw in (dict(x=MIS), dict(wr=MIS), dict(b=MIS), dict(ids=MIS), dict(w=MIS)):
         assert call(**kw) == ALIGN, kw
-    assert lib.moe_route_gated(_shape(T=0), _gate(), None, None, None, None, None, None) == OK
+    assert lib.moe_route_gated(_shape(T=0), _gate(), None, None, None, None, None, None, 0, None) == OK
+    n = ctypes.c_size_t(0)
+    size = lib.moe_route_gated_workspace_size
+    assert size(_shape(E=257), ctypes.byref(n)) == SHAPE and size(_shape(), None) == NULL
+    # 64 bf16 columns a block, 16 slices of 16 experts: 8 steps and more are split, up to 1024 tokens
+    for kw, want in ((dict(T=1, d=4096), 0), (dict(T=1, d=8192), 8 * (16 * 8 + 17 * 4)), (dict(T=1024, d=8192, E=256), 4 * (1024 * 2048 + 1280 * 4)),
+                     (dict(T=1025, d=8192), 0), (dict(T=0, d=8192), 0), (dict(T=17, d=4096, act_dtype=0), 8 * (17 * 128 + 33 * 4))):
+        assert size(_shape(**kw), ctypes.byref(n)) == OK and n.value == want, kw
+    big = _shape(T=1, d=8192)
+    call = lambda ws, b: lib.moe_route_gated(big, _gate(), A, A, None, A, A, ws, ctypes.c_size_t(b), None)
+    assert call(A, 8 * 196 - 1) == WORKSPACE and call(MIS, 8 * 196) == ALIGN
 
 
 def test_grouped_mm_int8(lib):

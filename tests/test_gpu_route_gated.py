@@ -200,6 +200,25 @@ def test_a_token_does_not_depend_on_its_batch():
             assert torch.equal(i, ids[rows]) and torch.equal(v, w[rows]), (E, rows)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E", [(1, 8192, 16), (5, 8192, 30), (17, 2048, 64), (33, 1088, 100), (64, 832, 250), (1024, 4096, 64),
+                                   (100, 576, 256)])
+def test_with_and_without_a_workspace(T, d, E, act):
+    """Rows split over workgroups or not, in a workspace of any contents: the same ids, and weights within their bounds."""
+    rng = np.random.default_rng(T + d)
+    x, wr = _draw(rng, T, d, E, act)
+    x[T // 2] = 0
+    select = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    kw = dict(sigmoid=True, groups=2 if E % 2 == 0 else 1, group_topk=1, top2=E % 2 == 0, scale=2.5)
+    ids, w = _check(x, wr, None, 4, select, "split", **kw)
+    g = _gate(select, **kw)
+    a, b = m.moe_route_gated(x.cuda(), wr.cuda(), None, 4, g, use_workspace=False)
+    assert torch.equal(a, ids) and torch.equal(b, w)
+    ws = torch.full((16 << 20,), 255, dtype=torch.uint8, device="cuda")
+    a, b = m.moe_route_gated(x.cuda(), wr.cuda(), None, 4, g, workspace=ws)
+    assert torch.equal(a, ids) and torch.equal(b, w)
+
+
 def test_streams_graphs_and_outputs():
     rng = np.random.default_rng(10)
     x, wr = _draw(rng, 300, 512, 64, "bf16")
