@@ -487,7 +487,7 @@ moe_status moe_route_gated(const moe_shape* shape, const moe_gate* gate, const v
  *     = T, row(r) = sorted_slots[r] / K; NULL: rows = T*K, row(r) = r.
  *   w_q, w_s, w2_q, w2_s  [E, f, d] tiled codes (moe_pack_rows) and [E, f] scales
  *     (w2_*: both NULL for the plain product).
- *   out [T*K, f] act_dtype, not overlapping any input; rows past off[E] are left untouched.
+ *   out [T*K, f] act_dtype, not overlapping any input (MOE_ERR_UNSUPPORTED); rows past off[E] are left untouched.
  * The sums are exact in int32; a sum becomes fp32 and takes its two scales there.
  * Any segment lengths. The schedules give the same bits. */
 moe_status moe_grouped_mm_int8(const moe_shape* shape, const int8_t* a_q, const float* a_s,
@@ -497,7 +497,8 @@ moe_status moe_grouped_mm_int8(const moe_shape* shape, const int8_t* a_q, const 
 /* The expert FFN with int8 weights AND activations, on the permuted rows: x is
  * quantized per token, gate/up with SwiGLU gives h (bf16), h is quantized per row
  * (moe_quantize_rows, fp32 scales), down gives y_rows. As moe_expert_ffn with int8
- * products (half as long at prefill) and the rounding of int8 activations.
+ * products (0.6 times as long at prefill) and the rounding of int8 activations. A
+ * token with an infinity or a NaN, in x or h, gives unspecified numbers.
  *   weight_fmt MOE_W_INT8; act_dtype is x's type;
  *   workspace >= moe_expert_ffn_int8_workspace_size bytes. */
 moe_status moe_expert_ffn_int8_workspace_size(const moe_shape* shape, size_t* bytes);

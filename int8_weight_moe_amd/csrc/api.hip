@@ -1415,6 +1415,24 @@ moe_status moe_grouped_mm_int8(const moe_shape* s, const int8_t* a_q, const floa
     REQUIRE_PTR(w2_s);
   }
   REQUIRE_PTR(out);
+  {
+    // workgroups read rows and matrices while others write out
+    const size_t rows = sorted_slots ? s->T : (size_t)s->T * s->K, mat = (size_t)s->E * s->f;
+    const size_t elem = s->act_dtype == MOE_BF16 ? 2 : 4, scale = s->scale_dtype == MOE_BF16 ? 2 : 4;
+    const struct {
+      const char* name;
+      const void* ptr;
+      size_t bytes;
+    } reads[] = {{"a_q", a_q, rows * s->d}, {"a_s", a_s, rows * 4}, {"w_q", w_q, mat * s->d}, {"w_s", w_s, mat * scale},
+                 {"w2_q", w2_q, mat * s->d}, {"w2_s", w2_s, mat * scale},
+                 {"expert_offsets", expert_offsets, (size_t)(s->E + 1) * 4},
+                 {"sorted_slots", sorted_slots, (size_t)s->T * s->K * 4}};
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), end = o + (size_t)s->T * s->K * s->f * elem;
+    for (const auto& r : reads) {
+      const uintptr_t u = reinterpret_cast<uintptr_t>(r.ptr);
+      if (r.ptr && u < end && o < u + r.bytes) return fail(MOE_ERR_UNSUPPORTED, "out overlaps %s", r.name);
+    }
+  }
   if (debug_on() && (st = debug_inputs(s, expert_offsets, sorted_slots, stream)) != MOE_OK) return st;
   moe::I8Args m;
   m.a = a_q;

@@ -219,7 +219,7 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
         const float wn = s.w_norm[e];
         delta[j] = units * kUnit * xn * wn;
         // norms that say nothing: past the fp32 range, or lost below it
-        if (!(delta[j] < INFINITY) || ((xn < 0x1p-45f || wn < 0x1p-45f) && l != 0)) delta[j] = INFINITY;
+        if (!(delta[j] < INFINITY) || xn < 0x1p-45f || wn < 0x1p-45f) delta[j] = INFINITY;
       }
       m = fmax(m, arg[j]);
       dmax = fmaxf(dmax, delta[j]);
@@ -482,10 +482,12 @@ __device__ __forceinline__ void choose_all(const GateArgs& a, const TokenState& 
   }
 }
 
-// Sum of a logit's parts, written with its bias; what is no number, or near the end of fp32's range, is left to fp64.
+// A logit's sum, written with its bias, once the norms are known. What is no number, or near the end of fp32's range, is
+// left to fp64; the zeros of a token or an expert of zeros (a padded batch) are exact as they are.
 __device__ __forceinline__ void put_logit(const GateArgs& a, const TokenState& s, int t, int e, double v) {
   s.logit[t * s.stride + e] = a.router_bias ? v + a.router_bias[e] : v;
   if (!(fabs(v) < 0x1p120)) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | e);
+  else if (v == 0 && (s.x_norm[t] == 0.f || s.w_norm[e] == 0.f)) atomicOr(&s.refined[t * 8 + (e >> 5)], 1u << (e & 31));
 }
 
 // ------------------------------------------------------------------ logits
@@ -778,8 +780,10 @@ __global__ __launch_bounds__(4 * kWave) void route_choose_kernel(GateArgs a, Spl
   if (threadIdx.x == 0) c.n_work = 0;
   __syncthreads();
   const TokenState s = {logit, c.x_norm, c.w_norm, &c.refined[0][0], work, &c.n_work, EP};
-  for (int e = threadIdx.x; e < a.E; e += kWaves * kWave) {
-    double v = 0;
+  static_assert(EP <= kWaves * kWave, "an expert a thread");
+  const int e = threadIdx.x;
+  double v = 0;
+  if (e < a.E) {
     float q = 0.f;
 #pragma unroll 8
     for (int k = 0; k < p.splits; ++k) {
@@ -787,7 +791,6 @@ __global__ __launch_bounds__(4 * kWave) void route_choose_kernel(GateArgs a, Spl
       q += p.w_sq[(long)k * a.E + e];
     }
     c.w_norm[e] = norm_of(q);
-    put_logit(a, s, 0, e, v);
   }
   if (threadIdx.x >= (kWaves - 1) * kWave) {
     float q = 0.f;
@@ -795,6 +798,8 @@ __global__ __launch_bounds__(4 * kWave) void route_choose_kernel(GateArgs a, Spl
     q = wave_sum(q);
     if ((threadIdx.x & 63) == 0) c.x_norm[0] = norm_of(q);
   }
+  __syncthreads();
+  if (e < a.E) put_logit(a, s, 0, e, v);
   __syncthreads();
   choose_all<Act, kWaves, 1, kSlots>(a, s, t, 1, kSumUnits<Act>);
 }

@@ -75,7 +75,8 @@ def test_route_gated_pointers(lib):
 
 
 def test_grouped_mm_int8(lib):
-    mm = lambda s, aq=A, asc=A, off=A, srt=A, w=A, ws=A, w2=None, w2s=None, out=A: lib.moe_grouped_mm_int8(
+    out_at = ctypes.c_void_p(1 << 40)
+    mm = lambda s, aq=A, asc=A, off=A, srt=A, w=A, ws=A, w2=None, w2s=None, out=out_at: lib.moe_grouped_mm_int8(
         s, aq, asc, off, srt, w, ws, w2, w2s, out, None)
     for fmt in (1, 2, 4):
         assert mm(_shape(weight_fmt=fmt)) == DTYPE
@@ -87,6 +88,12 @@ def test_grouped_mm_int8(lib):
     for kw in (dict(aq=MIS), dict(asc=MIS), dict(off=MIS), dict(srt=MIS), dict(w=MIS), dict(ws=MIS), dict(out=MIS),
                dict(w2=MIS, w2s=A), dict(w2=A, w2s=MIS)):
         assert mm(_shape(), **kw) == ALIGN, kw
+    # out [64, 512] bf16 may touch no input: rows [32, 256], matrices [16, 512, 256]
+    end = (1 << 40) + 64 * 512 * 2
+    P = ctypes.c_void_p
+    for kw in (dict(aq=P(end - 16)), dict(aq=P((1 << 40) - 32 * 256 + 16)), dict(asc=P(end - 16)), dict(w=P((1 << 40) - 16)),
+               dict(ws=out_at), dict(off=out_at), dict(srt=P(end - 256)), dict(w2=out_at, w2s=A), dict(w2=A, w2s=out_at)):
+        assert mm(_shape(), **kw) == UNSUPPORTED and b"overlaps" in lib.moe_last_error(), kw
     assert mm(_shape(T=0), None, None, None, None, None, None, None, None, None) == OK
 
 

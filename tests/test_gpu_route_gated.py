@@ -201,6 +201,22 @@ def test_a_token_does_not_depend_on_its_batch():
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("T,d,E,groups", [(1, 4096, 16, 1), (40, 8192, 64, 8), (700, 256, 60, 4), (4500, 128, 256, 8), (3, 8192, 256, 16)])
+def test_padded_batch(T, d, E, groups, act):
+    """Rows of zeros, of -0 and of the smallest numbers, and experts without weights: ties that the bias breaks, or the index."""
+    rng = np.random.default_rng(T)
+    x, wr = _draw(rng, T, d, E, act)
+    x[rng.random(T) < 0.7] = 0
+    x[T // 2] = -0.0
+    if T > 2:
+        x[1] = torch.finfo(x.dtype).smallest_normal
+    wr[E // 3] = 0
+    bias = np.where(rng.random(E) < 0.5, 0, 0.125 * rng.integers(-2, 3, E)).astype(np.float32)
+    for sigmoid, b, sel in itertools.product((False, True), (None, bias), (None, bias)):
+        _check(x, wr, b, 4, sel, "padded", sigmoid=sigmoid, groups=groups, group_topk=max(1, groups // 2), top2=True)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("T,d,E", [(1, 8192, 16), (5, 8192, 30), (17, 2048, 64), (33, 1088, 100), (64, 832, 250), (1024, 4096, 64),
                                    (100, 576, 256)])
 def test_with_and_without_a_workspace(T, d, E, act):
