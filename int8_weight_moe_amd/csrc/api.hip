@@ -712,7 +712,7 @@ moe_status scratch_on_current_device(void** out) {
 }
 
 // moe_forward_gated's workspace: moe_forward's, then moe_route_gated's, then with int8 activations
-// moe_expert_ffn_int8's but h.
+// moe_expert_ffn_int8's but h. Without a gate moe_forward's alone.
 size_t gated_ffn_at(const moe_shape* s) { return round_up(forward_layout(s).total) + round_up(route_gated_ws_bytes(s)); }
 size_t gated_ws_bytes(const moe_shape* s, int32_t expert_act) {
   return gated_ffn_at(s) + (expert_act == MOE_ACT_INT8 ? i8_ffn_layout(s, false).total : 0);
@@ -842,7 +842,7 @@ moe_status block_impl(const char* call, const moe_shape* s, const moe_gate* gate
     return fail(x ? MOE_ERR_UNSUPPORTED : MOE_ERR_NULL, "exactly one of x and pre_weight is given");
   if (!aligned16(pre_weight)) return fail(MOE_ERR_ALIGN, "pre_weight is not 16-byte aligned");
   REQUIRE_PTR(workspace);
-  const size_t fwd = round_up(gated_ws_bytes(s, expert_act)), need = fwd + block_x_bytes(s);
+  const size_t fwd = round_up(gate ? gated_ws_bytes(s, expert_act) : forward_layout(s).total), need = fwd + block_x_bytes(s);
   if (workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", workspace_bytes, need);
   // everything forward_impl checks, before the first launch

@@ -194,6 +194,24 @@ def test_block_forward_gated(lib):
     assert call(_shape(T=0)) == OK
 
 
+@pytest.mark.parametrize("T,d", [(3, 8192), (32, 256), (1024, 8192), (2000, 8192)])
+def test_blocks_ask_for_the_workspace_they_name(lib, T, d):
+    """moe_block_forward asks for moe_block_workspace_size whatever gated routing would split."""
+    post = _lib.MoePost(None, None, None, 1, 1.0, 1.0, 1e-6, 1e-6)
+    s = _shape(T=T, d=d)
+    n, g = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    assert lib.moe_block_workspace_size(s, ctypes.byref(n)) == OK
+    far = [ctypes.c_void_p((1 + i) << 40) for i in range(3)]
+    call = lambda b: lib.moe_block_forward(s, far[0], A, 1e-6, None, ctypes.byref(post), *[A] * 2, *[A] * 6, far[1], None, None, None,
+                                           A, ctypes.c_size_t(b), None)
+    assert call(n.value - 1) == WORKSPACE
+    assert f"required {n.value}".encode() in lib.moe_last_error()
+    assert lib.moe_block_gated_workspace_size(s, 0, ctypes.byref(g)) == OK
+    r = ctypes.c_size_t(0)
+    assert lib.moe_route_gated_workspace_size(s, ctypes.byref(r)) == OK
+    assert n.value + r.value <= g.value <= n.value + r.value + 1024
+
+
 def test_binding_of_the_layer():
     from tests.test_binding_mxfp4 import D, E, _experts
     x, wr = torch.zeros(4, D, dtype=torch.bfloat16), torch.zeros(E, D, dtype=torch.bfloat16)

@@ -93,6 +93,26 @@ def test_block_is_its_staged_calls(act_int8):
         assert o2 is stream and torch.equal(o2, r2)
 
 
+def test_blocks_of_long_rows():
+    """Rows that gated routing splits over workgroups: the plain block takes the workspace it names, and both are their
+    staged calls."""
+    x, wr, ex, _, _ = _case(3, 8192, 64, 4)
+    v = torch.ones(8192, dtype=torch.bfloat16, device="cuda")
+    n = m.moe_norm_pre(x, v)
+    for gate in (None, m.Gate()):
+        kw = dict(pre_weight=v, weight=v, residual_scale=0.5)
+        if gate is None:
+            out, _, ids, w = m.moe_block_forward(x, wr, None, ex, 2, **kw)
+            rid, rw = m.moe_route(n, wr, None, 2)
+        else:
+            out, _, ids, w = m.moe_block_forward_gated(x, wr, None, ex, 2, gate, **kw)
+            rid, rw = m.moe_route_gated(n, wr, None, 2, gate)
+        assert torch.equal(ids, rid) and torch.equal(w, rw)
+        off, slots, s2r = m.moe_permute(rid, 4)
+        rows = m.moe_expert_ffn(n, off, slots, ex, 2)
+        assert torch.equal(out, m.moe_combine_post(rows, s2r, rw, x, weight=v, residual_scale=0.5)[0])
+
+
 @pytest.mark.parametrize("T,d,f,E,K", [(5, 192, 256, 8, 2), (120, 320, 448, 12, 3)])
 def test_each_stage_against_the_oracle(T, d, f, E, K):
     """Routing, permutation, the tokens' codes, gate/up, h's codes, down and combine, as moe_expert_ffn_int8 chains them."""
