@@ -305,7 +305,8 @@ class Gate:
 
 class MoeLayer:
     """A resident MoE layer: router weights, int8 experts and a reusable workspace. With a gate the tokens are
-    routed by it, and with act_int8 the experts' products take int8 activations (moe_forward_gated)."""
+    routed by it, and with act_int8 the experts' products take int8 activations (moe_forward_gated). A forward captured
+    into a graph has a workspace of its own in the graph's memory: graphs neither share one nor lose it to a larger batch."""
 
     def __init__(self, router_w: torch.Tensor, bias: Optional[torch.Tensor], experts: Int8Experts, K: int,
                  gate: Optional[Gate] = None, act_int8: bool = False):
@@ -325,11 +326,11 @@ class MoeLayer:
 
     def forward(self, x: torch.Tensor, path: int = MOE_PATH_AUTO, y: Optional[torch.Tensor] = None,
                 ids: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None):
+        ws = None if torch.cuda.is_current_stream_capturing() else self.workspace(self.shape(x, path))
         if self.gate is not None:
             return moe_forward_gated(x, self.router_w, self.bias, self.experts, self.K, self.gate, self.act_int8,
-                                     path=path, y=y, ids=ids, w=w, workspace=self.workspace(self.shape(x, path)))
-        return moe_forward(x, self.router_w, self.bias, self.experts, self.K, path=path, y=y, ids=ids, w=w,
-                           workspace=self.workspace(self.shape(x, path)))
+                                     path=path, y=y, ids=ids, w=w, workspace=ws)
+        return moe_forward(x, self.router_w, self.bias, self.experts, self.K, path=path, y=y, ids=ids, w=w, workspace=ws)
 
     def shape(self, x: torch.Tensor, path: int = MOE_PATH_AUTO) -> MoeShape:
         e = self.experts

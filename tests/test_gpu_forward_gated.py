@@ -187,6 +187,35 @@ def test_layer_object_graph_streams_and_debug(monkeypatch):
         m.moe_permute(ids, 16)
 
 
+@pytest.mark.parametrize("gate", [None, m.Gate()])
+def test_a_layer_captured_twice_then_grown(gate):
+    """Two graphs of one layer replayed on two streams, and a larger batch between: no workspace is shared or lost."""
+    x, wr, ex, _, _ = _case(900, 256, 384, 8)
+    layer = m.MoeLayer(wr, None, ex, 2, gate=gate, act_int8=gate is not None)
+    want = [layer.forward(x[a:a + 40].contiguous())[0].clone() for a in (0, 100)]
+    graphs, outs, ins = [], [], []
+    for a in (0, 100):
+        ins.append(x[a:a + 40].contiguous())
+        outs.append(torch.empty_like(ins[-1]))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            layer.forward(ins[-1], y=outs[-1])
+    small = layer._ws.numel()
+    big = layer.forward(x)[0].clone()
+    assert layer._ws.numel() > small
+    other = [torch.full((small,), 7, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, v) for o, v in zip(outs, want))
+        assert all((o == 7).all() for o in other)
+        assert torch.equal(layer.forward(x)[0], big)
+
+
 def test_schedule_lines(monkeypatch, capfd):
     monkeypatch.setenv("MOE_LOG", "1")
     x, wr, ex, b, _ = _case(600, 256, 4096, 4)
