@@ -238,7 +238,7 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
 #pragma unroll
     for (int j = 0; j < kSlots; ++j)
       if (id[j] >= 0) {
-        arg[j] -= m;
+        arg[j] = (Real)(logit[id[j] & 0xffff] - (double)m);   // before it is rounded: the difference may be far smaller
         c[j] = exp_of(arg[j]);
         z += c[j];
       }

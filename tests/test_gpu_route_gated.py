@@ -117,6 +117,20 @@ def test_values_closer_than_fp32_sums(E, groups, act):
                top2=True)
 
 
+@pytest.mark.parametrize("E,groups,K", [(2, 1, 1), (16, 1, 3), (64, 8, 4), (256, 8, 8)])
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_a_bias_against_logits_finer_than_fp32(E, groups, K, sigmoid):
+    """Logits about 1000 that differ by less than fp32 holds there (6e-5), and biases of the same size as the scores'
+    differences: the scores have to come from the 64-bit logits."""
+    rng = np.random.default_rng(E + K)
+    T, d = 64, 64
+    x, wr = np.zeros((T, d), np.float32), np.zeros((E, d), np.float32)
+    x[:, 0], x[:, 1:9] = 1000, rng.standard_normal((T, 8))
+    wr[:, 0], wr[:, 1:9] = 0 if sigmoid else 1, 2e-5 * rng.standard_normal((E, 8))
+    _check(torch.from_numpy(x), torch.from_numpy(wr), None, K, select=(1e-5 / (4 if sigmoid else E) * rng.standard_normal(E)).astype(np.float32),
+           what="fine bias", sigmoid=sigmoid, groups=groups, group_topk=max(1, groups // 2), top2=groups > 1)
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("E,groups", [(8, 1), (40, 4), (256, 16)])
 def test_exact_ties_go_to_the_lower_index(E, groups, act):
