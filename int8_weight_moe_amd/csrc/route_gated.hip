@@ -388,7 +388,7 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
     above = wave_max(above);
     for (int k = a.K - 1; k >= 0; --k) {
       const Real lo = lane_value(my_lo, k), hi = lane_value(my_hi, k);
-      if (lo > kNone && !(lo > above)) {
+      if (lane_value(my_id, k) >= 0 && !(lo > above)) {   // lo: -inf where the error says nothing
         // it, and what may lie above its lower end
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)

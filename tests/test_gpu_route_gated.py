@@ -118,6 +118,21 @@ def test_values_closer_than_fp32_sums(E, groups, act):
 
 
 @pytest.mark.parametrize("E,groups,K", [(2, 1, 1), (16, 1, 3), (64, 8, 4), (256, 8, 8)])
+@pytest.mark.parametrize("base", [700.0, 3000.0])
+def test_logits_whose_fp32_sums_are_off_by_more_than_one(E, groups, K, base):
+    """Logits of 5e5 and 9e6 that differ by one or two: an fp32 sum's error there, 0.5 to 8, says nothing about a score."""
+    rng = np.random.default_rng(E + K)
+    T, d = 64, 128
+    x, wr = np.zeros((T, d), np.float32), np.zeros((E, d), np.float32)
+    x[:, 0], x[:, 1:17] = base, rng.standard_normal((T, 16))
+    wr[:, 0], wr[:, 1:17] = base, 0.3 * rng.standard_normal((E, 16))
+    _check(torch.from_numpy(x), torch.from_numpy(wr), None, K, what="coarse sums", groups=groups, group_topk=max(1, groups // 2),
+           top2=groups > 1)
+    _check(torch.from_numpy(x), torch.from_numpy(wr), None, K, select=(0.1 / E * rng.standard_normal(E)).astype(np.float32),
+           what="coarse sums", groups=groups, group_topk=max(1, groups // 2), top2=groups > 1)
+
+
+@pytest.mark.parametrize("E,groups,K", [(2, 1, 1), (16, 1, 3), (64, 8, 4), (256, 8, 8)])
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_a_bias_against_logits_finer_than_fp32(E, groups, K, sigmoid):
     """Logits about 1000 that differ by less than fp32 holds there (6e-5), and biases of the same size as the scores'
