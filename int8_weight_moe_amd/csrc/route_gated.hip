@@ -20,6 +20,12 @@
 // are marked, the workgroup's waves compute their logits again in fp64, and the choice is
 // repeated, in fp64 if it then hangs on the fp32 evaluation alone. So the ids are
 // those of 64-bit values, at the price of fp32 ones.
+//
+// What bounds it: 16 experts, the reads of x (16384 x 8192 bf16 in 60 us, 4.5 TB/s of a copy's 4.8). 256 experts (8192 x
+// 4096, 79 us): 50 us of logits, whose rows pass through LDS at 20 bytes a cycle and CU (nothing but the loads takes as
+// long), then 14 us of choosing, 1000 instructions a token at four waves a SIMD, and 15 us for the tokens of each workgroup
+// that are refined and chosen again. fp32 (2999 x 4096, 60 experts, 52 us): 41 us of logits, 16 of them the fp32
+// MFMAs'. One token is 7.5 us of latency: rows to LDS, sums, choice.
 #include "device_common.h"
 #include "kernels.h"
 
@@ -70,6 +76,19 @@ __device__ __forceinline__ Real wave_sum(Real v) {
   for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
   return v;
 }
+// The largest value of the lanes after this one, in lanes 0 .. 7 and of theirs.
+__device__ __forceinline__ float after(float v) {
+  v = dpp_or<0x101, 0xf>(v, -INFINITY);              // from the next lane of the row of 16
+  v = fmaxf(v, dpp_or<0x101, 0xf>(v, -INFINITY));
+  v = fmaxf(v, dpp_or<0x102, 0xf>(v, -INFINITY));
+  return fmaxf(v, dpp_or<0x104, 0xf>(v, -INFINITY));
+}
+__device__ __forceinline__ double after(double v) {
+  v = __shfl_down(v, 1);
+#pragma unroll
+  for (int off = 1; off <= 4; off <<= 1) v = fmax(v, __shfl_down(v, off));
+  return v;
+}
 __device__ __forceinline__ int wave_min(int v) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) v = min(v, __shfl_xor(v, off));
@@ -110,8 +129,11 @@ __device__ __forceinline__ double dot64(const Act* __restrict__ a, const Act* __
   return wave_sum(s);
 }
 
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+// The fp32 forms are the hardware's: one unit each, the exponential's with its argument's two roundings.
+__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
+__device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }
+__device__ __forceinline__ double inverse(double v) { return 1 / v; }
 
 // A lane's value, in every lane (lane: the same in all of them).
 __device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
@@ -150,9 +172,12 @@ struct TokenState {
   double* logit;       // [tokens][stride]
   float* x_norm;       // [tokens]  |x|, rounded up
   float* w_norm;       // [stride]  |w_e|, rounded up
+  float* bias;         // [stride]  select_bias, or 0
   uint32_t* refined;   // [tokens][8] bit e: the logit is a 64-bit one
   uint16_t* work;      // (token << 8 | expert) to refine
   int* n_work;
+  int16_t* chosen;     // [tokens][8]
+  double *top, *sum;   // [tokens]  what a softmax's exponentials are taken less of, and their sum where the weights need it
   int stride;
 };
 
@@ -169,26 +194,80 @@ struct ChoiceMap {
   }
 };
 
-// Compare and exchange: the larger value first, of equal ones the lower id.
+// Compare and exchange: the larger value first, of equal ones the lower id (in fp32 equal values decide nothing: their
+// intervals overlap).
 template <typename Real>
 __device__ __forceinline__ void order(Real& v0, Real& e0, int& i0, Real& v1, Real& e1, int& i1) {
-  const bool swap = v1 > v0 || (v1 == v0 && (i1 & 0xffff) < (i0 & 0xffff));
-  const Real v = v0, e = e0;
+  const bool swap = v1 > v0 || (sizeof(Real) == 8 && v1 == v0 && (i1 & 0xffff) < (i0 & 0xffff));
+  const Real e = e0;
   const int i = i0;
-  v0 = swap ? v1 : v0;
+  const Real least = fmin(v0, v1);
+  v0 = fmax(v0, v1);
+  v1 = least;
   e0 = swap ? e1 : e0;
   i0 = swap ? i1 : i0;
-  v1 = swap ? v : v1;
   e1 = swap ? e : e1;
   i1 = swap ? i : i1;
 }
 
+// A lane's slots in descending order, by exchanges of slots (i, j) that leave the larger in i (an odd-even merge sort).
+template <int kSlots, typename Exchange>
+__device__ __forceinline__ void sort_slots(Exchange exchange) {
+  if constexpr (kSlots == 2) exchange(0, 1);
+  if constexpr (kSlots >= 4) {
+#pragma unroll
+    for (int h = 0; h < kSlots; h += 4) {
+      exchange(h, h + 1);
+      exchange(h + 2, h + 3);
+      exchange(h, h + 2);
+      exchange(h + 1, h + 3);
+      exchange(h + 1, h + 2);
+    }
+  }
+  if constexpr (kSlots == 8) {
+    exchange(0, 4);
+    exchange(1, 5);
+    exchange(2, 6);
+    exchange(3, 7);
+    exchange(2, 4);
+    exchange(3, 5);
+    exchange(1, 2);
+    exchange(3, 4);
+    exchange(5, 6);
+  }
+}
+
+// Groups that rank before this lane's, whose value is val.
+template <typename Real>
+__device__ __forceinline__ int groups_before(const GateArgs& a, const ChoiceMap& map, Real val) {
+  int before = 0;
+  for (int g = 0; g < a.groups; ++g) {
+    const Real o = lane_value(val, g * map.lanes);
+    before += o > val || (o == val && g < map.group);
+  }
+  return before;
+}
+
+// Token t's choice stands: lane k has its k-th expert, or -1.
+template <typename Real>
+__device__ __forceinline__ void taken(const GateArgs& a, const TokenState& s, int t, int my_id, Real m) {
+  const int lane = threadIdx.x & 63;
+  if (lane < 8) s.chosen[t * 8 + lane] = (int16_t)my_id;
+  if (a.sigmoid) return;
+  if (lane == 0) s.top[t] = m;
+  if (a.renorm) return;
+  double sum = 0;
+  for (int e = lane; e < a.E; e += kWave) sum += exp(s.logit[t * s.stride + e] - m);
+  sum = wave_sum(sum);
+  if (lane == 0) s.sum[t] = sum;
+}
+
 enum Choice { kTaken, kRefine, kInDouble };
 
-// One token's choice by one wave, in fp32 or fp64: taken (and written); or the experts whose logits it hangs on are
+// One token's choice by one wave, in fp32 or fp64: taken (into s.chosen); or the experts whose logits it hangs on are
 // appended to the work; or (fp32) it hangs on the rounding of refined ones, or on values past the range.
 template <typename Real, int kSlots>
-__device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s, int t, int32_t* ids, float* w, float units) {
+__device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s, int t, float units) {
   constexpr bool kDouble = sizeof(Real) == 8;
   constexpr Real kNone = -INFINITY;
   constexpr int kOpen = 1 << 16, kMark = 1 << 17;   // beside an expert's id: not refined; the choice hangs on its logit
@@ -244,12 +323,13 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
       }
     z = wave_sum(z);
   }
+  const Real inv_z = kDouble ? z : inverse(z);
 #pragma unroll
   for (int j = 0; j < kSlots; ++j) {
     Real v = kNone, err = 0;
     if (id[j] >= 0) {
-      const Real score = a.sigmoid ? 1 / (1 + exp_of(-arg[j])) : c[j] / z;
-      const Real b = a.select_bias ? (Real)a.select_bias[id[j] & 0xffff] : (Real)0;
+      const Real score = a.sigmoid ? inverse(1 + exp_of(-arg[j])) : kDouble ? c[j] / z : c[j] * inv_z;
+      const Real b = s.bias[id[j] & 0xffff];
       v = score + b;
       // the score's change with its logit: s (1 - s), or s; exp(x) - 1 <= 1.3 x up to 0.5
       const Real part = a.sigmoid ? score * (1 - score) : score;
@@ -257,10 +337,11 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
       if (all) err += fabs(b) * (Real)(1.3f * dmax);
       if (!(delta[j] <= 0.5f) || (all && !(dmax <= 0.5f))) err = INFINITY;
       if constexpr (!kDouble) {
-        // The exponential (one unit; OCML), its argument's rounding, 1 + it and the division, the sum with b; a
-        // softmax's sum of up to eight and six additions matters next to a bias, as above.
-        const float own = 2 + fabsf(arg[j]);
-        err += kUnit * (score * (a.sigmoid ? (1 - score) * own + 3 : own + 2) + fabsf(b) * (all ? 17 : 1));
+        // The exponential (one unit) and its argument's roundings (to fp32, of log2(e), of the product); 1 + it and the
+        // inverse, or the product with one; the sum with b; a softmax's sum of up to eight and six additions matters
+        // next to a bias, as above.
+        const float own = 2 + 2 * fabsf(arg[j]);
+        err += kUnit * (score * (a.sigmoid ? (1 - score) * own + 3 : own + 4) + fabsf(b) * (all ? 17 : 1));
         err = fmaxf(err, 0x1p-120f);           // scores lost below the fp32 range
       }
       if (!(v > kNone)) v = kNone;
@@ -270,6 +351,7 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
     eps[j] = err;
   }
 
+  bool hangs = false;   // experts may be marked
   // what a refined logit leaves open: in fp32 the evaluation, in fp64 a softmax's sum next to a bias
   auto unsure = [&](int i) { return i >= 0 && (!kDouble || (i & kOpen) || (all && dmax > 0.f)); };
   if (a.groups > 1) {
@@ -301,16 +383,13 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
       hi = val + (a.top2 ? 2 * e : e);
       least = (a.top2 ? vc.second : vc.first) - e;
     }
-    int before = 0;
-    for (int g = 0; g < a.groups; ++g) {
-      const Real o = lane_value(val, g * map.lanes);
-      before += o > val || (o == val && g < map.group);
-    }
+    const int before = groups_before(a, map, val);
     const bool real = map.group < a.groups, kept = real && before < a.group_topk;
     if (a.group_topk < a.groups) {
       const Real floor = -wave_max(kept ? -lo : kNone);      // least value of a kept group
       const Real ceil = wave_max(real && !kept ? hi : kNone);
       if (!(floor > ceil)) {
+        hangs = true;
         const bool near = kept ? !(lo > ceil) : real && !(hi < floor);
 #pragma unroll
         for (int j = 0; j < kSlots; ++j)
@@ -325,30 +404,8 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
       }
   }
 
-  // a lane's experts in descending order (an odd-even merge sort's exchanges)
-  auto exchange = [&](int i, int j) { order(c[i], eps[i], id[i], c[j], eps[j], id[j]); };
-  if constexpr (kSlots == 2) exchange(0, 1);
-  if constexpr (kSlots >= 4) {
-#pragma unroll
-    for (int h = 0; h < kSlots; h += 4) {
-      exchange(h, h + 1);
-      exchange(h + 2, h + 3);
-      exchange(h, h + 2);
-      exchange(h + 1, h + 3);
-      exchange(h + 1, h + 2);
-    }
-  }
-  if constexpr (kSlots == 8) {
-    exchange(0, 4);
-    exchange(1, 5);
-    exchange(2, 6);
-    exchange(3, 7);
-    exchange(2, 4);
-    exchange(3, 5);
-    exchange(1, 2);
-    exchange(3, 4);
-    exchange(5, 6);
-  }
+  // a lane's experts in descending order
+  sort_slots<kSlots>([&](int i, int j) { order(c[i], eps[i], id[i], c[j], eps[j], id[j]); });
   // K rounds: the largest of the lanes' first ones, which its lane then drops; lane k keeps round k's
   int my_id = -1;
   Real my_lo = kNone, my_hi = kNone;
@@ -357,7 +414,7 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
     if (!(top > kNone)) break;
     const uint64_t equal = __ballot(c[0] == top);
     int owner = __ffsll((unsigned long long)equal) - 1;
-    if (__popcll(equal) > 1) {
+    if (kDouble && __popcll(equal) > 1) {
       const int e = c[0] == top ? id[0] & 0xffff : kMaxExperts;
       owner = __ffsll((unsigned long long)__ballot(e == wave_min(e))) - 1;
     }
@@ -380,63 +437,70 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
       id[kSlots - 1] = -1;
     }
   }
-  {
-    // every pick lies above all that rank after it
-    Real above = kNone;
+  // every pick has to lie above all that rank after it
+  Real above = kNone;
 #pragma unroll
-    for (int j = 0; j < kSlots; ++j) above = fmax(above, c[j] + eps[j]);
-    above = wave_max(above);
-    for (int k = a.K - 1; k >= 0; --k) {
-      const Real lo = lane_value(my_lo, k), hi = lane_value(my_hi, k);
-      if (lane_value(my_id, k) >= 0 && !(lo > above)) {   // lo: -inf where the error says nothing
-        // it, and what may lie above its lower end
+  for (int j = 0; j < kSlots; ++j) above = fmax(above, c[j] + eps[j]);
+  above = fmax(wave_max(above), after(my_hi));
+  const uint64_t bad = __ballot(my_id >= 0 && !(my_lo > above));
+  if (bad) {
+    // such picks, and what ranks after the first of them and may lie above the lowest of their lower ends
+    const Real lo = -wave_max(bad >> lane & 1 ? -my_lo : kNone);
+    hangs = true;
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j)
-          if (unsure(id[j]) && c[j] > kNone && !(c[j] + eps[j] < lo)) id[j] |= kMark;
-        if (lane >= k && unsure(my_id) && (lane == k || !(my_hi < lo))) my_id |= kMark;
-      }
-      above = fmax(above, hi);
+    for (int j = 0; j < kSlots; ++j)
+      if (unsure(id[j]) && c[j] > kNone && !(c[j] + eps[j] < lo)) id[j] |= kMark;
+    if (lane >= __ffsll((unsigned long long)bad) - 1 && unsure(my_id) && !(my_hi < lo)) my_id |= kMark;
+  }
+  if (hangs) {
+    bool on_open = my_id >= 0 && (my_id & kMark) && (my_id & kOpen), marked = my_id >= 0 && (my_id & kMark);
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) {
+      const bool mark = id[j] >= 0 && (id[j] & kMark);
+      marked = marked || mark;
+      on_open = on_open || (mark && (id[j] & kOpen));
+    }
+    if (__any(marked)) {
+      const bool some = __any(on_open);
+      if (!kDouble && !some) return kInDouble;
+      // the marked ones; if these are refined, every logit of the sum
+      auto append = [&](int i) {
+        if (i >= 0 && (i & kOpen) && (!some || (i & kMark))) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | (i & 0xff));
+      };
+      append(my_id);
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) append(id[j]);
+      return kRefine;
     }
   }
-  bool hangs = my_id >= 0 && (my_id & kMark), on_open = hangs && (my_id & kOpen);
-#pragma unroll
-  for (int j = 0; j < kSlots; ++j) {
-    const bool mark = id[j] >= 0 && (id[j] & kMark);
-    hangs = hangs || mark;
-    on_open = on_open || (mark && (id[j] & kOpen));
-  }
-  if (__any(hangs)) {
-    const bool some = __any(on_open);
-    if (!kDouble && !some) return kInDouble;
-    // the marked ones; if these are refined, every logit of the sum
-    auto append = [&](int i) {
-      if (i >= 0 && (i & kOpen) && (!some || (i & kMark))) s.work[atomicAdd(s.n_work, 1)] = (uint16_t)(t << 8 | (i & 0xff));
-    };
-    append(my_id);
-#pragma unroll
-    for (int j = 0; j < kSlots; ++j) append(id[j]);
-    return kRefine;
-  }
 
-  // weights, in fp64 from the logits of the chosen (lanes 0 .. 7)
-  if (my_id >= 0) my_id &= 0xffff;
-  double sk = 0;
-  if (my_id >= 0) sk = a.sigmoid ? 1 / (1 + exp(-logit[my_id])) : exp(logit[my_id] - m);
-  double total = 1;
-  if (a.renorm) {
-    total = sk;
-#pragma unroll
-    for (int off = 4; off >= 1; off >>= 1) total += __shfl_xor(total, off);
-  } else if (!a.sigmoid) {
-    total = 0;
-    for (int e = lane; e < a.E; e += kWave) total += exp(logit[e] - m);
-    total = wave_sum(total);
-  }
-  if (lane < a.K) {
-    ids[lane] = my_id;
-    w[lane] = total > 0 ? (float)(sk / total * a.scale) : 0.f;
-  }
+  taken(a, s, t, my_id >= 0 ? my_id & 0xffff : -1, m);
   return kTaken;
+}
+
+// Ids and weights of the workgroup's n tokens once all are chosen, in fp64 from the logits of the chosen: a thread each
+// (by each token's own wave: 66.0 -> 64.3 us with the hardware's exponentials above, 16384 tokens, 16 experts).
+__device__ __forceinline__ void write_chosen(const GateArgs& a, const TokenState& s, int tok0, int n) {
+  for (int i = threadIdx.x; i < 8 * n; i += blockDim.x) {
+    const int t = i >> 3, k = i & 7;
+    const int id = k < a.K ? s.chosen[i] : -1;
+    double sk = 0;
+    if (id >= 0) {
+      const double l = s.logit[t * s.stride + id];
+      sk = a.sigmoid ? 1 / (1 + exp(-l)) : exp(l - s.top[t]);
+    }
+    double total = a.sigmoid ? 1 : s.sum[t];
+    if (a.renorm) {
+      total = sk;
+#pragma unroll
+      for (int off = 4; off >= 1; off >>= 1) total += __shfl_xor(total, off);
+    }
+    if (k < a.K) {
+      const long at = (long)(tok0 + t) * a.K + k;
+      a.topk_ids[at] = id;
+      a.topk_w[at] = total > 0 ? (float)(sk / total * a.scale) : 0.f;
+    }
+  }
 }
 
 // The choice of the workgroup's tokens (kTok of them at most, n present) once their logits lie in LDS. All waves call
@@ -471,15 +535,14 @@ __device__ __forceinline__ void choose_all(const GateArgs& a, const TokenState& 
     for (int i = 0; i < kMine; ++i) {
       if (!(pending >> i & 1)) continue;
       const int t = wave + kWaves * i;
-      int32_t* ids = a.topk_ids + (long)(tok0 + t) * a.K;
-      float* w = a.topk_w + (long)(tok0 + t) * a.K;
-      Choice c = choose<float, kSlots>(a, s, t, ids, w, units);
-      if (c == kInDouble) c = choose<double, kSlots>(a, s, t, ids, w, units);
+      Choice c = choose<float, kSlots>(a, s, t, units);
+      if (c == kInDouble) c = choose<double, kSlots>(a, s, t, units);
       if (c == kTaken) pending &= ~(1u << i);
     }
     __syncthreads();
     if (*s.n_work == 0) break;   // a token that is not taken has added to it
   }
+  write_chosen(a, s, tok0, n);
 }
 
 // A logit's sum, written with its bias, once the norms are known. What is no number, or near the end of fp32's range, is
@@ -680,9 +743,11 @@ __device__ __forceinline__ void tile_logits(const GateArgs& a, int tok0, int n, 
 // What a workgroup's choice needs besides the logits.
 template <int TOK, int EP>
 struct ChoiceLds {
-  float x_norm[TOK], w_norm[EP];
+  double top[TOK], sum[TOK];
+  float x_norm[TOK], w_norm[EP], bias[EP];
   uint32_t refined[TOK][8];
   int n_work;
+  int16_t chosen[TOK * 8];
 };
 
 // Logits and choice of 16*TB tokens in one workgroup.
@@ -698,6 +763,7 @@ __global__ __launch_bounds__(kWaves* kWave, 4) void route_gated_kernel(GateArgs 
   const int blocks = (int)((long)a.d * sizeof(Act) / kBlockBytes);
   if (threadIdx.x < TOK * 8) (&c.refined[0][0])[threadIdx.x] = 0;
   if (threadIdx.x == 0) c.n_work = 0;
+  if (threadIdx.x < a.E) c.bias[threadIdx.x] = a.select_bias ? a.select_bias[threadIdx.x] : 0.f;
   tile_logits<Act, NEB, TB, kWaves, D>(a, tok0, n, 0, (blocks + KS - 1) / KS, lds, x_sq, w_sq);
 
   // the slices' sums, each thread's before any is overwritten
@@ -719,8 +785,8 @@ __global__ __launch_bounds__(kWaves* kWave, 4) void route_gated_kernel(GateArgs 
     else c.w_norm[i - TOK] = norm_of(q);
   }
   __syncthreads();
-  const TokenState s = {reinterpret_cast<double*>(lds), c.x_norm, c.w_norm, &c.refined[0][0],
-                        reinterpret_cast<uint16_t*>(lds + TOK * EP * 8), &c.n_work, EP};
+  const TokenState s = {reinterpret_cast<double*>(lds), c.x_norm, c.w_norm, c.bias, &c.refined[0][0],
+                        reinterpret_cast<uint16_t*>(lds + TOK * EP * 8), &c.n_work, c.chosen, c.top, c.sum, EP};
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int at = threadIdx.x + i * kWaves * kWave, t = at / EP, e = at % EP;
@@ -779,7 +845,7 @@ __global__ __launch_bounds__(4 * kWave) void route_choose_kernel(GateArgs a, Spl
   if (threadIdx.x < 8) c.refined[0][threadIdx.x] = 0;
   if (threadIdx.x == 0) c.n_work = 0;
   __syncthreads();
-  const TokenState s = {logit, c.x_norm, c.w_norm, &c.refined[0][0], work, &c.n_work, EP};
+  const TokenState s = {logit, c.x_norm, c.w_norm, c.bias, &c.refined[0][0], work, &c.n_work, c.chosen, c.top, c.sum, EP};
   static_assert(EP <= kWaves * kWave, "an expert a thread");
   const int e = threadIdx.x;
   double v = 0;
@@ -791,6 +857,7 @@ __global__ __launch_bounds__(4 * kWave) void route_choose_kernel(GateArgs a, Spl
       q += p.w_sq[(long)k * a.E + e];
     }
     c.w_norm[e] = norm_of(q);
+    c.bias[e] = a.select_bias ? a.select_bias[e] : 0.f;
   }
   if (threadIdx.x >= (kWaves - 1) * kWave) {
     float q = 0.f;
