@@ -14,7 +14,7 @@
 // reduction is cut into KS slices, streamed by the KS waves of a workgroup and
 // added through LDS (integers: exact in any order).
 // Bound by HBM: gate/up of one token (d 4096, f 14336, two experts) 39 us, 6.0
-// TB/s; down of 64 tokens (d 24576, f 8192, E 16) 506 us, 6.4 TB/s.
+// TB/s; down of 64 tokens (d 24576, f 8192, E 16) 490 us, 6.6 TB/s.
 #include "i8_common.h"
 #include "kernels.h"
 
