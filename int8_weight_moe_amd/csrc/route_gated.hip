@@ -340,7 +340,7 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
         // The exponential (one unit) and its argument's roundings (to fp32, of log2(e), of the product); 1 + it and the
         // inverse, or the product with one; the sum with b; a softmax's sum of up to eight and six additions matters
         // next to a bias, as above.
-        const float own = 2 + 2 * fabsf(arg[j]);
+        const float own = 2 + 2 * fminf(fabsf(arg[j]), 200.f);   // past it the score is 0 or 1, and 0 * infinity no number
         err += kUnit * (score * (a.sigmoid ? (1 - score) * own + 3 : own + 4) + fabsf(b) * (all ? 17 : 1));
         err = fmaxf(err, 0x1p-120f);           // scores lost below the fp32 range
       }

@@ -132,6 +132,19 @@ def test_logits_whose_fp32_sums_are_off_by_more_than_one(E, groups, K, base):
            what="coarse sums", groups=groups, group_topk=max(1, groups // 2), top2=groups > 1)
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_a_bias_against_a_score_step_by_step(sigmoid):
+    """An expert without a score (a router bias of -inf) whose bias is another one's score but for a few units of fp32, up
+    and down over the tokens."""
+    T, d, E = 4096, 64, 3
+    x, wr = np.zeros((T, d), np.float32), np.zeros((E, d), np.float32)
+    x[:, 0], x[:, 1] = 1, (np.arange(T) - T / 2) * 2.0 ** -32
+    wr[0, :2] = 0.75, 1
+    score = 1 / (1 + np.exp(-0.75))
+    _check(torch.from_numpy(x), torch.from_numpy(wr), np.array([0, 0, -INF], np.float32), 1,
+           select=np.array([0, -1, score], np.float32), what="steps", sigmoid=sigmoid)
+
+
 @pytest.mark.parametrize("E,groups,K", [(2, 1, 1), (16, 1, 3), (64, 8, 4), (256, 8, 8)])
 @pytest.mark.parametrize("sigmoid", [False, True])
 def test_a_bias_against_logits_finer_than_fp32(E, groups, K, sigmoid):
