@@ -915,7 +915,9 @@ void launch_experts(const GateArgs& a, hipStream_t stream) {
   } else if (a.T <= 16 * 256) {
     launch_tile<Act, NEB, 1, 16, kSlots>(a, 16, stream);
   } else {
-    launch_tile<Act, NEB, 2, 16, kSlots>(a, 32, stream);
+    // tokens spread over the CUs, which leaves each fewer to choose for (5000 tokens, 256 experts: 76.3 -> 73.9 us; up to
+    // 4096 it gains nothing: a wave has one token at most, 2000 tokens 55.5 -> 56.5 us)
+    launch_tile<Act, NEB, 2, 16, kSlots>(a, min(32, (a.T + 255) / 256), stream);
   }
 }
 

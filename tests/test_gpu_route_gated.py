@@ -98,6 +98,20 @@ def test_against_oracle(T, d, E, K, groups, group_topk, sigmoid, act):
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("E,groups", [(72, 4), (128, 1), (250, 10), (256, 8)])
+@pytest.mark.parametrize("T", [4096, 4097, 5000, 8193])
+def test_many_tokens_of_many_experts(T, E, groups, act):
+    """Two blocks of tokens a workgroup, full and partial, and one: against the oracle, and as in another batch."""
+    rng = np.random.default_rng(T + E)
+    x, wr = _draw(rng, T, 192, E, act)
+    select = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    kw = dict(sigmoid=True, groups=groups, group_topk=max(1, groups // 2), top2=True)
+    ids, _ = _check(x, wr, None, 6, select, "many", **kw)
+    part, _ = m.moe_route_gated(x[-700:].contiguous().cuda(), wr.cuda(), None, 6, _gate(select, **kw))
+    assert torch.equal(ids[-700:], part)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("E,groups", [(16, 1), (64, 8), (256, 8), (96, 3)])
 def test_values_closer_than_fp32_sums(E, groups, act):
     """Pairs of experts whose rows differ in one element, by its last bit, against an x that is tiny there: their
