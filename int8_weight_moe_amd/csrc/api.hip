@@ -116,12 +116,17 @@ constexpr long kMxFewTilesWideRowsPerExpert = 20;
 constexpr long kMxFewTilesChannels = 16384;
 
 // Rows an expert on average up to which a product of int8 rows streams its weights,
-// and the same where tiles are fewer than one a CU. Measured, us, stream / tiled: gate/up, d
+// and the same where tiles are fewer than one a CU: then also as long as the streaming
+// kernel's passes of 64 rows, which few tiles spread over workgroups, are no more than the CUs. Measured, us, stream / tiled: gate/up, d
 // 4096, f 14336, E 16: 8 rows 312 / 330, 16 334 / 350, 32 434 / 348; down, d 24576, f 8192: 8 595 / 626, 16
 // 597 / 609. Beyond 8 rows the tiles are within 5% and do not read the weights of a crowded expert again (999 slots, E 40,
 // unevenly: 93 / 60). One expert, 64 rows, d 24576, f 8192 (64 tiles): 69 / 150.
+// Passes, few tiles: one expert, d 8960, f 896: 450 rows (224 passes) 28 / 48, 1000 (448) 51 / 48; 5 experts, d 17984, f 384: 256
+// rows each (240) 50 / 127; 4 experts, SwiGLU, d 4096, f 1024: 128 rows each (256) 19 / 21, 200 (512) 34 / 21; 16 experts, d
+// 1024, f 512: 96 rows each (512) 11 / 10.
 constexpr long kI8StreamRowsPerExpert = 8;
 constexpr long kI8FewTilesRowsPerExpert = 64;
+constexpr long kI8FewTilesPasses = 256;
 
 // routes: the call's K experts of a token are distinct ones of the E.
 moe_status check_shape(const moe_shape* s, bool routes = true, int max_experts = 64) {
@@ -427,7 +432,9 @@ moe_status check_i8_shape(const moe_shape* s, bool routes) {
 moe_status run_i8(const char* call, const char* what, const moe_shape* s, const moe::I8Args& m, hipStream_t stream) {
   bool by_stream = s->ffn_path == MOE_PATH_STREAM;
   if (s->ffn_path == MOE_PATH_AUTO)
-    by_stream = m.S <= (moe::i8_few_tiles(m) ? kI8FewTilesRowsPerExpert : kI8StreamRowsPerExpert) * m.E;
+    by_stream = m.S <= kI8StreamRowsPerExpert * m.E ||
+                (moe::i8_few_tiles(m) &&
+                 (m.S <= kI8FewTilesRowsPerExpert * m.E || moe::i8_stream_passes(m) <= kI8FewTilesPasses));
   // rows past the tiled kernel's 32-bit offsets
   if (!moe::i8_tiled_offsets_fit(m.a_rows, m.Kd)) by_stream = true;
   if (log_on()) {

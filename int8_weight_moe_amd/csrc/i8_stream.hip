@@ -12,7 +12,9 @@
 // rows does not wait for the weights behind them).
 // Items are numbered over the experts that have rows. With few items the
 // reduction is cut into KS slices, streamed by the KS waves of a workgroup and
-// added through LDS (integers: exact in any order).
+// added through LDS (integers: exact in any order). Where a tiled product would have
+// fewer tiles than CUs the passes are spread over workgroups, whose weights come from the
+// caches then (one expert, 450 rows, d 8960, f 896: 28 us, tiles 48).
 // Bound by HBM: gate/up of one token (d 4096, f 14336, two experts) 39 us, 6.0
 // TB/s; down of 64 tokens (d 24576, f 8192, E 16) 490 us, 6.6 TB/s.
 #include "i8_common.h"
@@ -65,7 +67,7 @@ __global__ __launch_bounds__(block_waves(KS) * kWave) void i8_stream_kernel(I8Ar
           for (int m = 0; m < NMAT; ++m) wb[j][ng][m] = load_nt16(wp[ng][m] + (long)(s + j) * 1024);
   };
 
-  for (int p0 = 0; p0 < nrows; p0 += 16 * RB) {
+  for (int p0 = blockIdx.y * 16 * RB; p0 < nrows; p0 += gridDim.y * 16 * RB) {
     const int nrb = min(RB, (nrows - p0 + 15) >> 4);
     // the first weights are requested before the row numbers are looked up
     load_w(s_begin, w[0]);
@@ -170,8 +172,10 @@ long stream_items(const I8Args& a, int NG) { return (long)min(a.E, a.S) * (a.N /
 template <int NMAT, bool kOutBf16, int NG, int RB, int KS, int U>
 hipError_t launch(const I8Args& a, hipStream_t stream) {
   const long items = stream_items(a, NG);
+  // the rows of an expert are known on the device alone: workgroups past its last pass return
+  const int passes = i8_few_tiles(a) ? min(16, (a.S + 16 * RB - 1) / (16 * RB)) : 1;
   hipLaunchKernelGGL((i8_stream_kernel<NMAT, kOutBf16, NG, RB, KS, U>),
-                     dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves)),
+                     dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves), passes),
                      dim3(block_waves(KS) * kWave), 0, stream, a);
   return hipGetLastError();
 }
@@ -198,6 +202,11 @@ I8StreamPlan i8_stream_plan(const I8Args& a) {
   const long few = (long)min(a.E, a.S) * a.N / 32 < 2048;   // fewer 32-channel items than two waves a SIMD
   if (a.S <= (few ? 8L : 4L) * a.E) return {16, 16, 4};
   return a.S <= 8L * a.E ? I8StreamPlan{32, 32, 2} : I8StreamPlan{32, 64, 4};
+}
+
+long i8_stream_passes(const I8Args& a) {
+  const long experts = min(a.E, a.S), rows = (a.S + experts - 1) / experts;
+  return stream_items(a, 2) * ((rows + 63) / 64);
 }
 
 hipError_t launch_i8_stream(const I8Args& a, hipStream_t stream) {

@@ -117,7 +117,12 @@ INSTANCES = [(4, 16, 4160, MOE_PATH_AUTO, "16-channel items, 16-row passes, redu
              (9, 16, 4160, MOE_PATH_STREAM, "32-channel items, 64-row passes, reduction in 4 slices"),
              (9, 16, 4160, MOE_PATH_AUTO, "tiled schedule, 128x"),
              (64, 1, 1024, MOE_PATH_AUTO, "32-channel items, 64-row passes, reduction in 4 slices"),
-             (65, 1, 1024, MOE_PATH_AUTO, "tiled schedule, 128x128 tiles"),
+             (65, 1, 1024, MOE_PATH_AUTO, "32-channel items, 64-row passes, reduction in 4 slices"),
+             (512, 1, 1024, MOE_PATH_AUTO, "32-channel items, 64-row passes, reduction in 4 slices"),
+             (513, 1, 1024, MOE_PATH_AUTO, "tiled schedule, 128x128 tiles"),
+             (1700, 1, 64, MOE_PATH_AUTO, "32-channel items, 64-row passes, reduction in 4 slices"),
+             (128, 4, 1024, MOE_PATH_AUTO, "32-channel items, 64-row passes, reduction in 4 slices"),
+             (129, 4, 1024, MOE_PATH_AUTO, "tiled schedule, 128x128 tiles"),
              (64, 16, 8320, MOE_PATH_AUTO, "tiled schedule, 128x"), (65, 16, 8320, MOE_PATH_AUTO, "tiled schedule, 128x256 tiles"),
              (40, 4, 512, MOE_PATH_TILED, "tiled schedule, 128x128 tiles")]
 
