@@ -312,6 +312,10 @@ __device__ __forceinline__ Choice choose(const GateArgs& a, const TokenState& s,
   Real z = 1;
   if (!a.sigmoid) {
     m = wave_max(m);
+    // Exponentials are taken less of the largest logit. Rounded to fp32 it is off by one at most up to 2^24; by 64 from 2^30 on,
+    // which takes them all to 0 or the largest to infinity.
+    if constexpr (!kDouble)
+      if (!(fabsf(m) <= 0x1p24f)) return kInDouble;
     dmax = all ? wave_max(dmax) : 0.f;
     z = 0;
 #pragma unroll
