@@ -506,10 +506,10 @@ moe_status run_i8_ffn(const char* call, const moe_shape* s, const void* x, const
   moe_status st = run_i8(call, "gate/up", s, m, stream);
   if (st != MOE_OK) return st;
 
-  // rows past off[E] hold whatever was there: their codes are never read
+  // rows past off[E] hold whatever was there, and a shard of the experts has many of them
   q = reinterpret_cast<int8_t*>(ws + L.hq);
   qs = reinterpret_cast<float*>(ws + L.hs);
-  e = moe::launch_quantize_rows(S, s->f, true, h, false, q, qs, false, false, stream);
+  e = moe::launch_quantize_present(S, offsets + s->E, s->f, true, h, q, qs, stream);
   if (e != hipSuccess) return hip_fail(e, "quantize launch");
   m.a = q;
   m.a_s = qs;

@@ -82,6 +82,9 @@ hipError_t launch_pack_rows(long rows, int cols, const int8_t* src, int8_t* dst,
 // in the tiled layout (tiled = true: rows % 16 == 0, cols % 64 == 0)
 hipError_t launch_quantize_rows(int64_t rows, int cols, bool src_bf16, const void* w, bool scale_bf16, int8_t* q,
                                 void* s, bool fp8, bool tiled, hipStream_t stream);
+// int8 codes, row-major, and fp32 scales of the first *present (on the device) of `rows` rows; the others are neither read nor written
+hipError_t launch_quantize_present(int64_t rows, const int32_t* present, int cols, bool src_bf16, const void* w, int8_t* q,
+                                   float* s, hipStream_t stream);
 
 // MXFP4 (mx_common.h): quantizer, dequantizer and packer. tiled: rows % 16 ==
 // 0, cols % 128 == 0; row-major: cols % 32 == 0.

@@ -106,9 +106,11 @@ __device__ __forceinline__ long code_offset(long row, int c, int cols) {
 
 template <bool kSrcBf16, bool kScaleBf16, bool kFp8, bool kTiled>
 __global__ __launch_bounds__(kQuantThreads) void quantize_rows_kernel(const void* __restrict__ w, int cols,
-                                                                      int8_t* __restrict__ q, void* __restrict__ s) {
+                                                                      int8_t* __restrict__ q, void* __restrict__ s,
+                                                                      const int32_t* __restrict__ present) {
   __shared__ float wmax[kQuantThreads / kWave];
   const long row = blockIdx.x;
+  if (present && row >= *present) return;   // the whole workgroup
   const long base = row * cols;
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
@@ -237,7 +239,7 @@ __global__ __launch_bounds__(kQuantThreads) void quantize_pack_kernel(const void
 
 template <bool kFp8, bool kTiled>
 hipError_t launch_quantize(int64_t rows, int cols, bool src_bf16, const void* w, bool scale_bf16, int8_t* q, void* s,
-                           hipStream_t stream) {
+                           hipStream_t stream, const int32_t* present = nullptr) {
   if (rows == 0) return hipSuccess;
   const dim3 block(kQuantThreads);
   if constexpr (kTiled) {
@@ -259,14 +261,14 @@ hipError_t launch_quantize(int64_t rows, int cols, bool src_bf16, const void* w,
   const dim3 grid((unsigned)rows);
   if (src_bf16) {
     if (scale_bf16)
-      hipLaunchKernelGGL((quantize_rows_kernel<true, true, kFp8, false>), grid, block, 0, stream, w, cols, q, s);
+      hipLaunchKernelGGL((quantize_rows_kernel<true, true, kFp8, false>), grid, block, 0, stream, w, cols, q, s, present);
     else
-      hipLaunchKernelGGL((quantize_rows_kernel<true, false, kFp8, false>), grid, block, 0, stream, w, cols, q, s);
+      hipLaunchKernelGGL((quantize_rows_kernel<true, false, kFp8, false>), grid, block, 0, stream, w, cols, q, s, present);
   } else {
     if (scale_bf16)
-      hipLaunchKernelGGL((quantize_rows_kernel<false, true, kFp8, false>), grid, block, 0, stream, w, cols, q, s);
+      hipLaunchKernelGGL((quantize_rows_kernel<false, true, kFp8, false>), grid, block, 0, stream, w, cols, q, s, present);
     else
-      hipLaunchKernelGGL((quantize_rows_kernel<false, false, kFp8, false>), grid, block, 0, stream, w, cols, q, s);
+      hipLaunchKernelGGL((quantize_rows_kernel<false, false, kFp8, false>), grid, block, 0, stream, w, cols, q, s, present);
   }
   return hipGetLastError();
 }
@@ -281,6 +283,11 @@ hipError_t launch_quantize_rows(int64_t rows, int cols, bool src_bf16, const voi
   }
   return fp8 ? launch_quantize<true, false>(rows, cols, src_bf16, w, scale_bf16, q, s, stream)
              : launch_quantize<false, false>(rows, cols, src_bf16, w, scale_bf16, q, s, stream);
+}
+
+hipError_t launch_quantize_present(int64_t rows, const int32_t* present, int cols, bool src_bf16, const void* w, int8_t* q,
+                                   float* s, hipStream_t stream) {
+  return launch_quantize<false, false>(rows, cols, src_bf16, w, false, q, s, stream, present);
 }
 
 }  // namespace moe
