@@ -489,8 +489,8 @@ moe_status moe_route_gated(const moe_shape* shape, const moe_gate* gate, const v
  *     (w2_*: both NULL for the plain product).
  *   out [T*K, f] act_dtype, not overlapping any input (MOE_ERR_UNSUPPORTED); rows past off[E] are left untouched.
  * The sums are exact in int32; a sum becomes fp32 and takes its two scales there.
- * Any segment lengths. The schedules give the same bits; rows of a_q of 4 GiB and
- * more take STREAM, whatever ffn_path asks for. */
+ * Any segment lengths. The schedules give the same bits; with
+ * sorted_slots rows of a_q of 4 GiB and more take STREAM, whatever ffn_path asks for. */
 moe_status moe_grouped_mm_int8(const moe_shape* shape, const int8_t* a_q, const float* a_s,
                                const int32_t* expert_offsets, const int32_t* sorted_slots, const int8_t* w_q,
                                const void* w_s, const int8_t* w2_q, const void* w2_s, void* out, hipStream_t stream);

@@ -435,8 +435,8 @@ moe_status run_i8(const char* call, const char* what, const moe_shape* s, const 
     by_stream = m.S <= kI8StreamRowsPerExpert * m.E ||
                 (moe::i8_few_tiles(m) &&
                  (m.S <= kI8FewTilesRowsPerExpert * m.E || moe::i8_stream_passes(m) <= kI8FewTilesPasses));
-  // rows past the tiled kernel's 32-bit offsets
-  if (!moe::i8_tiled_offsets_fit(m.a_rows, m.Kd)) by_stream = true;
+  // gathered rows past the tiled kernel's 32-bit offsets
+  if (!moe::i8_tiled_offsets_fit(m)) by_stream = true;
   if (log_on()) {
     char how[128];
     if (!by_stream) {

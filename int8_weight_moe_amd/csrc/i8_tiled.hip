@@ -63,13 +63,16 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(k
   const int n0 = nt * CH_TILE;
 
   // ---- row sources: load j of this wave covers rows RPI*(wave + kWaves*j) + lane/CPR (so the first loads of all the
-  // waves cover the first rows); byte offset of this lane's chunk at step 0
+  // waves cover the first rows); byte offset of this lane's chunk at step 0, 32 bits from the tile's first row (128 rows of
+  // 131072 at most), or for gathered rows from row 0 (i8_tiled_offsets_fit). Streamed instead, rows past 4 GiB take 6 to 40
+  // times as long (90000 rows of 49152, E 8, f 4096: 91.2 / 14.7 ms).
+  const int8_t* rows = a.sorted_slots ? a.a : a.a + (long)row0 * a.Kd;
   uint32_t a_off[A_INSTR];
 #pragma unroll
   for (int j = 0; j < A_INSTR; ++j) {
     const int r = RPI * (wave + kWaves * j) + lane / CPR;
-    const int rr = row0 + (r < nrows ? r : 0);
-    const uint32_t src = (uint32_t)(a.sorted_slots ? a.sorted_slots[rr] / a.topk : rr);
+    const int rr = r < nrows ? r : 0;
+    const uint32_t src = (uint32_t)(a.sorted_slots ? a.sorted_slots[row0 + rr] / a.topk : rr);
     a_off[j] = src * (uint32_t)a.Kd + (uint32_t)(((lane % CPR) ^ (r % CPR)) * 16);
   }
   // The second block of the last step of an odd number of blocks re-reads the first one: 64 bytes back for the lanes
@@ -94,7 +97,7 @@ __global__ __launch_bounds__(kWaves* kWave) __attribute__((amdgpu_waves_per_eu(k
     const uint32_t off = step_off(min(step, nsteps - 1));
 #pragma unroll
     for (int j = 0; j < LOADS; ++j)
-      dma16(a.a, a_off[j] + off, lds_addr(&As[buf][0]) + (wave + kWaves * j) * 1024);
+      dma16(rows, a_off[j] + off, lds_addr(&As[buf][0]) + (wave + kWaves * j) * 1024);
   };
   auto load_b = [&](int step, uint4 (&b)[NB][KB]) {
 #pragma unroll
@@ -212,7 +215,7 @@ hipError_t launch_columns(const I8Args& a, hipStream_t stream) {
 
 }  // namespace
 
-bool i8_tiled_offsets_fit(long rows, int cols) { return (uint64_t)rows * (uint64_t)cols < (1ull << 32); }
+bool i8_tiled_offsets_fit(const I8Args& a) { return !a.sorted_slots || (uint64_t)a.a_rows * (uint64_t)a.Kd < (1ull << 32); }
 
 bool i8_few_tiles(const I8Args& a) {
   return (long)max(min(a.E, a.S), (a.S + 127) / 128) * tile_columns(a, 128) < 256;

@@ -153,8 +153,8 @@ I8StreamPlan i8_stream_plan(const I8Args& a);
 // Passes of 64 rows by 32 channels over experts of as many rows each.
 long i8_stream_passes(const I8Args& a);
 hipError_t launch_i8_stream(const I8Args& a, hipStream_t stream);
-// Whether rows of `cols` codes lie within 32-bit byte offsets, as launch_i8_tiled needs the rows of a to.
-bool i8_tiled_offsets_fit(long rows, int cols);
+// Whether the rows of a lie within 32-bit byte offsets, as launch_i8_tiled needs gathered ones to.
+bool i8_tiled_offsets_fit(const I8Args& a);
 // Channels of a tile (both matrices'), and whether tiles are fewer than one a CU.
 int i8_tile_columns(const I8Args& a);
 bool i8_few_tiles(const I8Args& a);
