@@ -3,16 +3,16 @@
 //
 //   out[r, n] = a_s[row(r)] * w_s[n] * sum_k a_q[row(r), k] * w_q[n, k],   or   silu(p0) * p1
 //
-// for the rows r of every expert's segment. A wave owns one (expert, 16*NG output
+// for the rows r of every expert's segment. A workgroup owns one (expert, 16*NG output
 // channels) item and takes 16*RB rows a pass, with the channels as MFMA rows and
 // the tokens as MFMA columns. Per 64-wide step it reads one 1 KiB block per 16
 // channels and matrix (16 bytes a lane) and 16 bytes a lane of the rows, U steps
 // at a time: the rows of these steps are requested, then the weights of the next
 // ones, then the steps are computed (loads return in order, so waiting for the
 // rows does not wait for the weights behind them).
-// Items are numbered over the experts that have rows. With few items the
-// reduction is cut into KS slices, streamed by the KS waves of a workgroup and
-// added through LDS (integers: exact in any order). Where a tiled product would have
+// Items are numbered over the experts that have rows. The reduction is cut
+// into KS slices, streamed by the KS waves of the workgroup and added through
+// LDS (integers: exact in any order). Where a tiled product would have
 // fewer tiles than CUs the passes are spread over workgroups, whose weights come from the
 // caches then (one expert, 450 rows, d 8960, f 896: 28 us, tiles 48).
 // Bound by HBM: gate/up of one token (d 4096, f 14336, two experts) 39 us, 6.0
@@ -24,26 +24,21 @@ namespace moe {
 
 namespace {
 
-constexpr int kStreamWaves = 4;
-constexpr int block_waves(int KS) { return KS > 1 ? KS : kStreamWaves; }
-
 template <int NMAT, bool kOutBf16, int NG, int RB, int KS, int U>
-__global__ __launch_bounds__(block_waves(KS) * kWave) void i8_stream_kernel(I8Args a) {
-  constexpr int IPW = block_waves(KS) / KS;   // items per workgroup
-  __shared__ i32x4 red[KS > 1 ? KS - 1 : 1][NG][NMAT][kWave];
+__global__ __launch_bounds__(KS * kWave) void i8_stream_kernel(I8Args a) {
+  static_assert(KS > 1, "the slices are added through LDS");
+  __shared__ i32x4 red[KS - 1][NG][NMAT][kWave];
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
+  const int kslice = threadIdx.x >> 6;
   const int li = lane & 15;
   const int lg = lane >> 4;
   const int N = a.N, n = a.Kd / kI8Step;      // steps of a row
 
   const int gpe = N / (16 * NG);
-  const int item = blockIdx.x * IPW + wave / KS;
-  const int kslice = wave % KS;
-  const int te = item / gpe;
-  const int grp = item - te * gpe;
+  const int te = blockIdx.x / gpe;
+  const int grp = blockIdx.x - te * gpe;
   int e, row0, nrows;
-  // KS > 1: the workgroup is one item, so all its waves return here together
+  // the workgroup is one item, so all its waves return here together
   if (!find_touched_expert(a.offsets, a.E, te, e, row0, nrows)) return;
   const int ch_base = grp * 16 * NG;
 
@@ -125,29 +120,27 @@ __global__ __launch_bounds__(block_waves(KS) * kWave) void i8_stream_kernel(I8Ar
       run(int_constant<RB>{});
     }
 
-    if constexpr (KS > 1) {
 #pragma unroll
-      for (int rb = 0; rb < RB; ++rb) {
-        if (rb < nrb) {
-          if (kslice > 0) {
+    for (int rb = 0; rb < RB; ++rb) {
+      if (rb < nrb) {
+        if (kslice > 0) {
+#pragma unroll
+          for (int ng = 0; ng < NG; ++ng)
+#pragma unroll
+            for (int m = 0; m < NMAT; ++m) red[kslice - 1][ng][m][lane] = acc[rb][ng][m];
+        }
+        __syncthreads();
+        if (kslice == 0) {
+          for (int j = 0; j < KS - 1; ++j)
 #pragma unroll
             for (int ng = 0; ng < NG; ++ng)
 #pragma unroll
-              for (int m = 0; m < NMAT; ++m) red[kslice - 1][ng][m][lane] = acc[rb][ng][m];
-          }
-          __syncthreads();
-          if (kslice == 0) {
-            for (int j = 0; j < KS - 1; ++j)
-#pragma unroll
-              for (int ng = 0; ng < NG; ++ng)
-#pragma unroll
-                for (int m = 0; m < NMAT; ++m) acc[rb][ng][m] += red[j][ng][m][lane];
-          }
-          __syncthreads();
+              for (int m = 0; m < NMAT; ++m) acc[rb][ng][m] += red[j][ng][m][lane];
         }
+        __syncthreads();
       }
-      if (kslice > 0) continue;
     }
+    if (kslice > 0) continue;
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
       const int r = p0 + rb * 16 + li;
@@ -178,8 +171,7 @@ hipError_t launch(const I8Args& a, hipStream_t stream) {
   const int most = (a.S + 16 * RB - 1) / (16 * RB);
   const int passes = i8_few_tiles(a) ? min(16, most) : items < 256 ? min((int)(256 / items), most) : 1;
   hipLaunchKernelGGL((i8_stream_kernel<NMAT, kOutBf16, NG, RB, KS, U>),
-                     dim3((unsigned)(KS > 1 ? items : (items + kStreamWaves - 1) / kStreamWaves), passes),
-                     dim3(block_waves(KS) * kWave), 0, stream, a);
+                     dim3((unsigned)items, passes), dim3(KS * kWave), 0, stream, a);
   return hipGetLastError();
 }
 

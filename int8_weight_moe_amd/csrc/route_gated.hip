@@ -939,23 +939,18 @@ void launch_experts(const GateArgs& a, hipStream_t stream) {
   }
 }
 
-// Slots of a lane: a group's experts over its lanes, of which there are more than 32 / groups; 8 at most, 4 if the groups
-// are a power of two, as they mostly are.
-template <typename Act, int NEB>
-void launch_slots(const GateArgs& a, hipStream_t stream) {
-  int lanes = kWave;
-  while (lanes * a.groups > kWave) lanes >>= 1;
-  if (a.E / a.groups <= 4 * lanes) launch_experts<Act, NEB, 4>(a, stream);
-  else launch_experts<Act, NEB, 8>(a, stream);
-}
-
+// Slots of a lane: a group's experts over its lanes, of which there are more than 32 / groups, so at most E / 32: 4 for 128
+// experts; for 256 experts 8, or 4 if the groups are a power of two, as they mostly are.
 template <typename Act>
 void launch(const GateArgs& a, hipStream_t stream) {
+  int lanes = kWave;
+  while (lanes * a.groups > kWave) lanes >>= 1;
   if (a.E <= 16) launch_experts<Act, 1, 1>(a, stream);
   else if (a.E <= 32) launch_experts<Act, 2, 1>(a, stream);
   else if (a.E <= 64) launch_experts<Act, 4, 2>(a, stream);
-  else if (a.E <= 128) launch_slots<Act, 8>(a, stream);
-  else launch_slots<Act, 16>(a, stream);
+  else if (a.E <= 128) launch_experts<Act, 8, 4>(a, stream);
+  else if (a.E / a.groups <= 4 * lanes) launch_experts<Act, 16, 4>(a, stream);
+  else launch_experts<Act, 16, 8>(a, stream);
 }
 
 }  // namespace
