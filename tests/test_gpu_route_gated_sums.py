@@ -1,9 +1,10 @@
 """What the gated router's ids rest on: the error that its fp32 sums are taken to have, and rows whose squares fp32 loses.
 
-A block of a row is 64 bf16 or 32 fp32 columns. Its sum may be off by 6 (bf16) or 8 (fp32) units of 2^-23 of the sum of its
-terms' magnitudes: how the matrix instructions round inside is measured, here too, not documented.
+A block of a row is 64 bf16 or 32 fp32 columns. Its sum may be off by 8 units of 2^-23 of the sum of its terms' magnitudes. How the
+matrix instructions round inside is measured, not documented. bf16: eight products (columns 8 i .. 8 i + 7 of the block) are cut off
+at 2^-24 of the power of two below the largest and added, and each of the eight such sums of a block is rounded to nearest as it is
+added to the others: at most 7 products' 2^-24 of the largest, and 8 roundings of 2^-24, 7.5 units. fp32: 16 roundings of 2^-24.
 """
-import math
 import sys
 
 import numpy as np
@@ -16,7 +17,7 @@ from tests.test_gpu_route_gated import DT, _gate
 
 pytestmark = pytest.mark.gpu
 
-UNITS = {"bf16": 6.0, "f32": 8.0}
+UNITS = 8.0
 BLOCK = {"bf16": 64, "f32": 32}
 
 
@@ -47,32 +48,82 @@ def _patterns(rng, act, T, n):
     return torch.from_numpy(v.astype(np.float32)).to(DT[act])
 
 
+def _worst(act, sign, just_below):
+    """Each place of a large term in a block: with bf16 the other seven of its eight are just below what is cut off, and one term of
+    each other eight is just below what rounds up; with fp32 every term is (those before the large one are not lost)."""
+    n = BLOCK[act]
+    small = sign * just_below * 2.0 ** -24
+    v = np.full((n, n), small if act == "f32" else 0.0)
+    for p in range(n):
+        if act == "bf16":
+            v[p, ::8] = small
+            v[p, p // 8 * 8:p // 8 * 8 + 8] = small
+        v[p, p] = 1
+    return v
+
+
+def _off(x, act):
+    """How far the kernel's sums of the rows of x (one block each) are off, and their magnitudes' 2^-23.
+
+    One expert is never looked at again, so its sigmoid is that of the kernel's own sum. The true sum is taken off by terms that
+    have a block each, which is exact, but for a rest that is known; what is left is the error, l: the weight is
+    1 / (1 + exp(-l)), rounded to fp32, so l is known to 4 * 2^-25 (and some 1e-15) where it is below 0.1."""
+    T, n = x.shape
+    terms = np64(x)
+    rest, parts = terms.sum(1), []                       # to 2^-53 of the magnitudes, at most 2^9, an addition
+    for _ in range(5 if act == "bf16" else 3):
+        parts.append(torch.from_numpy(rest).to(DT[act]))
+        rest = rest - np64(parts[-1])
+    d = -(-(1 + len(parts)) * n // 64) * 64
+    rows, w = torch.zeros(T, d, dtype=DT[act]), torch.zeros(1, d, dtype=DT[act])
+    rows[:, :n], w[0, :n] = x, 1
+    for i, p in enumerate(parts):
+        rows[:, (i + 1) * n], w[0, (i + 1) * n] = p, -1
+    _, wt = m.moe_route_gated(rows.cuda(), w.cuda(), None, 1, _gate(sigmoid=True, renorm=False))
+    l = -np.log(1 / np64(wt)[:, 0] - 1)
+    assert (np.abs(l) < 0.1).all()
+    return np.abs(l - rest), 2.0 ** -23 * np.abs(terms).sum(1)
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
-@pytest.mark.parametrize("seed", range(4))
-def test_sums_of_a_block_are_off_by_no_more_than_taken(act, seed):
-    """One expert is never looked at again, so its sigmoid is that of the kernel's own sum. With the sum's rounded value taken off
-    as the router's bias what is left is the error, l: the weight is 0.5 + l / 4 to 2^-25 and |l|^3 / 48."""
-    rng = np.random.default_rng(seed)
-    T, n = 768, BLOCK[act]
-    x = _patterns(rng, act, T, n)
-    w = _patterns(rng, act, 6, n)[seed] if seed else torch.ones(n, dtype=DT[act])
-    x = torch.cat([x, torch.zeros(T, 64 - n, dtype=DT[act])], 1)
-    w = torch.cat([w, torch.zeros(64 - n, dtype=DT[act])])
-    terms = np64(x) * np64(w)                            # exact in fp64
-    mag = np.abs(terms).sum(1)
-    k = 2.0 ** np.floor(np.log2(2.0 ** 9 / mag))         # magnitudes between 2^8 and 2^9, one token a call: its bias is its own
-    worst = 0.0
-    for t in range(0, T, 8):
-        xt = (x[t:t + 1].float() * float(k[t])).to(DT[act])
-        s = math.fsum((np64(xt) * np64(w))[0])
-        bias = np.float32(-s)
-        _, wt = m.moe_route_gated(xt.cuda(), w[None].cuda(), torch.tensor([bias]).cuda(), 1, _gate(sigmoid=True, renorm=False))
-        l = (float(wt[0, 0]) - 0.5) * 4
-        off = abs(l - (s + float(bias)))
-        unit = 2.0 ** -23 * mag[t] * k[t]
-        assert off <= UNITS[act] * unit + 4 * 2.0 ** -25 + abs(l) ** 3 / 12, f"{off / unit:.2f} units (pattern {t % 6})"
-        worst = max(worst, off / unit)
-    _say(f"{act} seed {seed}: off by {worst:.2f} units at most")
+def test_sums_of_a_block_are_off_by_no_more_than_taken(act):
+    rng = np.random.default_rng(1)
+    rows = [_patterns(rng, act, 12000, BLOCK[act]).float()]
+    for sign in (1, -1):
+        for just_below in (0.996, 0.992, 0.5, 1.0, 1.008, 1.99):
+            rows.append(torch.from_numpy(_worst(act, sign, just_below).astype(np.float32)))
+    x = torch.cat(rows)
+    mag = x.abs().sum(1, dtype=torch.float64)
+    x = (x * (2.0 ** torch.floor(8 - mag.log2()))[:, None].float()).to(DT[act])   # magnitudes between 2^7 and 2^9
+    off, unit = _off(x, act)
+    assert (off <= UNITS * unit + 4 * 2.0 ** -25 + 1e-11).all(), f"{(off / unit).max():.2f} units"
+    _say(f"{act}: off by {(off / unit).max():.2f} units at most")
+
+
+@pytest.mark.parametrize("power", [8, 12, 16, 18, 19, 20])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_a_bias_between_a_sum_and_its_error(power, sign):
+    """A bf16 sum of 2^power, off by 6.9 units of it, next to a router's bias that leaves a logit of -6, against another expert's bias
+    halfway, in the score, between the sum's logit and the true one, and at other places: the id is the true one's."""
+    a = 255 / 256                                        # x and w both hold it: |x| |w| is the sum of the magnitudes
+    for p in range(0, 64, 9):                            # the large term in each eight
+        v = np.abs(_worst("bf16", 1, 1.0)[p])
+        x, wr = np.zeros((1, 64), np.float32), np.zeros((2, 64), np.float32)
+        x[0] = np.where(v == 1, 1, np.sqrt(v) * a) * 2.0 ** (power - power // 2)
+        wr[0] = np.where(v == 1, 1, sign * np.sqrt(v) * a) * 2.0 ** (power // 2)
+        bias = np.array([-(2.0 ** power + 6), 0], np.float32)
+        true = float((x[0].astype(np.float64) * wr[0]).sum() + bias[0])
+        error = true + 6                                 # the kernel's sum is 2^power
+        assert 6.8 < abs(error) / 2.0 ** (power - 23) < 7
+        xt, wt = torch.from_numpy(x).to(torch.bfloat16), torch.from_numpy(wr).to(torch.bfloat16)
+        assert np.array_equal(np64(xt), x) and np.array_equal(np64(wt), wr)
+        score = lambda l: 1 / (1 + np.exp(-l))
+        for part in (-0.5, 0.02, 0.1, 0.3, 0.5, 0.7, 0.9, 0.98, 1.02, 1.5):
+            select = np.array([0, score(-6 + part * error) - 0.5], np.float32)
+            want = int(score(true) <= 0.5 + float(select[1]))
+            ids, _ = m.moe_route_gated(xt.cuda(), wt.cuda(), torch.from_numpy(bias).cuda(), 1, _gate(select, sigmoid=True))
+            if abs(score(true) - 0.5 - float(select[1])) > 1e-15:
+                assert int(ids[0, 0]) == want, f"large term {p}, at {part} of an error of {error:.3g}"
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
