@@ -462,8 +462,9 @@ typedef struct moe_gate {
   float scale;              /* finite                                              */
 } moe_gate;
 
-/* As moe_route; here shape->E may be up to 256 (a GPU that holds some of them
- * permutes ids less its first expert's: ids outside [0, its experts) are not placed).
+/* As moe_route; here shape->E may be up to 256 (a GPU that holds some of them, K at
+ * least, permutes ids less its first expert's: ids outside [0, its experts) are not
+ * placed; MOE_DEBUG's check of moe_permute reports such ids, -1 among them).
  *   workspace: NULL, or 16-byte aligned and at least moe_route_gated_workspace_size
  *     bytes (0 for shapes that have no use for it). With it the rows of few tokens
  *     are split over workgroups (half as long for 63 tokens and 64 experts). */
@@ -497,7 +498,8 @@ moe_status moe_grouped_mm_int8(const moe_shape* shape, const int8_t* a_q, const 
 
 /* The expert FFN with int8 weights AND activations, on the permuted rows: x is
  * quantized per token, gate/up with SwiGLU gives h (bf16), h is quantized per row
- * (moe_quantize_rows, fp32 scales), down gives y_rows. As moe_expert_ffn with int8
+ * (moe_quantize_rows, fp32 scales), down gives y_rows. Rows past off[E] are neither
+ * read nor written, in the workspace too. As moe_expert_ffn with int8
  * products (0.6 times as long at prefill) and the rounding of int8 activations. A
  * token with an infinity or a NaN, in x or h, gives unspecified numbers.
  *   weight_fmt MOE_W_INT8; act_dtype is x's type;
