@@ -18,7 +18,7 @@
 // Rows past the segment read row 0 of the tile and channels past N read channel
 // 0; their results are not stored.
 // Bound by the clock and the wait of each step: 8192 tokens of two experts of 16 (d 4096, f 14336, gate/up) 1804 to 1908 us
-// by the box, 2.02 to 2.13 POP/s, the MFMAs busy 54% of the cycles at 1.9 GHz; 16384 tokens skewed (d 24576, f 8192, down) 5700
+// by the card, 2.02 to 2.13 POP/s, the MFMAs busy 54% of the cycles at 1.9 GHz; 16384 tokens skewed (d 24576, f 8192, down) 5700
 // to 6003 us, 2.20 to 2.31 POP/s, 64% at 1.7 GHz; no bank conflicts. A library product of these sizes reaches 2.1 and 2.45. Slower: two steps a barrier (1%),
 // non-temporal weights (20 to 50%), 64 rows (17 to 33%), and one wave a SIMD on 256 rows x 256 channels (11 to 21%:
 // nothing runs while it waits).
